@@ -467,3 +467,20 @@ def fp8_block_gemm_backward_w_noalloc(qdy, sdy, qw, sw, qdyT, sdyT, qxT, sxT, dx
         qxT.data_ptr(), sxT.data_ptr(), dx.data_ptr(), _odt(dx.dtype), dw.data_ptr(),
         _odt(dw.dtype, accumulate_dw, dw), scale_mode, _stream(stream)))
     return dx, dw
+
+
+# ------------------------------------------- any number of tokens, experts --
+# moe.py binds include/fp8moe.h.  It is loaded on first use: it imports torch,
+# which importing this package does not.
+
+_MOE = ("fp8_linear", "fp8_linear_workspace_size", "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_experts",
+        "fp8_moe_layer", "fp8_moe_workspace_size", "FP8MOE_BF16", "FP8MOE_FP32", "FP8MOE_MAX_EXPERTS",
+        "FP8MOE_MAX_TOPK", "FP8MOE_MAX_TOKENS")
+
+
+def __getattr__(name):
+    if name not in _MOE:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import moe
+    globals().update({n: getattr(moe, n) for n in _MOE})
+    return globals()[name]

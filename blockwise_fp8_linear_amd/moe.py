@@ -1,0 +1,288 @@
+"""Binding of include/fp8moe.h: the FP8 linear layer at any number of tokens,
+the router of a mixture of experts with its gradient, and a whole
+mixture-of-experts layer for a few tokens.
+
+The manner is the package's: the C entry points' names, torch tensors on the
+current device, checks of dtype, layout and shape before any C call,
+RuntimeError on a non-zero status.  These calls stand in decoding loops, where
+their own cost is what a caller waits for, so the checks of an operand are one
+function and the stream is taken as a raw handle.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import torch
+
+import blockwise_fp8_linear_amd as _fb
+
+HEADER_PATH = os.path.join(os.path.dirname(_fb.HEADER_PATH), "fp8moe.h")
+
+# enum values and limits of include/fp8moe.h
+FP8MOE_BF16 = 0
+FP8MOE_FP32 = 1
+FP8MOE_MAX_EXPERTS = 1024
+FP8MOE_MAX_TOPK = 16
+FP8MOE_MAX_TOKENS = 512
+
+_FUNCTIONS = None
+
+
+def _functions():
+    """The entry points with their signatures set (once per loaded library)."""
+    global _FUNCTIONS
+    lib = _fb.load_library()
+    if _FUNCTIONS is not None and _FUNCTIONS[0] is lib:
+        return _FUNCTIONS[1]
+    vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    sig = {
+        "fp8_linear": [i64, i64, i64, vp, i64, vp, vp, vp, i32, i32, vp, sz, vp],
+        "fp8_moe_route": [i64, i64, i32, vp, i32, i64, i32, vp, vp, vp],
+        "fp8_moe_route_backward": [i64, i64, i32, vp, i32, i64, vp, vp, i32, vp, i64, vp],
+        "fp8_moe_experts": [i64, i64, i64, i64, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, sz, vp],
+        "fp8_moe_layer": [i64, i64, i64, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz,
+                          vp],
+    }
+    for name, args in sig.items():
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, i32
+    lib.fp8_linear_workspace_size.argtypes = [i64, i64, i64]
+    lib.fp8_linear_workspace_size.restype = sz
+    lib.fp8_moe_workspace_size.argtypes = [i64, i64, i64, i64, i32]
+    lib.fp8_moe_workspace_size.restype = sz
+    _FUNCTIONS = (lib, lib)
+    return lib
+
+
+def _device(x, name):
+    """The device a call runs on: its first operand's, which has to be the
+    current one (the library launches there)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    d = x.device
+    if d.type != "cuda":
+        raise ValueError(f"{name}: must be a device tensor")
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {d}, but the library launches on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    return d
+
+
+def _stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _new(shape, dtype, device, stream):
+    """torch.empty whose memory belongs to the stream the call launches on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _fb._new(shape, dtype, device, stream)
+
+
+def _operand(t, dtype, shape, name, device, strided=False):
+    """Check one tensor: a device tensor of this dtype and shape, dense (or,
+    `strided`, with a contiguous last dimension).  Returns its address."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, but the call runs on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if strided:
+        if t.stride(-1) != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(x, dtypes, name):
+    """The first operand: a matrix of one of these types, rows any distance
+    apart.  Returns its device, sizes and row stride (a single row has none
+    that matters)."""
+    device = _device(x, name)
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dims, got {x.dim()}")
+    rows, cols = x.shape
+    if x.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return device, rows, cols, x.stride(0) if rows > 1 else cols
+
+
+def _result(out, shape, dtype, name, device, stream):
+    if out is None:
+        return _new(shape, dtype, device, stream)
+    _operand(out, dtype, shape, name, device)
+    return out
+
+
+def _scratch(need, workspace, device, stream):
+    """(the workspace, to be kept until the call has been made, its address and size)."""
+    if need == 0:
+        return None, None, 0
+    if workspace is None:
+        # belongs to `stream`: freed when the call returns, its memory is
+        # reused only by work queued behind the kernels that use it
+        workspace = _new((need,), torch.uint8, device, stream)
+    else:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace: expected a torch.Tensor")
+        if workspace.device != device:
+            raise ValueError(f"workspace: on {workspace.device}, but the call runs on {device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _invalid(need):
+    """Whether a workspace query refused the shape (the call then says why)."""
+    return need == ctypes.c_size_t(-1).value
+
+
+# ------------------------------------------------------------------- linear --
+
+def fp8_linear_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_functions().fp8_linear_workspace_size(M, N, K))
+
+
+def fp8_linear(x, qw, sw, out_dtype=None, out=None, workspace=None, stream=None, accumulate=False,
+               scale_mode=_fb.FP8BLK_SCALE_POW2):
+    """Y = X W^T for any number of tokens.  x bf16 [M,K] (row stride may exceed
+    K), qw [N,K] and sw [N/128,K/128] from fp8_quantize_block -> Y [M,N] bf16
+    or fp32.  x is quantized on the way by scale_mode's rule, the one that made
+    sw.  accumulate: out += result in fp32 (out_dtype float32, `out` given)."""
+    bf16 = torch.bfloat16
+    device, M, K, ld = _matrix(x, (bf16,), "x")
+    if not isinstance(qw, torch.Tensor) or qw.dim() != 2:
+        raise ValueError("qw: expected a 2-dim tensor")
+    N = qw.shape[0]
+    pqw = _operand(qw, torch.uint8, (N, K), "qw", device)
+    psw = _operand(sw, torch.float32, (N // 128, K // 128), "sw", device)
+    odt = _fb.FP8BLK_OUT_BF16
+    if out_dtype is None:
+        out_dtype = bf16
+    if accumulate or out_dtype is not bf16:
+        odt = _fb._odt(out_dtype, accumulate, out)
+    lib = _functions()
+    need = lib.fp8_linear_workspace_size(M, N, K)
+    keep, ws, size = (None, None, 0) if _invalid(need) else _scratch(need, workspace, device, stream)
+    y = _result(out, (M, N), out_dtype, "out", device, stream)
+    _fb._check(lib.fp8_linear(M, N, K, x.data_ptr(), ld, pqw, psw, y.data_ptr(), odt, scale_mode, ws, size,
+                              _stream(stream, device)))
+    return y
+
+
+# ------------------------------------------------------------------- router --
+
+_LOGITS = (torch.bfloat16, torch.float32)
+
+
+def fp8_moe_route(logits, topk, renormalize=True, ids=None, weights=None, stream=None):
+    """The router's choice.  logits bf16 or fp32 [T,E] (row stride may exceed
+    E) -> (ids int32 [T,topk], weights fp32 [T,topk]): each token's experts with
+    the largest logits, largest first, equal ones by lower index, and their
+    softmax weights -- over the chosen ones (renormalize) or over all.  Experts
+    whose logit is -inf or NaN are masked out; where fewer than topk are left
+    the rest of the row is id -1, weight 0."""
+    device, T, E, ld = _matrix(logits, _LOGITS, "logits")
+    ids = _result(ids, (T, topk), torch.int32, "ids", device, stream)
+    weights = _result(weights, (T, topk), torch.float32, "weights", device, stream)
+    _fb._check(_functions().fp8_moe_route(T, E, topk, logits.data_ptr(),
+                                          FP8MOE_FP32 if logits.dtype is torch.float32 else FP8MOE_BF16, ld,
+                                          int(bool(renormalize)), ids.data_ptr(), weights.data_ptr(),
+                                          _stream(stream, device)))
+    return ids, weights
+
+
+def fp8_moe_route_backward(logits, ids, dweights, renormalize=True, dlogits=None, stream=None):
+    """Gradient of fp8_moe_route's weights: logits and ids as it took and gave
+    them, dweights fp32 [T,topk] -> dlogits [T,E] in the logits' type (or into
+    `dlogits`, whose row stride may exceed E)."""
+    device, T, E, ld = _matrix(logits, _LOGITS, "logits")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids: expected a 2-dim tensor")
+    k = ids.shape[1]
+    pids = _operand(ids, torch.int32, (T, k), "ids", device)
+    pg = _operand(dweights, torch.float32, (T, k), "dweights", device)
+    if dlogits is None:
+        dlogits = _new((T, E), logits.dtype, device, stream)
+    else:
+        _operand(dlogits, logits.dtype, (T, E), "dlogits", device, strided=True)
+    _fb._check(_functions().fp8_moe_route_backward(T, E, k, logits.data_ptr(),
+                                                   FP8MOE_FP32 if logits.dtype is torch.float32 else FP8MOE_BF16, ld,
+                                                   pids, pg, int(bool(renormalize)), dlogits.data_ptr(),
+                                                   dlogits.stride(0) if T > 1 else E, _stream(stream, device)))
+    return dlogits
+
+
+# ------------------------------------------------------------------ experts --
+
+def fp8_moe_workspace_size(T: int, H: int, I: int, E: int, topk: int) -> int:
+    return int(_functions().fp8_moe_workspace_size(T, H, I, E, topk))
+
+
+def _experts(qw1, sw1, qw2, sw2, H, device):
+    """(E, I, the four addresses) of the experts' weights for a hidden size H."""
+    if not isinstance(qw1, torch.Tensor) or qw1.dim() != 3 or qw1.shape[1] % 2:
+        raise ValueError("qw1: expected a 3-dim tensor [E, 2 I, H]")
+    E, I = qw1.shape[0], qw1.shape[1] // 2
+    return (E, I, _operand(qw1, torch.uint8, (E, 2 * I, H), "qw1", device),
+            _operand(sw1, torch.float32, (E, 2 * I // 128, H // 128), "sw1", device),
+            _operand(qw2, torch.uint8, (E, H, I), "qw2", device),
+            _operand(sw2, torch.float32, (E, H // 128, I // 128), "sw2", device))
+
+
+def _moe_out(T, H, I, E, k, out_dtype, out, workspace, device, stream):
+    """(output, its type code, workspace to keep, its address and size)."""
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    need = _functions().fp8_moe_workspace_size(T, H, I, E, k)
+    keep, ws, size = (None, None, 0) if _invalid(need) else _scratch(need, workspace, device, stream)
+    return _result(out, (T, H), out_dtype, "out", device, stream), _fb._odt(out_dtype), keep, ws, size
+
+
+def fp8_moe_experts(x, ids, weights, qw1, sw1, qw2, sw2, out_dtype=None, out=None, workspace=None, stream=None,
+                    scale_mode=_fb.FP8BLK_SCALE_POW2):
+    """The experts of a mixture for a few tokens (at most FP8MOE_MAX_TOKENS):
+    y[t] = sum_i weights[t,i] Wd[e] (silu(G[e] x[t]) * (U[e] x[t])), e =
+    ids[t,i]; ids that are no expert (-1) are left out.  x bf16 [T,H] (row
+    stride may exceed H); ids int32, weights fp32 [T,topk]; qw1 [E,2I,H] (G's
+    rows, then U's) and qw2 [E,H,I] codes, sw1 [E,2I/128,H/128] and sw2
+    [E,H/128,I/128], each as fp8_quantize_block quantizes the stacked matrix
+    -> y [T,H] bf16 or fp32.  Activations are quantized by scale_mode's rule,
+    the one that made the weights' scales."""
+    device, T, H, ld = _matrix(x, (torch.bfloat16,), "x")
+    E, I, pq1, ps1, pq2, ps2 = _experts(qw1, sw1, qw2, sw2, H, device)
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids: expected a 2-dim tensor")
+    k = ids.shape[1]
+    pids = _operand(ids, torch.int32, (T, k), "ids", device)
+    pw = _operand(weights, torch.float32, (T, k), "weights", device)
+    y, odt, keep, ws, size = _moe_out(T, H, I, E, k, out_dtype, out, workspace, device, stream)
+    _fb._check(_functions().fp8_moe_experts(T, H, I, E, k, x.data_ptr(), ld, pids, pw, pq1, ps1, pq2, ps2,
+                                            y.data_ptr(), odt, scale_mode, ws, size, _stream(stream, device)))
+    return y
+
+
+def fp8_moe_layer(x, wr, qw1, sw1, qw2, sw2, topk, renormalize=True, out_dtype=None, out=None, ids=None,
+                  weights=None, workspace=None, stream=None, scale_mode=_fb.FP8BLK_SCALE_POW2):
+    """A whole mixture-of-experts layer for a few tokens: router logits x wr^T
+    (wr bf16 [E,H]), fp8_moe_route's choice of topk experts, fp8_moe_experts of
+    it.  `ids` (int32) and `weights` (fp32) [T,topk], where given, get the
+    choice."""
+    device, T, H, ld = _matrix(x, (torch.bfloat16,), "x")
+    E, I, pq1, ps1, pq2, ps2 = _experts(qw1, sw1, qw2, sw2, H, device)
+    pwr = _operand(wr, torch.bfloat16, (E, H), "wr", device)
+    pids = None if ids is None else _operand(ids, torch.int32, (T, topk), "ids", device)
+    pw = None if weights is None else _operand(weights, torch.float32, (T, topk), "weights", device)
+    y, odt, keep, ws, size = _moe_out(T, H, I, E, topk, out_dtype, out, workspace, device, stream)
+    _fb._check(_functions().fp8_moe_layer(T, H, I, E, topk, int(bool(renormalize)), x.data_ptr(), ld, pwr, pq1, ps1,
+                                          pq2, ps2, y.data_ptr(), odt, scale_mode, pids, pw, ws, size,
+                                          _stream(stream, device)))
+    return y
