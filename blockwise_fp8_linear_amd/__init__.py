@@ -474,7 +474,7 @@ def fp8_block_gemm_backward_w_noalloc(qdy, sdy, qw, sw, qdyT, sdyT, qxT, sxT, dx
 # which importing this package does not.
 
 _MOE = ("fp8_linear", "fp8_linear_workspace_size", "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_experts",
-        "fp8_moe_layer", "fp8_moe_workspace_size", "FP8MOE_BF16", "FP8MOE_FP32", "FP8MOE_MAX_EXPERTS",
+        "fp8_moe_layer", "fp8_moe_workspace_size", "FP8_LINEAR_FP32_ROWS", "FP8MOE_BF16", "FP8MOE_FP32", "FP8MOE_MAX_EXPERTS",
         "FP8MOE_MAX_TOPK", "FP8MOE_MAX_TOKENS")
 
 

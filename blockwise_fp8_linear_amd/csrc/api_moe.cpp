@@ -14,7 +14,7 @@ namespace {
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Rows of x from which fp8_linear hands the multiples of 128 to the GEMMs.
-constexpr int64_t kGemmRows = 128;
+constexpr int64_t kGemmRows = FP8_LINEAR_FP32_ROWS + 1;
 
 // The rows that the GEMMs take, and their codes and scales in the workspace.
 int64_t gemm_rows(int64_t M) { return M < kGemmRows ? 0 : M / kGroup * kGroup; }

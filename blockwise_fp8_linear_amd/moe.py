@@ -20,6 +20,7 @@ import blockwise_fp8_linear_amd as _fb
 HEADER_PATH = os.path.join(os.path.dirname(_fb.HEADER_PATH), "fp8moe.h")
 
 # enum values and limits of include/fp8moe.h
+FP8_LINEAR_FP32_ROWS = 127
 FP8MOE_BF16 = 0
 FP8MOE_FP32 = 1
 FP8MOE_MAX_EXPERTS = 1024

@@ -24,6 +24,9 @@ extern "C" {
 /* Element type of router logits and of their gradient. */
 enum fp8moe_dtype { FP8MOE_BF16 = 0, FP8MOE_FP32 = 1 };
 
+/* fp8_linear sums products with fp32 faithfulness up to this many rows. */
+#define FP8_LINEAR_FP32_ROWS 127
+
 /* Limits of the mixture-of-experts entry points. */
 #define FP8MOE_MAX_EXPERTS 1024 /* E */
 #define FP8MOE_MAX_TOPK 16      /* k */
@@ -40,10 +43,10 @@ enum fp8moe_dtype { FP8MOE_BF16 = 0, FP8MOE_FP32 = 1 };
  *   N, K positive multiples of 128; x, qw, y 16-byte aligned.
  *   workspace: at least fp8_linear_workspace_size(M, N, K) bytes, 16-byte
  *     aligned; may be NULL when that size is 0 (it is for small M).
- * Small M is bound by reading the weights and runs as one launch that
- * quantizes x on the way, its products summed with fp32 faithfulness.  From
- * larger M on x is quantized into the workspace first and the multiples of
- * 128 rows go through the GEMMs of fp8blk.h, with their accuracy.
+ * Up to FP8_LINEAR_FP32_ROWS rows the call is bound by reading the weights; it
+ * quantizes x on the way and sums the products with fp32 faithfulness.  Above,
+ * x is quantized into the workspace first and the multiples of 128 rows go
+ * through the GEMMs of fp8blk.h, with their accuracy.
  */
 int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t *x, int64_t ld_x,
                const uint8_t *qw, const float *sw, void *y, int out_dtype, int scale_mode,
