@@ -94,7 +94,10 @@ MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int k) {
   w.logits = take(T * E, sizeof(float));
   w.ids = take(T * k, sizeof(int32_t));
   w.weights = take(T * k, sizeof(float));
+  w.qx = take(T * H, sizeof(uint8_t));
+  w.sx = take(T * (H / kGroup), sizeof(float));
   w.h = take(T * k * I, sizeof(uint16_t));
+  w.sh = take(T * k * (I / kGroup), sizeof(float));
   w.partial = take(T * k * H, sizeof(float));
   w.bytes = at;
   return w;

@@ -46,7 +46,7 @@ struct MoeArgs {
 // Where the pieces of a call's workspace start; ids and weights are used only
 // where the caller of the layer does not take them.
 struct MoeWorkspace {
-  size_t logits, ids, weights, h, partial, bytes;
+  size_t logits, ids, weights, qx, sx, h, sh, partial, bytes;
 };
 MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int k);
 

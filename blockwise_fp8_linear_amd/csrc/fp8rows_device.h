@@ -173,4 +173,68 @@ __device__ __forceinline__ void rows_product(const uint8_t* const (&wp)[RT], con
   }
 }
 
+// The same for x that is quantized already, and for a wave that owns its
+// weight rows over the whole reduction: xp[tt] points at the lane's piece of
+// its token's codes, xs[tt] at its token's scales.  Two stages are in
+// registers, one being multiplied while the next one loads; past the end the
+// last block is loaded again and not used, so that the loads of a stage stay
+// one run without branches and the compiler can wait for one stage while the
+// other is in flight.  Only the first `tiles` of the TT token tiles are read.
+template <int RT, int TT>
+struct RowsStage {
+  CodeFrag w[RT], x[TT];
+  float sx[TT], s[RT];
+
+  __device__ __forceinline__ void load(const uint8_t* const (&wp)[RT], const float* const (&sw)[RT],
+                                       const uint8_t* const (&xp)[TT], const float* const (&xs)[TT], int tiles,
+                                       int b) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) w[rt] = load_weights(wp[rt] + (int64_t)b * 128);
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      if (tt < tiles) {
+        x[tt] = load_codes(xp[tt] + b * 128);
+        sx[tt] = xs[tt][b];
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) s[rt] = sw[rt][b];
+  }
+
+  __device__ __forceinline__ void multiply(int tiles, v4f (&acc)[RT][TT]) const {
+    BfFrag wf[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) wf[rt] = decode(w[rt]);
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      if (tt < tiles) {
+        const BfFrag xf = decode(x[tt]);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const v4f p = block_product(wf[rt], xf);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[rt][tt][i] = __builtin_fmaf(p[i], sx[tt] * s[rt], acc[rt][tt][i]);
+        }
+      }
+    }
+  }
+};
+
+template <int RT, int TT>
+__device__ __forceinline__ void rows_stream(const uint8_t* const (&wp)[RT], const float* const (&sw)[RT],
+                                            const uint8_t* const (&xp)[TT], const float* const (&xs)[TT], int tiles,
+                                            int nkb, v4f (&acc)[RT][TT]) {
+  RowsStage<RT, TT> even, odd;
+  even.load(wp, sw, xp, xs, tiles, 0);
+  for (int b = 0; b < nkb; b += 2) {
+    odd.load(wp, sw, xp, xs, tiles, min(b + 1, nkb - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    even.multiply(tiles, acc);
+    if (b + 1 >= nkb) break;
+    even.load(wp, sw, xp, xs, tiles, min(b + 2, nkb - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    odd.multiply(tiles, acc);
+  }
+}
+
 }  // namespace fp8blk

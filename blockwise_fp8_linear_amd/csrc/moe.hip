@@ -1,5 +1,6 @@
 // A mixture-of-experts layer for a few tokens (include/fp8moe.h), gfx950.
 #include "fp8moe_launch.h"
+#include "fp8route_device.h"
 #include "fp8rows_device.h"
 
 namespace fp8blk {
@@ -38,6 +39,47 @@ __global__ __launch_bounds__(64 * kWaves) void logits_kernel(int T, int E, int H
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (t < T && e0 + 4 * c + i < E) logits[(int64_t)t * E + e0 + 4 * c + i] = acc[i];
+  }
+}
+
+// The choice of one token by one wave, from its logits.
+template <int NI>
+__device__ __forceinline__ RouteChoice choose(const float* __restrict__ row, int E, int k, bool renorm, int lane) {
+  float v[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) v[i] = lane + i * 64 < E ? row[lane + i * 64] : -INFINITY;
+  return route_choose<64, NI>(v, k, renorm, lane);
+}
+__device__ __forceinline__ RouteChoice choose(const float* __restrict__ row, int E, int k, bool renorm, int lane) {
+  if (E <= 64) return choose<1>(row, E, k, renorm, lane);
+  if (E <= 128) return choose<2>(row, E, k, renorm, lane);
+  if (E <= 256) return choose<4>(row, E, k, renorm, lane);
+  return choose<16>(row, E, k, renorm, lane);
+}
+
+// ---------------------------------------------------------------------------
+// One workgroup per token: its choice (where there are logits) and its row of
+// x quantized, 16 lanes per group of 128.
+// ---------------------------------------------------------------------------
+template <class S>
+__global__ __launch_bounds__(256) void prepare_kernel(MoeArgs a, const float* __restrict__ logits,
+                                                      uint8_t* __restrict__ qx, float* __restrict__ sx) {
+  const int t = blockIdx.x, l16 = threadIdx.x & 15;
+  for (int g = threadIdx.x >> 4; g < a.H / 128; g += 16) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(a.x + t * a.ld_x + g * 128 + l16 * 8);
+    uint32_t m = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
+    m = row16_max(max(m & 0xFFFFu, m >> 16));
+    const S sc(m);
+    *reinterpret_cast<uint2*>(qx + (int64_t)t * a.H + g * 128 + l16 * 8) =
+        make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
+    if (l16 == 0) sx[(int64_t)t * (a.H / 128) + g] = sc.s;
+  }
+  if (logits && threadIdx.x < 64) {
+    const RouteChoice c = choose(logits + (int64_t)t * a.E, a.E, a.k, a.renorm, threadIdx.x);
+    if ((int)threadIdx.x < a.k) {
+      a.ids[t * a.k + threadIdx.x] = c.id;
+      a.weights[t * a.k + threadIdx.x] = c.weight;
+    }
   }
 }
 
@@ -164,6 +206,118 @@ __global__ __launch_bounds__(64 * W) void down_kernel(MoeArgs a, const uint16_t*
   }
 }
 
+// ---------------------------------------------------------------------------
+// The same two products for many rows per launch: each wave owns 16 columns of
+// I (their G and their U rows), or 16 RT columns of H, over the whole
+// reduction, and the eight waves of a workgroup share the tokens' codes
+// through the caches.  128 columns of I in one workgroup are one group of h,
+// so h leaves quantized.
+// ---------------------------------------------------------------------------
+template <int TT, class S>
+__global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint8_t* __restrict__ qx,
+                                                           const float* __restrict__ sx, uint8_t* __restrict__ qh,
+                                                           float* __restrict__ sh) {
+  extern __shared__ uint16_t list[];
+  __shared__ int scratch[8];
+  __shared__ uint32_t amax[8][16 * TT];
+  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = blockIdx.y, n0 = blockIdx.x * 128 + wave * 16, nkb = a.H / 128;
+  const int rows = rows_of_expert(a.ids, a.T * a.k, e, list, scratch);
+
+  const uint8_t* base = a.qw1 + (int64_t)e * 2 * a.I * a.H;
+  const float* sbase = a.sw1 + (int64_t)e * (2 * a.I / 128) * nkb;
+  const uint8_t* const wp[2] = {base + (int64_t)(n0 + r) * a.H + c * 16, base + (int64_t)(a.I + n0 + r) * a.H + c * 16};
+  const float* const sp[2] = {sbase + n0 / 128 * nkb, sbase + (a.I + n0) / 128 * nkb};
+  for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
+    const uint8_t* xp[TT];
+    const float* xs[TT];
+    const int tiles = min(TT, (rows - r0 + 15) / 16);
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      const int t = list[min(r0 + tt * 16 + r, rows - 1)] / a.k;
+      xp[tt] = qx + (int64_t)t * a.H + c * 16;
+      xs[tt] = sx + (int64_t)t * nkb;
+    }
+    v4f acc[2][TT];
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) acc[0][tt] = acc[1][tt] = v4f{};
+    rows_stream<2, TT>(wp, sp, xp, xs, tiles, nkb, acc);
+    uint32_t h[TT][2];
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      const v4f g = acc[0][tt], u = acc[1][tt];
+      h[tt][0] = bf16x2_rne(silu(g[0]) * u[0], silu(g[1]) * u[1]);
+      h[tt][1] = bf16x2_rne(silu(g[2]) * u[2], silu(g[3]) * u[3]);
+      const uint32_t m = pk_max_u16(abs2(h[tt][0]), abs2(h[tt][1]));
+      amax[wave][tt * 16 + r] = quarter_max(max(m & 0xFFFFu, m >> 16));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) m = max(m, amax[w][tt * 16 + r]);
+      const S sc(m);
+      const int row = r0 + tt * 16 + r;
+      if (row < rows) {
+        const int64_t s = list[row];
+        *reinterpret_cast<uint32_t*>(qh + s * a.I + n0 + 4 * c) = quant4(h[tt][0], h[tt][1], sc);
+        if (wave == 0 && c == 0) sh[s * (a.I / 128) + blockIdx.x] = sc.s;
+      }
+    }
+    __syncthreads();  // before the next rows' maxima
+  }
+}
+
+template <int RT, int TT>
+__global__ __launch_bounds__(512) void down_wide_kernel(MoeArgs a, const uint8_t* __restrict__ qh,
+                                                        const float* __restrict__ sh, float* __restrict__ partial) {
+  extern __shared__ uint16_t list[];
+  __shared__ int scratch[8];
+  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = blockIdx.y, n0 = (blockIdx.x * 8 + wave) * 16 * RT, nkb = a.I / 128;
+  const int rows = rows_of_expert(a.ids, a.T * a.k, e, list, scratch);
+  if (n0 >= a.H) return;
+
+  const uint8_t* wp[RT];
+  const float* sp[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    wp[rt] = a.qw2 + ((int64_t)e * a.H + n0 + rt * 16 + r) * a.I + c * 16;
+    sp[rt] = a.sw2 + ((int64_t)e * (a.H / 128) + (n0 + rt * 16) / 128) * nkb;
+  }
+  for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
+    const uint8_t* xp[TT];
+    const float* xs[TT];
+    const int tiles = min(TT, (rows - r0 + 15) / 16);
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      const int64_t s = list[min(r0 + tt * 16 + r, rows - 1)];
+      xp[tt] = qh + s * a.I + c * 16;
+      xs[tt] = sh + s * nkb;
+    }
+    v4f acc[RT][TT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = v4f{};
+    rows_stream<RT, TT>(wp, sp, xp, xs, tiles, nkb, acc);
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      const int row = r0 + tt * 16 + r;
+      if (row < rows) {
+        const int64_t s = list[row];
+        const float w = a.weights[s];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          *reinterpret_cast<v4f*>(partial + s * a.H + n0 + rt * 16 + 4 * c) = acc[rt][tt] * w;
+      }
+    }
+  }
+}
+
 // y[t] = the sum of the token's terms in the order of its choice; ids that are
 // none have no term.
 __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, const float* __restrict__ partial) {
@@ -201,6 +355,35 @@ hipError_t experts_by_tokens(const MoeArgs& a, uint16_t* h, float* partial, hipS
   return experts<4, 4, S>(a, h, partial, stream);
 }
 
+template <int TT, class S>
+hipError_t experts_wide(const MoeArgs& a, const uint8_t* qx, const float* sx, uint8_t* qh, float* sh, float* partial,
+                        hipStream_t stream) {
+  const size_t lds = (size_t)a.T * a.k * sizeof(uint16_t);
+  hipLaunchKernelGGL((gate_up_wide_kernel<TT, S>), dim3(a.I / 128, a.E), dim3(512), lds, stream, a, qx, sx, qh, sh);
+  if (hipError_t e = hipGetLastError()) return e;
+  hipLaunchKernelGGL((down_wide_kernel<2, TT>), dim3((a.H + 255) / 256, a.E), dim3(512), lds, stream, a, qh, sh,
+                     partial);
+  if (hipError_t e = hipGetLastError()) return e;
+  hipLaunchKernelGGL(combine_kernel, dim3((a.T * (a.H / 4) + 255) / 256), dim3(256), 0, stream, a, partial);
+  return hipGetLastError();
+}
+
+template <class S>
+hipError_t moe_wide(const MoeArgs& a, const MoeWorkspace& w, const float* logits, hipStream_t stream) {
+  char* ws = static_cast<char*>(a.ws);
+  uint8_t* qx = reinterpret_cast<uint8_t*>(ws + w.qx);
+  float* sx = reinterpret_cast<float*>(ws + w.sx);
+  uint8_t* qh = reinterpret_cast<uint8_t*>(ws + w.h);
+  float* sh = reinterpret_cast<float*>(ws + w.sh);
+  float* partial = reinterpret_cast<float*>(ws + w.partial);
+  hipLaunchKernelGGL(prepare_kernel<S>, dim3(a.T), dim3(256), 0, stream, a, logits, qx, sx);
+  if (hipError_t e = hipGetLastError()) return e;
+  const int rows = a.T * a.k / a.E;
+  if (rows <= 8) return experts_wide<1, S>(a, qx, sx, qh, sh, partial, stream);
+  if (rows <= 20) return experts_wide<2, S>(a, qx, sx, qh, sh, partial, stream);
+  return experts_wide<4, S>(a, qx, sx, qh, sh, partial, stream);
+}
+
 }  // namespace
 
 hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
@@ -208,13 +391,16 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
   char* ws = static_cast<char*>(a.ws);
   uint16_t* h = reinterpret_cast<uint16_t*>(ws + w.h);
   float* partial = reinterpret_cast<float*>(ws + w.partial);
+  float* const logits = a.wr ? reinterpret_cast<float*>(ws + w.logits) : nullptr;
   if (a.wr) {
-    float* logits = reinterpret_cast<float*>(ws + w.logits);
     hipLaunchKernelGGL(logits_kernel, dim3((a.E + 15) / 16, (a.T + 15) / 16), dim3(64 * kWaves), 0, stream, a.T, a.E,
                        a.H, a.x, a.ld_x, a.wr, logits);
     if (hipError_t e = hipGetLastError()) return e;
-    if (hipError_t e = launch_moe_route(a.T, a.E, a.k, logits, true, a.E, a.renorm, a.ids, a.weights, stream)) return e;
   }
+  if (a.T > 16)
+    return a.fp32_scale ? moe_wide<Fp32Scale>(a, w, logits, stream) : moe_wide<Pow2Scale>(a, w, logits, stream);
+  if (a.wr)
+    if (hipError_t e = launch_moe_route(a.T, a.E, a.k, logits, true, a.E, a.renorm, a.ids, a.weights, stream)) return e;
   return a.fp32_scale ? experts_by_tokens<Fp32Scale>(a, h, partial, stream)
                       : experts_by_tokens<Pow2Scale>(a, h, partial, stream);
 }
