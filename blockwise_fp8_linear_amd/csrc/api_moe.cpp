@@ -11,20 +11,30 @@ using namespace fp8blk;
 
 namespace {
 
+// The kernels hold the offset of a row within 16 of them in 32 bits.
+constexpr int64_t kMaxStride = int64_t(1) << 26;
+
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Rows of x from which fp8_linear hands the multiples of 128 to the GEMMs.
-constexpr int64_t kGemmRows = FP8_LINEAR_FP32_ROWS + 1;
-
-// The rows that the GEMMs take, and their codes and scales in the workspace.
-int64_t gemm_rows(int64_t M) { return M < kGemmRows ? 0 : M / kGroup * kGroup; }
-size_t codes_bytes(int64_t M, int64_t K) { return up256((size_t)(gemm_rows(M) * K)); }
-size_t linear_bytes(int64_t M, int64_t K) {
-  return gemm_rows(M) ? codes_bytes(M, K) + up256((size_t)(gemm_rows(M) * (K / kGroup)) * sizeof(float)) : 0;
+// The rows that the GEMMs of fp8blk.h take: none where their 256x256 tiles
+// would leave most CUs idle, else the multiples of 128.  kGemmOutputs outputs are where
+// the two paths take the same time.
+constexpr int64_t kGemmOutputs = 3500000;
+int64_t gemm_rows(int64_t M, int64_t N) {
+  return M <= FP8_LINEAR_FP32_ROWS || M * N <= kGemmOutputs ? 0 : M / kGroup * kGroup;
+}
+// Their codes and scales in the workspace, in front of the other rows'.
+size_t codes_bytes(int64_t rows, int64_t K) { return up256((size_t)(rows * K)); }
+size_t gemm_bytes(int64_t rows, int64_t K) {
+  return rows ? codes_bytes(rows, K) + up256((size_t)(rows * (K / kGroup)) * sizeof(float)) : 0;
+}
+size_t linear_bytes(int64_t M, int64_t N, int64_t K) {
+  const int64_t main = gemm_rows(M, N);
+  return gemm_bytes(main, K) + rows_workspace_bytes(M - main, K);
 }
 
 bool linear_limits(int64_t M, int64_t N, int64_t K) {
-  return N / kGroup < (1 << 20) && K / kGroup < (1 << 20) && M < (int64_t(1) << 27) && prod_le(M, N, kMaxElems) &&
+  return N / kGroup < (1 << 20) && K / kGroup < (1 << 19) && M < (int64_t(1) << 27) && prod_le(M, N, kMaxElems) &&
          prod_le(M, K, kMaxElems) && prod_le(N, K, kMaxElems) && prod_lt(M, K / kGroup, int64_t(1) << 31);
 }
 
@@ -44,7 +54,7 @@ int check_route(int64_t T, int64_t E, int k, const void* logits, int dtype, int6
 int check_moe_shape(int64_t T, int64_t H, int64_t I, int64_t E, int k) {
   if (T <= 0 || E <= 0 || k <= 0 || !mult128(H) || !mult128(I)) return FP8BLK_ERR_DIM;
   if (T > FP8MOE_MAX_TOKENS || E > FP8MOE_MAX_EXPERTS || k > FP8MOE_MAX_TOPK || k > E || H > (1 << 20) ||
-      I > (1 << 20) || !prod_le(H, I, kMaxElems / (2 * FP8MOE_MAX_EXPERTS)))
+      I > (1 << 20) || !prod_le(H, I, kMaxElems / (2 * FP8MOE_MAX_EXPERTS)) || !prod_lt(T * k, I, int64_t(1) << 32))
     return FP8BLK_ERR_ARG;
   return FP8BLK_OK;
 }
@@ -58,7 +68,7 @@ int moe(int64_t T, int64_t H, int64_t I, int64_t E, int k, const uint16_t* x, in
     return FP8BLK_ERR_ARG;
   if (!x || !qw1 || !sw1 || !qw2 || !sw2 || !y) return FP8BLK_ERR_NULL;
   if (int rc = check_moe_shape(T, H, I, E, k)) return rc;
-  if (ld_x < H || !prod_le(T, ld_x, kMaxElems)) return FP8BLK_ERR_ARG;
+  if (ld_x < H || ld_x > kMaxStride) return FP8BLK_ERR_ARG;
   if (!aligned16(x) || ld_x % 8 || !aligned16(qw1) || !aligned16(qw2) || !aligned16(y) || !aligned4(sw1) ||
       !aligned4(sw2) || !aligned4(ids) || !aligned4(weights) || !aligned16(wr))
     return FP8BLK_ERR_ALIGN;
@@ -98,7 +108,8 @@ MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int k) {
   w.sx = take(T * (H / kGroup), sizeof(float));
   w.h = take(T * k * I, sizeof(uint16_t));
   w.sh = take(T * k * (I / kGroup), sizeof(float));
-  w.partial = take(T * k * H, sizeof(float));
+  // by row of h, or (few tokens) by workgroup that shares a column
+  w.partial = take((T <= 16 && k < 16 ? 16 : k) * T * H, sizeof(float));
   w.bytes = at;
   return w;
 }
@@ -109,7 +120,7 @@ extern "C" {
 
 size_t fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || !mult128(N) || !mult128(K) || !linear_limits(M, N, K)) return (size_t)-1;
-  return linear_bytes(M, K);
+  return linear_bytes(M, N, K);
 }
 
 int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw, const float* sw,
@@ -119,17 +130,17 @@ int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x,
     return FP8BLK_ERR_ARG;
   if (!x || !qw || !sw || !y) return FP8BLK_ERR_NULL;
   if (M <= 0 || !mult128(N) || !mult128(K)) return FP8BLK_ERR_DIM;
-  if (ld_x < K || !linear_limits(M, N, K) || !prod_le(M, ld_x, kMaxElems)) return FP8BLK_ERR_ARG;
+  if (ld_x < K || ld_x > kMaxStride || !linear_limits(M, N, K) || !prod_le(M, ld_x, kMaxElems)) return FP8BLK_ERR_ARG;
   if (!aligned16(x) || ld_x % 8 || !aligned16(qw) || !aligned4(sw) || !aligned16(y)) return FP8BLK_ERR_ALIGN;
-  const size_t need = linear_bytes(M, K);
+  const size_t need = linear_bytes(M, N, K);
   if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8BLK_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
   if (int rc = check_device()) return rc;
   const bool f32 = out_dtype != FP8BLK_OUT_BF16, fp32_scale = scale_mode == FP8BLK_SCALE_FP32;
-  const int64_t main = gemm_rows(M);
+  const int64_t main = gemm_rows(M, N);
   if (main > 0) {
     uint8_t* q = static_cast<uint8_t*>(workspace);
-    float* s = reinterpret_cast<float*>(q + codes_bytes(M, K));
+    float* s = reinterpret_cast<float*>(q + codes_bytes(main, K));
     if (hipError_t e = launch_quant_rowgroup(x, main, K, ld_x, q, K, s, fp32_scale, stream)) return finish(e);
     if (int rc = fp8_block_gemm(FP8BLK_OP_FPROP, main, N, K, q, s, qw, sw, y, out_dtype, FP8BLK_ALGO_DEFAULT,
                                 scale_mode, nullptr, 0, stream))
@@ -137,7 +148,8 @@ int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x,
   }
   if (main == M) return FP8BLK_OK;
   const RowsOut out{static_cast<char*>(y) + main * N * (f32 ? 4 : 2), f32, out_dtype == FP8BLK_OUT_FP32_ACCUM};
-  return finish(launch_linear_rows(M - main, N, K, x + main * ld_x, ld_x, qw, sw, out, fp32_scale, stream));
+  return finish(launch_linear_rows(M - main, N, K, x + main * ld_x, ld_x, qw, sw, out, fp32_scale,
+                                   static_cast<char*>(workspace) + gemm_bytes(main, K), stream));
 }
 
 int fp8_moe_route(int64_t T, int64_t E, int k, const void* logits, int dtype, int64_t ld, int renormalize,

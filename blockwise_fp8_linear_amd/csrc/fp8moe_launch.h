@@ -16,9 +16,16 @@ struct RowsOut {
   bool accumulate;  // fp32 only: y += result
 };
 
-// y = x W^T for M rows; x is quantized by the kernel (fp32_scale: amax / 448).
+// y = x W^T for M rows; x is quantized on the way (fp32_scale: amax / 448).
+// Above kRawRows rows through the workspace: codes, and from rows_scales_at on
+// their scales.
+constexpr int64_t kRawRows = 64;
+inline size_t rows_scales_at(int64_t M, int64_t K) { return ((size_t)(M * K) + 255) & ~size_t(255); }
+inline size_t rows_workspace_bytes(int64_t M, int64_t K) {
+  return M <= kRawRows ? 0 : rows_scales_at(M, K) + (((size_t)(M * (K / 128)) * sizeof(float) + 255) & ~size_t(255));
+}
 hipError_t launch_linear_rows(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
-                              const float* sw, RowsOut out, bool fp32_scale, hipStream_t stream);
+                              const float* sw, RowsOut out, bool fp32_scale, void* ws, hipStream_t stream);
 
 // f32: the logits' (and dlogits') type is fp32 instead of bf16.
 hipError_t launch_moe_route(int64_t T, int E, int k, const void* logits, bool f32, int64_t ld, bool renorm,

@@ -7,11 +7,11 @@
 //               sum_{k in b} dec(qx[t][k]) * dec(qw[n][k]),
 // with x quantized as by fp8_quantize_rowgroup (the same codes and scales).
 //
-// For few rows it is bound by reading the weights once, so it is laid out for
-// that: a wave takes 16 weight rows x 128 reduction values per step, straight
-// from memory into registers (no LDS: every weight byte is used by one wave
-// only), and the waves of a workgroup split the reduction and add their sums
-// through LDS in wave order, so results are deterministic.
+// For few rows it is bound by reading the weights once, and laid out for that:
+// a wave takes tiles of 16 weight rows x 128 reduction values, loaded by whole
+// lines into LDS that only it uses, and the waves of a workgroup split the
+// reduction (adding their sums in wave order at the end) or the weight rows;
+// either way the order of every sum is fixed.
 //
 // The products run on the bf16 matrix instructions, not the fp8 ones: an E4M3
 // value is a bf16 value exactly, a product of two is exact in fp32, and the
@@ -79,162 +79,253 @@ __device__ __forceinline__ uint32_t quarter_max(uint32_t v) {
   return max((uint32_t)b[0], (uint32_t)b[1]);
 }
 
-// A lane's 32 bf16 values of one 128-group, as loaded: the pieces 16 c .. +7,
-// 16 c + 8 .. +15, 64 + 16 c .. +7 and 64 + 16 c + 8 .. +15.
-struct RawFrag {
-  u32x4 w[4];
-};
+// ---------------------------------------------------------------------------
+// Operand tiles in LDS, filled by direct 16-byte global->LDS loads.
+//
+// Loading a fragment straight into registers would put neighbouring lanes on
+// different rows, and the address unit then takes one lane at a time: 16
+// bytes per clock and CU, measured as 57 cache accesses per load and the bound
+// of the first form of these kernels.  In a direct load neighbouring lanes take
+// neighbouring 16-byte chunks of one row (a whole 128-byte line per row of
+// codes), and the fragments are then read from LDS.
+//
+// Chunk i of row r of a tile lies at place i ^ (r & 7) of the row, so that
+// eight rows read at one chunk touch different banks.
+// ---------------------------------------------------------------------------
+constexpr int kCodeTile = 16 * 128;  // bytes of a tile of codes: 16 rows x 128
 
-__device__ __forceinline__ RawFrag load_raw(const uint16_t* p) {
-  RawFrag r;
-  r.w[0] = *reinterpret_cast<const u32x4*>(p);
-  r.w[1] = *reinterpret_cast<const u32x4*>(p + 8);
-  r.w[2] = *reinterpret_cast<const u32x4*>(p + 64);
-  r.w[3] = *reinterpret_cast<const u32x4*>(p + 72);
-  return r;
+// The row of the tile that lane p of direct load `load` brings a chunk of, and
+// the chunk's byte offset in that row: a load covers 8 rows.
+__device__ __forceinline__ uint32_t code_row(uint32_t p, int load) { return load * 8 + (p >> 3); }
+__device__ __forceinline__ uint32_t code_chunk(uint32_t p, int load) {
+  return ((p & 7) ^ (code_row(p, load) & 7)) << 4;
+}
+__device__ __forceinline__ CodeFrag read_codes(const uint8_t* tile, uint32_t r, uint32_t c) {
+  const uint32_t at = r * 128 + ((c ^ (r & 7)) << 4);
+  CodeFrag q;
+  q.lo = *reinterpret_cast<const u32x4*>(tile + at);
+  q.hi = *reinterpret_cast<const u32x4*>(tile + (at ^ 64));
+  return q;
 }
 
-// The group's codes (this lane's part) and its scale, exactly as the row-group
-// quantizer forms them: amax over the group, scale rule S, round to nearest
-// even.
+// Rows that are still bf16 come through registers, 4 to a load: lane p has the
+// chunk p % 16 (8 values) of row 4 load + p / 16, sixteen neighbouring lanes a
+// whole group.  They are quantized on the way into the tile of codes -- the
+// same codes and scale that the row-group quantizer gives: amax over the group,
+// scale rule S, round to nearest even -- and each row's scale goes to
+// scale[row].
+__device__ __forceinline__ uint32_t raw_row(uint32_t p, int load) { return load * 4 + (p >> 4); }
+
 template <class S>
-__device__ __forceinline__ CodeFrag quantize_group(const RawFrag& r, float& scale) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    m = pk_max_u16(m, pk_max_u16(pk_max_u16(abs2(r.w[j][0]), abs2(r.w[j][1])),
-                                 pk_max_u16(abs2(r.w[j][2]), abs2(r.w[j][3]))));
-  m = quarter_max(max(m & 0xFFFFu, m >> 16));
-  const S sc(m);
-  scale = sc.s;
-  CodeFrag q;
-  q.lo = u32x4{quant4(r.w[0][0], r.w[0][1], sc), quant4(r.w[0][2], r.w[0][3], sc), quant4(r.w[1][0], r.w[1][1], sc),
-               quant4(r.w[1][2], r.w[1][3], sc)};
-  q.hi = u32x4{quant4(r.w[2][0], r.w[2][1], sc), quant4(r.w[2][2], r.w[2][3], sc), quant4(r.w[3][0], r.w[3][1], sc),
-               quant4(r.w[3][2], r.w[3][3], sc)};
-  return q;
+__device__ __forceinline__ void quantize_into(uint8_t* tile, float* scale, const u32x4& v, uint32_t p, int load) {
+  const uint32_t row = raw_row(p, load), l16 = p & 15;
+  const uint32_t m = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
+  const S sc(row16_max(max(m & 0xFFFFu, m >> 16)));
+  *reinterpret_cast<uint2*>(tile + row * 128 + (((l16 >> 1) ^ (row & 7)) << 4) + (l16 & 1) * 8) =
+      make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
+  if (l16 == 0) scale[row] = sc.s;
 }
 
-__device__ __forceinline__ CodeFrag load_codes(const uint8_t* p) {
-  CodeFrag q;
-  q.lo = *reinterpret_cast<const u32x4*>(p);
-  q.hi = *reinterpret_cast<const u32x4*>(p + 64);
-  return q;
-}
+// The wave's direct loads have landed / its LDS reads have returned.  (Written
+// out because the compiler does not know of the direct loads.)
+__device__ __forceinline__ void loads_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void reads_returned() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// Weights: read once by one wave; each line of 128 bytes is taken by two
-// adjacent loads of the same wave.
-__device__ __forceinline__ CodeFrag load_weights(const uint8_t* p) { return load_codes(p); }
-
+// ---------------------------------------------------------------------------
 // acc[rt][tt] += the blocks [b0, b1) of RT 16-row weight tiles times TT
-// 16-token tiles.  Per lane: wp[rt] is its piece of its weight row at block
-// 0, xp[tt] its piece of its token's row; sw[rt] points at the scales of the
-// weight blocks that hold the tile (wave-uniform).  A lane without a token of
-// its own points at some other row that may be read: the tokens are columns of
-// the matrix instruction and do not mix, and its sums are not for use (leaving
-// such loads out by a mask measured slower).  All loads of D blocks are issued
-// before the first is used.
-template <int RT, int TT, int D, class S>
-__device__ __forceinline__ void rows_product(const uint8_t* const (&wp)[RT], const float* const (&sw)[RT],
-                                             const uint16_t* const (&xp)[TT], int b0, int b1, v4f (&acc)[RT][TT]) {
+// 16-token tiles, by one wave on its own: `lds` is its own area of
+// D * rows_stage_bytes<RT, TT, RAW, XL>() bytes and no barrier is passed.  The
+// loads of up to D blocks are issued together and then waited for; what hides
+// them is the other waves of the CU, each at its own place.
+//   w[rt]: the tile's first row at block 0 (wave-uniform), rows K bytes apart
+//   sw[rt]: the scales of the weight blocks that hold the tile
+//   RAW: the tokens' rows are bf16 and quantized here by rule S; otherwise they
+//     are codes, and xs[tt] points at the scales of token l % 16 of the tile,
+//     xs_b apart from block to block
+//   XL: loads per token tile, 4 rows each (codes: 8); with fewer than the
+//     tile has, the rows beyond repeat the last one (the tokens are columns of
+//     the matrix instruction and do not mix, and nobody wants theirs)
+//   x: base of the tokens' rows (wave-uniform), xoff[tt][u]: for this lane the
+//     byte offset of its chunk of the row that load u of tile tt brings
+// ---------------------------------------------------------------------------
+template <int RT, int TT, bool RAW, int XL>
+__device__ __host__ constexpr int rows_stage_bytes() {
+  return RT * kCodeTile + TT * XL * (RAW ? 512 + 16 : 1024);
+}
+
+template <int RT, int TT, int XL, int D, bool RAW, class S>
+__device__ __forceinline__ void rows_product(uint8_t* lds, const uint8_t* const (&w)[RT], const float* const (&sw)[RT],
+                                             int64_t K, const uint8_t* x, const uint32_t (&xoff)[TT][XL],
+                                             const float* const (&xs)[TT], int64_t xs_b, int b0, int b1,
+                                             v4f (&acc)[RT][TT]) {
+  constexpr int SB = rows_stage_bytes<RT, TT, RAW, XL>(), ROWS = XL * (RAW ? 4 : 8);
+  constexpr int TILE = ROWS * 128, SCALES = RT * kCodeTile + TT * TILE;  // (raw) the rows' scales behind the tiles
+  const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4, xr = min(r, (uint32_t)ROWS - 1);
+  const uint32_t at = lds_offset(lds);
+  const uint32_t woff[2] = {(uint32_t)(code_row(lane, 0) * K) + code_chunk(lane, 0),
+                            (uint32_t)(code_row(lane, 1) * K) + code_chunk(lane, 1)};
   for (int b = b0; b < b1; b += D) {
-    CodeFrag w[D][RT];
-    RawFrag x[D][TT];
-    float s[D][RT];
+    float s[D][RT], m[D][TT];
+    u32x4 v[D][TT][RAW ? XL : 1];
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      const int i = min(b + d, b1 - 1);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) w[d][rt] = load_weights(wp[rt] + (int64_t)i * 128);
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) x[d][tt] = load_raw(xp[tt] + (int64_t)i * 128);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) s[d][rt] = sw[rt][i];
-    }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (d > 0 && b + d >= b1) break;
-      BfFrag xf[TT];
-      float m[TT];
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) xf[tt] = decode(quantize_group<S>(x[d][tt], m[tt]));
+      if (b + d >= b1) break;
+      const int i = b + d;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const BfFrag wf = decode(w[d][rt]);
+        dma16(w[rt] + (int64_t)i * 128, woff[0], at + d * SB + rt * kCodeTile);
+        dma16(w[rt] + (int64_t)i * 128, woff[1], at + d * SB + rt * kCodeTile + 1024);
+        s[d][rt] = sw[rt][i];
+      }
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+#pragma unroll
+        for (int u = 0; u < XL; ++u) {
+          if constexpr (RAW)
+            v[d][tt][u] = *reinterpret_cast<const u32x4*>(x + (int64_t)i * 256 + xoff[tt][u]);
+          else
+            dma16(x + (int64_t)i * 128, xoff[tt][u], at + d * SB + RT * kCodeTile + tt * TILE + u * 1024);
+        }
+        if constexpr (!RAW) m[d][tt] = xs[tt][i * xs_b];
+      }
+    }
+    if constexpr (RAW) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (b + d >= b1) break;
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+          for (int u = 0; u < XL; ++u)
+            quantize_into<S>(lds + d * SB + RT * kCodeTile + tt * TILE,
+                             reinterpret_cast<float*>(lds + d * SB + SCALES) + tt * ROWS, v[d][tt][u], lane, u);
+      }
+    }
+    loads_landed();
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (b + d >= b1) break;
+      const uint8_t* st = lds + d * SB;
+      BfFrag xf[TT];
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        if constexpr (RAW) m[d][tt] = reinterpret_cast<const float*>(st + SCALES)[tt * ROWS + xr];
+        xf[tt] = decode(read_codes(st + RT * kCodeTile + tt * TILE, xr, c));
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const BfFrag wf = decode(read_codes(st + rt * kCodeTile, r, c));
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
           const v4f p = block_product(wf, xf[tt]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[rt][tt][i] = __builtin_fmaf(p[i], m[tt] * s[d][rt], acc[rt][tt][i]);
+          for (int i = 0; i < 4; ++i) acc[rt][tt][i] = __builtin_fmaf(p[i], m[d][tt] * s[d][rt], acc[rt][tt][i]);
+        }
+      }
+    }
+    reads_returned();  // before the next loads overwrite what was read
+  }
+}
+
+// ---------------------------------------------------------------------------
+// acc[rt][tt] += all blocks of RT 16-row weight tiles (each wave its own) times
+// the TT 16-token tiles that the workgroup's eight waves share.  Every thread
+// of the workgroup calls it, with the same x, xs and nkb.
+//   The blocks go through a ring of D slots in LDS, filled D - 1 blocks ahead;
+// each wave loads its own weight tiles and an eighth of the tokens' codes (some
+// twice where there are fewer loads than waves, so that every wave has the same
+// number in flight).  One barrier per block says that the block has landed for
+// everyone and that the slot before it may be filled again.
+//   Scales: the weights' in registers, lane i holding block i's; the tokens' in
+// LDS, [block][token]; both for 64 blocks at a time.
+//   xoff: the byte offset, from x, of the row of this lane's load;
+//   xscale(token of the TT tiles, block) gives a scale from memory.
+// ---------------------------------------------------------------------------
+constexpr int kPanel = 64;
+
+template <int RT, int TT, int D>
+__device__ __host__ constexpr int rows_ring_bytes() {
+  return D * (8 * RT + TT) * kCodeTile + kPanel * 16 * TT * 4;
+}
+
+template <int RT, int TT, int D, class XScale>
+__device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w)[RT], const float* const (&sw)[RT],
+                                          int64_t K, const uint8_t* x, uint32_t xoff, XScale xscale, int nkb,
+                                          v4f (&acc)[RT][TT]) {
+  constexpr int SLOT = (8 * RT + TT) * kCodeTile, PER = 2 * RT + 1;
+  static_assert(D == 2 || D == 3 || D == 4, "the waits below");
+  const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), xload = wave % (2 * TT);
+  const uint32_t at = lds_offset(lds);
+  float* const scales = reinterpret_cast<float*>(lds + D * SLOT);
+  const uint32_t woff[2] = {(uint32_t)(code_row(lane, 0) * K) + code_chunk(lane, 0),
+                            (uint32_t)(code_row(lane, 1) * K) + code_chunk(lane, 1)};
+  for (int p0 = 0; p0 < nkb; p0 += kPanel) {
+    const int nb = min(kPanel, nkb - p0);
+    float s[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) s[rt] = sw[rt][p0 + min((int)lane, nb - 1)];
+    __syncthreads();  // the scales and slots before have been read
+    for (int i = threadIdx.x; i < nb * 16 * TT; i += 512) scales[i] = xscale(i % (16 * TT), p0 + i / (16 * TT));
+
+    const auto issue = [&](int b) {
+      const uint32_t slot = at + (b % D) * SLOT;
+      const int64_t k = (int64_t)(p0 + b) * 128;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        dma16(w[rt] + k, woff[0], slot + (wave * RT + rt) * kCodeTile);
+        dma16(w[rt] + k, woff[1], slot + (wave * RT + rt) * kCodeTile + 1024);
+      }
+      dma16(x + k, xoff, slot + 8 * RT * kCodeTile + xload * 1024);
+    };
+    __syncthreads();  // the scales are there (and every load known to the compiler has landed)
+#pragma unroll
+    for (int b = 0; b < D - 1; ++b)
+      if (b < nb) issue(b);
+    for (int b = 0; b < nb; ++b) {
+      if (D > 3 && b + 2 < nb)
+        wait_vmcnt<(D > 3 ? 2 : 0) * PER>();
+      else if (D > 2 && b + 1 < nb)
+        wait_vmcnt<(D > 2 ? 1 : 0) * PER>();
+      else
+        wait_vmcnt<0>();
+      lds_barrier();
+      if (b + D - 1 < nb) issue(b + D - 1);
+      const uint8_t* slot = lds + (b % D) * SLOT;
+      BfFrag wf[RT];
+      float sb[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        wf[rt] = decode(read_codes(slot + (wave * RT + rt) * kCodeTile, r, c));
+        sb[rt] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s[rt]), b));
+      }
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        const BfFrag xf = decode(read_codes(slot + (8 * RT + tt) * kCodeTile, r, c));
+        const float m = scales[b * 16 * TT + tt * 16 + r];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const v4f p = block_product(wf[rt], xf);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[rt][tt][i] = __builtin_fmaf(p[i], m * sb[rt], acc[rt][tt][i]);
         }
       }
     }
   }
 }
 
-// The same for x that is quantized already, and for a wave that owns its
-// weight rows over the whole reduction: xp[tt] points at the lane's piece of
-// its token's codes, xs[tt] at its token's scales.  Two stages are in
-// registers, one being multiplied while the next one loads; past the end the
-// last block is loaded again and not used, so that the loads of a stage stay
-// one run without branches and the compiler can wait for one stage while the
-// other is in flight.  Only the first `tiles` of the TT token tiles are read.
-template <int RT, int TT>
-struct RowsStage {
-  CodeFrag w[RT], x[TT];
-  float sx[TT], s[RT];
-
-  __device__ __forceinline__ void load(const uint8_t* const (&wp)[RT], const float* const (&sw)[RT],
-                                       const uint8_t* const (&xp)[TT], const float* const (&xs)[TT], int tiles,
-                                       int b) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) w[rt] = load_weights(wp[rt] + (int64_t)b * 128);
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-      if (tt < tiles) {
-        x[tt] = load_codes(xp[tt] + b * 128);
-        sx[tt] = xs[tt][b];
-      }
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) s[rt] = sw[rt][b];
-  }
-
-  __device__ __forceinline__ void multiply(int tiles, v4f (&acc)[RT][TT]) const {
-    BfFrag wf[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) wf[rt] = decode(w[rt]);
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-      if (tt < tiles) {
-        const BfFrag xf = decode(x[tt]);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const v4f p = block_product(wf[rt], xf);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[rt][tt][i] = __builtin_fmaf(p[i], sx[tt] * s[rt], acc[rt][tt][i]);
-        }
-      }
-    }
-  }
+// f(tag) for the number of 16-row tiles that hold
+// `rows` rows, at most MAX.
+template <int V>
+struct Tiles {
+  static constexpr int value = V;
 };
-
-template <int RT, int TT>
-__device__ __forceinline__ void rows_stream(const uint8_t* const (&wp)[RT], const float* const (&sw)[RT],
-                                            const uint8_t* const (&xp)[TT], const float* const (&xs)[TT], int tiles,
-                                            int nkb, v4f (&acc)[RT][TT]) {
-  RowsStage<RT, TT> even, odd;
-  even.load(wp, sw, xp, xs, tiles, 0);
-  for (int b = 0; b < nkb; b += 2) {
-    odd.load(wp, sw, xp, xs, tiles, min(b + 1, nkb - 1));
-    __builtin_amdgcn_sched_barrier(0);
-    even.multiply(tiles, acc);
-    if (b + 1 >= nkb) break;
-    even.load(wp, sw, xp, xs, tiles, min(b + 2, nkb - 1));
-    __builtin_amdgcn_sched_barrier(0);
-    odd.multiply(tiles, acc);
+template <int MAX, class F>
+__device__ __forceinline__ void with_tiles(int rows, F f) {
+  if constexpr (MAX > 1) {
+    if (rows <= 16 * (MAX - 1)) return with_tiles<MAX - 1>(rows, f);
   }
+  f(Tiles<MAX>{});
 }
 
 }  // namespace fp8blk

@@ -1,4 +1,5 @@
 // A mixture-of-experts layer for a few tokens (include/fp8moe.h), gfx950.
+#include "fp8blk_launch.h"
 #include "fp8moe_launch.h"
 #include "fp8route_device.h"
 #include "fp8rows_device.h"
@@ -7,34 +8,34 @@ namespace fp8blk {
 
 namespace {
 
-constexpr int kWaves = 8;  // of every kernel that multiplies
-
 // ---------------------------------------------------------------------------
 // Router logits x wr^T, fp32: 16 experts x 16 tokens per workgroup, the waves
 // split H.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(64 * kWaves) void logits_kernel(int T, int E, int H, const uint16_t* __restrict__ x,
+constexpr int kLogitsWaves = 16;
+__global__ __launch_bounds__(64 * kLogitsWaves) void logits_kernel(int T, int E, int H, const uint16_t* __restrict__ x,
                                                              int64_t ld_x, const uint16_t* __restrict__ wr,
                                                              float* __restrict__ logits) {
-  __shared__ v4f red[kWaves][64];
+  __shared__ v4f red[kLogitsWaves][64];
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16, nkb = H / 128;
   const uint16_t* wp = wr + (int64_t)min(e0 + r, E - 1) * H + c * 16;
   const uint16_t* xp = x + (int64_t)min(t0 + r, T - 1) * ld_x + c * 16;
   v4f acc{};
-  for (int b = wave; b < nkb; b += kWaves) {
-    const RawFrag w = load_raw(wp + b * 128), v = load_raw(xp + b * 128);
+  for (int b = wave; b < nkb; b += kLogitsWaves) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf_t, w.w[j]),
-                                                    __builtin_bit_cast(v8bf_t, v.w[j]), acc, 0, 0, 0);
+    for (int j = 0; j < 4; ++j) {
+      const int at = b * 128 + (j >> 1) * 64 + (j & 1) * 8;
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const v8bf_t*>(wp + at),
+                                                    *reinterpret_cast<const v8bf_t*>(xp + at), acc, 0, 0, 0);
+    }
   }
   red[wave][lane] = acc;
   __syncthreads();
   if (wave == 0) {
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) acc += red[w][lane];
+    for (int w = 1; w < kLogitsWaves; ++w) acc += red[w][lane];
     const int t = t0 + r;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(MoeArgs a, const float* __
     const S sc(m);
     *reinterpret_cast<uint2*>(qx + (int64_t)t * a.H + g * 128 + l16 * 8) =
         make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
-    if (l16 == 0) sx[(int64_t)t * (a.H / 128) + g] = sc.s;
+    if (l16 == 0) sx[(int64_t)g * a.T + t] = sc.s;
   }
   if (logits && threadIdx.x < 64) {
     const RouteChoice c = choose(logits + (int64_t)t * a.E, a.E, a.k, a.renorm, threadIdx.x);
@@ -106,104 +107,253 @@ __device__ __forceinline__ int rows_of_expert(const int32_t* __restrict__ ids, i
   return found;
 }
 
+// Four neighbouring elements of the result.
+__device__ __forceinline__ void store4(const RowsOut& out, int64_t at, const v4f& v) {
+  if (out.f32)
+    *reinterpret_cast<v4f*>(static_cast<float*>(out.y) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out.y) + at) =
+        make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+}
+
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
 // ---------------------------------------------------------------------------
-// h[row] = bf16(silu(G x) * (U x)) for the rows that chose expert blockIdx.y:
-// 16 columns of I per workgroup.
+// Up to 16 tokens: the tokens themselves are the columns of the matrix
+// instruction, whichever expert is multiplied, and the waves of a workgroup
+// split the reduction, so that a few experts of one token fill the chip.
 // ---------------------------------------------------------------------------
-template <int W, int TT, class S>
-__global__ __launch_bounds__(64 * W) void gate_up_kernel(MoeArgs a, uint16_t* __restrict__ h) {
-  __shared__ uint16_t list[8192];
-  __shared__ int scratch[W];
-  extern __shared__ v4f red[];  // [W][2 * TT][64]
-  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int e = blockIdx.y, n0 = blockIdx.x * 16, nkb = a.H / 128;
-  const int rows = rows_of_expert(a.ids, a.T * a.k, e, list, scratch);
+constexpr int kFew = 16;
+constexpr int kParts = 16;  // workgroups that share a column of y, at most
+
+// The choice of the whole call in LDS, and the experts it reaches, in the order
+// of their first mention.
+struct FewChoice {
+  int32_t ids[kFew * 16];    // -1 where there is none
+  float weights[kFew * 16];
+  int32_t first[1024];       // by expert: the first place that names it
+};
+
+// Fills it: from the logits (ROUTE), or from a.ids and a.weights.  Every
+// thread of the workgroup calls it.
+template <bool ROUTE>
+__device__ __forceinline__ void few_choice(const MoeArgs& a, const float* __restrict__ logits, FewChoice& f) {
+  const int n = a.T * a.k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) f.first[i] = n;
+  if constexpr (ROUTE) {
+    for (int t = wave; t < a.T; t += waves) {
+      const RouteChoice c = choose(logits + (int64_t)t * a.E, a.E, a.k, a.renorm, lane);
+      if (lane < a.k) {
+        f.ids[t * a.k + lane] = c.id;
+        f.weights[t * a.k + lane] = c.weight;
+      }
+    }
+  } else {
+    for (int s = threadIdx.x; s < n; s += blockDim.x) {
+      const int id = a.ids[s];
+      f.ids[s] = id >= 0 && id < a.E ? id : -1;
+      f.weights[s] = a.weights[s];
+    }
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < n; s += blockDim.x)
+    if (f.ids[s] >= 0) atomicMin(&f.first[f.ids[s]], s);  // a minimum: the order does not matter
+  __syncthreads();
+}
+
+// The `want`-th expert reached, -1 if there are fewer; by one wave.
+__device__ __forceinline__ int few_expert(const FewChoice& f, int n, int want) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int s0 = 0; s0 < n; s0 += 64) {
+    const int s = s0 + lane, id = s < n ? f.ids[s] : -1;
+    const uint64_t mask = __ballot(id >= 0 && f.first[max(id, 0)] == s);
+    const int rank = before + __popcll(mask & ((1ull << lane) - 1));
+    const uint64_t found = __ballot(((mask >> lane) & 1) && rank == want);
+    if (found) return __builtin_amdgcn_readlane(id, __builtin_ctzll(found));
+    before += __popcll(mask);
+  }
+  return -1;
+}
+
+// The first place of token t that names expert e, -1 if there is none.
+__device__ __forceinline__ int few_place(const FewChoice& f, int t, int k, int e) {
+  for (int j = 0; j < k; ++j)
+    if (f.ids[t * k + j] == e) return t * k + j;
+  return -1;
+}
+
+// h[place] = bf16(silu(G x) * (U x)): 16 columns of I of the blockIdx.y-th
+// expert reached.  XL loads bring x's rows of a block, 4 each.
+template <int W, int XL, int D, bool ROUTE, class S>
+__global__ __launch_bounds__(64 * W) void gate_up_few_kernel(MoeArgs a, const float* __restrict__ logits,
+                                                             uint16_t* __restrict__ h) {
+  extern __shared__ uint8_t lds[];  // the waves' areas; then their sums, [W][2][64] v4f
+  __shared__ FewChoice f;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16, nkb = a.H / 128, n = a.T * a.k;
+  few_choice<ROUTE>(a, logits, f);
+  if (ROUTE && blockIdx.x == 0 && blockIdx.y == 0) {
+    for (int s = threadIdx.x; s < n; s += 64 * W) {
+      a.ids[s] = f.ids[s];
+      a.weights[s] = f.weights[s];
+    }
+  }
+  const int e = few_expert(f, n, blockIdx.y);
+  if (e < 0) return;
 
   const uint8_t* base = a.qw1 + (int64_t)e * 2 * a.I * a.H;
   const float* sbase = a.sw1 + (int64_t)e * (2 * a.I / 128) * nkb;
-  const uint8_t* const wp[2] = {base + (int64_t)(n0 + r) * a.H + c * 16, base + (int64_t)(a.I + n0 + r) * a.H + c * 16};
+  const uint8_t* const wp[2] = {base + (int64_t)n0 * a.H, base + (int64_t)(a.I + n0) * a.H};
   const float* const sp[2] = {sbase + n0 / 128 * nkb, sbase + (a.I + n0) / 128 * nkb};
-  for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
-    const uint16_t* xp[TT];
+  const float* const none[1] = {nullptr};
+  uint32_t xoff[1][XL];
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
-      xp[tt] = a.x + (list[min(r0 + tt * 16 + r, rows - 1)] / a.k) * a.ld_x + c * 16;
-    v4f acc[2][TT];
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) acc[0][tt] = acc[1][tt] = v4f{};
-    rows_product<2, TT, 1, S>(wp, sp, xp, wave * nkb / W, (wave + 1) * nkb / W, acc);
-    if (r0) __syncthreads();  // the previous tile's sums have been read
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) red[(wave * 2 * TT + rt * TT + tt) * 64 + lane] = acc[rt][tt];
-    __syncthreads();
-    for (int u = threadIdx.x; u < TT * 64; u += 64 * W) {
-      v4f g = red[u], up = red[TT * 64 + u];
-      for (int w = 1; w < W; ++w) {
-        g += red[w * 2 * TT * 64 + u];
-        up += red[w * 2 * TT * 64 + TT * 64 + u];
-      }
-      const int row = r0 + (u >> 6) * 16 + (u & 15);
-      if (row < rows)
-        *reinterpret_cast<uint2*>(h + (int64_t)list[row] * a.I + n0 + 4 * ((u & 63) >> 4)) =
-            make_uint2(bf16x2_rne(silu(g[0]) * up[0], silu(g[1]) * up[1]),
-                       bf16x2_rne(silu(g[2]) * up[2], silu(g[3]) * up[3]));
+  for (int u = 0; u < XL; ++u)
+    xoff[0][u] = (uint32_t)(min((int)raw_row(lane, u), a.T - 1) * a.ld_x * 2) + (lane & 15) * 16;
+  v4f acc[2][1] = {};
+  rows_product<2, 1, XL, D, true, S>(lds + wave * D * rows_stage_bytes<2, 1, true, XL>(), wp, sp, a.H,
+                                     reinterpret_cast<const uint8_t*>(a.x), xoff, none, 0, wave * nkb / W,
+                                     (wave + 1) * nkb / W, acc);
+  v4f* red = reinterpret_cast<v4f*>(lds);
+  __syncthreads();
+  red[(wave * 2) * 64 + lane] = acc[0][0];
+  red[(wave * 2 + 1) * 64 + lane] = acc[1][0];
+  __syncthreads();
+  if (wave == 0 && (lane & 15) < a.T) {
+    v4f g = red[lane], u = red[64 + lane];
+    for (int w = 1; w < W; ++w) {
+      g += red[w * 128 + lane];
+      u += red[w * 128 + 64 + lane];
     }
+    const int place = few_place(f, lane & 15, a.k, e);
+    if (place >= 0)
+      *reinterpret_cast<uint2*>(h + (int64_t)place * a.I + n0 + 4 * (lane >> 4)) =
+          make_uint2(bf16x2_rne(silu(g[0]) * u[0], silu(g[1]) * u[1]), bf16x2_rne(silu(g[2]) * u[2], silu(g[3]) * u[3]));
   }
 }
 
-// ---------------------------------------------------------------------------
-// partial[row] = weight * Wd h[row], fp32, for the rows that chose expert
-// blockIdx.y: 16 RT columns of H per workgroup.
-// ---------------------------------------------------------------------------
-template <int W, int RT, int TT, class S>
-__global__ __launch_bounds__(64 * W) void down_kernel(MoeArgs a, const uint16_t* __restrict__ h,
-                                                      float* __restrict__ partial) {
-  __shared__ uint16_t list[8192];
-  __shared__ int scratch[W];
-  extern __shared__ v4f red[];  // [W][RT * TT][64]
+// y, 16 columns of H per workgroup: the blocks of all experts reached are one
+// long reduction, which the workgroups of a column (gridDim.y) and their waves
+// split; a term's routing weight goes into its block's scale.  RAW: h is bf16
+// [place][I] and quantized here; otherwise it is codes, with the scales
+// sh[I / 128][place].  With several workgroups per column their sums go to
+// partial[blockIdx.y][t][H] instead of y.
+template <int W, int XL, int D, bool RAW, class S>
+__global__ __launch_bounds__(64 * W) void down_few_kernel(MoeArgs a, const uint8_t* __restrict__ h,
+                                                          const float* __restrict__ sh, float* __restrict__ partial) {
+  extern __shared__ uint8_t lds[];  // the waves' areas; then their sums, [W][64] v4f
+  __shared__ FewChoice f;
+  __shared__ int16_t place[kFew * 16][kFew];  // by expert reached and token: the place whose h it is, -1 none
+  __shared__ float weight[kFew * 16];         // by place: of the expert named there, all of its token's mentions
+  __shared__ int16_t expert[kFew * 16];
+  constexpr int SB = rows_stage_bytes<1, 1, RAW, XL>(), ROWS = XL * (RAW ? 4 : 8), TILE = ROWS * 128;
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int e = blockIdx.y, n0 = blockIdx.x * 16 * RT, nkb = a.I / 128;
-  const int rows = rows_of_expert(a.ids, a.T * a.k, e, list, scratch);
-
-  const uint8_t* wp[RT];
-  const float* sp[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    wp[rt] = a.qw2 + ((int64_t)e * a.H + n0 + rt * 16 + r) * a.I + c * 16;
-    sp[rt] = a.sw2 + ((int64_t)e * (a.H / 128) + (n0 + rt * 16) / 128) * nkb;
+  const int n0 = blockIdx.x * 16, nkb = a.I / 128, n = a.T * a.k;
+  few_choice<false>(a, nullptr, f);
+  int reached = 0;
+  for (int s0 = 0; s0 < n; s0 += 64) {  // every wave finds the same list
+    const int s = s0 + lane, id = s < n ? f.ids[s] : -1;
+    const bool is = id >= 0 && f.first[max(id, 0)] == s;
+    const uint64_t mask = __ballot(is);
+    if (is) expert[reached + __popcll(mask & ((1ull << lane) - 1))] = (int16_t)id;
+    reached += __popcll(mask);
   }
-  for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
-    const uint16_t* xp[TT];
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) xp[tt] = h + (int64_t)list[min(r0 + tt * 16 + r, rows - 1)] * a.I + c * 16;
-    v4f acc[RT][TT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = v4f{};
-    rows_product<RT, TT, 1, S>(wp, sp, xp, wave * nkb / W, (wave + 1) * nkb / W, acc);
-    if (r0) __syncthreads();  // the previous tile's sums have been read
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) red[(wave * RT * TT + rt * TT + tt) * 64 + lane] = acc[rt][tt];
-    __syncthreads();
-    for (int u = threadIdx.x; u < RT * TT * 64; u += 64 * W) {
-      v4f v = red[u];
-      for (int w = 1; w < W; ++w) v += red[w * RT * TT * 64 + u];
-      const int tile = u >> 6, l = u & 63, row = r0 + (tile % TT) * 16 + (l & 15);
-      if (row < rows) {
-        const int s = list[row];
-        *reinterpret_cast<v4f*>(partial + (int64_t)s * a.H + n0 + (tile / TT) * 16 + 4 * (l >> 4)) = v * a.weights[s];
+  __syncthreads();
+  for (int i = threadIdx.x; i < reached * kFew; i += 64 * W) {
+    const int at = i / kFew, t = i % kFew, e = expert[at];
+    int p = -1;
+    float w = 0.0f;
+    if (t < a.T) {
+      for (int j = a.k - 1; j >= 0; --j) {
+        if (f.ids[t * a.k + j] == e) {
+          p = t * a.k + j;
+          w += f.weights[p];
+        }
       }
     }
+    place[at][t] = (int16_t)p;
+    if (p >= 0) weight[p] = w;
   }
+  __syncthreads();
+
+  v4f acc{};
+  uint8_t* const area = lds + wave * D * SB;
+  const uint32_t at0 = lds_offset(area), xr = min(r, ROWS - 1);
+  const uint32_t woff[2] = {(uint32_t)(code_row(lane, 0) * a.I) + code_chunk(lane, 0),
+                            (uint32_t)(code_row(lane, 1) * a.I) + code_chunk(lane, 1)};
+  const int64_t total = (int64_t)reached * nkb, parts = (int64_t)gridDim.y * W, part = (int64_t)blockIdx.y * W + wave;
+  const int end = (int)((part + 1) * total / parts);
+  for (int b = (int)(part * total / parts); b < end; b += D) {
+    float s[D], m[D];
+    u32x4 v[D][RAW ? XL : 1];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (b + d >= end) break;
+      const int which = (b + d) / nkb, i = b + d - which * nkb;
+      const int e = __builtin_amdgcn_readfirstlane(expert[which]);
+      const uint8_t* w = a.qw2 + ((int64_t)e * a.H + n0) * a.I + (int64_t)i * 128;
+      dma16(w, woff[0], at0 + d * SB);
+      dma16(w, woff[1], at0 + d * SB + 1024);
+      s[d] = a.sw2[((int64_t)e * (a.H / 128) + n0 / 128) * nkb + i];
+#pragma unroll
+      for (int u = 0; u < XL; ++u) {
+        const int64_t p = max((int)place[which][RAW ? raw_row(lane, u) : code_row(lane, u)], 0);
+        if constexpr (RAW)
+          v[d][u] = *reinterpret_cast<const u32x4*>(h + (p * a.I + i * 128) * 2 + (lane & 15) * 16);
+        else
+          dma16(h + (int64_t)i * 128, (uint32_t)(p * a.I) + code_chunk(lane, u), at0 + d * SB + kCodeTile + u * 1024);
+      }
+      if constexpr (!RAW) m[d] = sh[(int64_t)i * n + max((int)place[which][r], 0)];
+    }
+    if constexpr (RAW) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (b + d >= end) break;
+#pragma unroll
+        for (int u = 0; u < XL; ++u)
+          quantize_into<S>(area + d * SB + kCodeTile, reinterpret_cast<float*>(area + d * SB + kCodeTile + TILE), v[d][u],
+                           lane, u);
+      }
+    }
+    loads_landed();
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (b + d >= end) break;
+      const int which = (b + d) / nkb, p = place[which][r];
+      const uint8_t* st = area + d * SB;
+      if constexpr (RAW) m[d] = reinterpret_cast<const float*>(st + kCodeTile + TILE)[xr];
+      const v4f prod = block_product(decode(read_codes(st, r, c)), decode(read_codes(st + kCodeTile, xr, c)));
+      const float scale = m[d] * weight[max(p, 0)] * s[d];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // others' values do not come near (they may not even be finite)
+        acc[i] = p >= 0 ? __builtin_fmaf(prod[i], scale, acc[i]) : acc[i];
+    }
+    reads_returned();
+  }
+  v4f* red = reinterpret_cast<v4f*>(lds);
+  __syncthreads();
+  red[wave * 64 + lane] = acc;
+  __syncthreads();
+  if (wave == 0 && r < a.T) {
+    v4f v = red[lane];
+    for (int w = 1; w < W; ++w) v += red[w * 64 + lane];
+    const int64_t at = (int64_t)r * a.H + n0 + 4 * c;
+    if (gridDim.y > 1)
+      *reinterpret_cast<v4f*>(partial + (int64_t)blockIdx.y * a.T * a.H + at) = v;
+    else
+      store4(a.out, at, v);
+  }
+}
+
+// y = the sum of `parts` partial results, in their order.
+__global__ __launch_bounds__(256) void sum_parts_kernel(MoeArgs a, const float* __restrict__ partial, int parts) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, size = (int64_t)a.T * a.H;
+  if (at >= size) return;
+  v4f v{};
+  for (int p = 0; p < parts; ++p) v += *reinterpret_cast<const v4f*>(partial + p * size + at);
+  store4(a.out, at, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -213,13 +363,21 @@ __global__ __launch_bounds__(64 * W) void down_kernel(MoeArgs a, const uint16_t*
 // through the caches.  128 columns of I in one workgroup are one group of h,
 // so h leaves quantized.
 // ---------------------------------------------------------------------------
-template <int TT, class S>
+template <int TT>
+constexpr int kSlots = 2;
+// Dynamic LDS: the ring for the most tiles, then the list of rows.
+constexpr int kMostRows = 8192;  // T k
+template <int TMAX>
+constexpr int kRing = rows_ring_bytes<2, TMAX, kSlots<TMAX>>();
+
+template <int TMAX, class S>
 __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint8_t* __restrict__ qx,
                                                            const float* __restrict__ sx, uint8_t* __restrict__ qh,
                                                            float* __restrict__ sh) {
-  extern __shared__ uint16_t list[];
+  extern __shared__ uint8_t lds[];
   __shared__ int scratch[8];
-  __shared__ uint32_t amax[8][16 * TT];
+  __shared__ uint32_t amax[8][16 * TMAX];
+  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<TMAX>);
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = blockIdx.y, n0 = blockIdx.x * 128 + wave * 16, nkb = a.H / 128;
@@ -227,94 +385,87 @@ __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint
 
   const uint8_t* base = a.qw1 + (int64_t)e * 2 * a.I * a.H;
   const float* sbase = a.sw1 + (int64_t)e * (2 * a.I / 128) * nkb;
-  const uint8_t* const wp[2] = {base + (int64_t)(n0 + r) * a.H + c * 16, base + (int64_t)(a.I + n0 + r) * a.H + c * 16};
+  const uint8_t* const wp[2] = {base + (int64_t)n0 * a.H, base + (int64_t)(a.I + n0) * a.H};
   const float* const sp[2] = {sbase + n0 / 128 * nkb, sbase + (a.I + n0) / 128 * nkb};
-  for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
-    const uint8_t* xp[TT];
-    const float* xs[TT];
-    const int tiles = min(TT, (rows - r0 + 15) / 16);
+  for (int r0 = 0; r0 < rows; r0 += 16 * TMAX) {
+    with_tiles<TMAX>(rows - r0, [&](auto tag) {
+      constexpr int TT = decltype(tag)::value;
+      const int load = wave % (2 * TT), row = r0 + (load >> 1) * 16 + code_row(lane, load & 1);
+      const uint32_t xoff = (uint32_t)(list[min(row, rows - 1)] / a.k) * a.H + code_chunk(lane, load & 1);
+      v4f acc[2][TT];
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-      const int t = list[min(r0 + tt * 16 + r, rows - 1)] / a.k;
-      xp[tt] = qx + (int64_t)t * a.H + c * 16;
-      xs[tt] = sx + (int64_t)t * nkb;
-    }
-    v4f acc[2][TT];
+      for (int tt = 0; tt < TT; ++tt) acc[0][tt] = acc[1][tt] = v4f{};
+      rows_ring<2, TT, kSlots<TMAX>>(
+          lds, wp, sp, a.H, qx, xoff,
+          [&](int i, int b) { return sx[(int64_t)b * a.T + list[min(r0 + i, rows - 1)] / a.k]; }, nkb, acc);
+      uint32_t h[TT][2];
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt) acc[0][tt] = acc[1][tt] = v4f{};
-    rows_stream<2, TT>(wp, sp, xp, xs, tiles, nkb, acc);
-    uint32_t h[TT][2];
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-      const v4f g = acc[0][tt], u = acc[1][tt];
-      h[tt][0] = bf16x2_rne(silu(g[0]) * u[0], silu(g[1]) * u[1]);
-      h[tt][1] = bf16x2_rne(silu(g[2]) * u[2], silu(g[3]) * u[3]);
-      const uint32_t m = pk_max_u16(abs2(h[tt][0]), abs2(h[tt][1]));
-      amax[wave][tt * 16 + r] = quarter_max(max(m & 0xFFFFu, m >> 16));
-    }
-    __syncthreads();
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) m = max(m, amax[w][tt * 16 + r]);
-      const S sc(m);
-      const int row = r0 + tt * 16 + r;
-      if (row < rows) {
-        const int64_t s = list[row];
-        *reinterpret_cast<uint32_t*>(qh + s * a.I + n0 + 4 * c) = quant4(h[tt][0], h[tt][1], sc);
-        if (wave == 0 && c == 0) sh[s * (a.I / 128) + blockIdx.x] = sc.s;
+      for (int tt = 0; tt < TT; ++tt) {
+        const v4f g = acc[0][tt], u = acc[1][tt];
+        h[tt][0] = bf16x2_rne(silu(g[0]) * u[0], silu(g[1]) * u[1]);
+        h[tt][1] = bf16x2_rne(silu(g[2]) * u[2], silu(g[3]) * u[3]);
+        const uint32_t m = pk_max_u16(abs2(h[tt][0]), abs2(h[tt][1]));
+        amax[wave][tt * 16 + r] = quarter_max(max(m & 0xFFFFu, m >> 16));
       }
-    }
-    __syncthreads();  // before the next rows' maxima
+      __syncthreads();
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) m = max(m, amax[w][tt * 16 + r]);
+        const S sc(m);
+        const int row = r0 + tt * 16 + r;
+        if (row < rows) {
+          const int64_t s = list[row];
+          *reinterpret_cast<uint32_t*>(qh + s * a.I + n0 + 4 * c) = quant4(h[tt][0], h[tt][1], sc);
+          if (wave == 0 && c == 0) sh[(int64_t)blockIdx.x * (a.T * a.k) + s] = sc.s;
+        }
+      }
+      // (the next rows' maxima are written behind rows_ring's barriers)
+    });
   }
 }
 
-template <int RT, int TT>
+template <int TMAX>
 __global__ __launch_bounds__(512) void down_wide_kernel(MoeArgs a, const uint8_t* __restrict__ qh,
                                                         const float* __restrict__ sh, float* __restrict__ partial) {
-  extern __shared__ uint16_t list[];
+  extern __shared__ uint8_t lds[];
   __shared__ int scratch[8];
+  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<TMAX>);
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int e = blockIdx.y, n0 = (blockIdx.x * 8 + wave) * 16 * RT, nkb = a.I / 128;
+  const int e = blockIdx.y, n0 = (blockIdx.x * 8 + wave) * 32, nkb = a.I / 128;
+  // waves past the last column (H may be an odd number of 128s) repeat it: they pass the barriers and store nothing
+  const int n = min(n0, a.H - 32);
   const int rows = rows_of_expert(a.ids, a.T * a.k, e, list, scratch);
-  if (n0 >= a.H) return;
 
-  const uint8_t* wp[RT];
-  const float* sp[RT];
+  const uint8_t* base = a.qw2 + ((int64_t)e * a.H + n) * a.I;
+  const float* s = a.sw2 + ((int64_t)e * (a.H / 128) + n / 128) * nkb;
+  const uint8_t* const wp[2] = {base, base + (int64_t)16 * a.I};
+  const float* const sp[2] = {s, s};
+  for (int r0 = 0; r0 < rows; r0 += 16 * TMAX) {
+    with_tiles<TMAX>(rows - r0, [&](auto tag) {
+      constexpr int TT = decltype(tag)::value;
+      const int load = wave % (2 * TT), row = r0 + (load >> 1) * 16 + code_row(lane, load & 1);
+      const uint32_t xoff = (uint32_t)list[min(row, rows - 1)] * a.I + code_chunk(lane, load & 1);
+      v4f acc[2][TT];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    wp[rt] = a.qw2 + ((int64_t)e * a.H + n0 + rt * 16 + r) * a.I + c * 16;
-    sp[rt] = a.sw2 + ((int64_t)e * (a.H / 128) + (n0 + rt * 16) / 128) * nkb;
-  }
-  for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
-    const uint8_t* xp[TT];
-    const float* xs[TT];
-    const int tiles = min(TT, (rows - r0 + 15) / 16);
+      for (int tt = 0; tt < TT; ++tt) acc[0][tt] = acc[1][tt] = v4f{};
+      rows_ring<2, TT, kSlots<TMAX>>(
+          lds, wp, sp, a.I, qh, xoff,
+          [&](int i, int b) { return sh[(int64_t)b * (a.T * a.k) + list[min(r0 + i, rows - 1)]]; }, nkb, acc);
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-      const int64_t s = list[min(r0 + tt * 16 + r, rows - 1)];
-      xp[tt] = qh + s * a.I + c * 16;
-      xs[tt] = sh + s * nkb;
-    }
-    v4f acc[RT][TT];
+      for (int tt = 0; tt < TT; ++tt) {
+        const int row = r0 + tt * 16 + r;
+        if (row < rows && n0 < a.H) {
+          const int64_t s = list[row];
+          const float w = a.weights[s];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = v4f{};
-    rows_stream<RT, TT>(wp, sp, xp, xs, tiles, nkb, acc);
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-      const int row = r0 + tt * 16 + r;
-      if (row < rows) {
-        const int64_t s = list[row];
-        const float w = a.weights[s];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          *reinterpret_cast<v4f*>(partial + s * a.H + n0 + rt * 16 + 4 * c) = acc[rt][tt] * w;
+          for (int rt = 0; rt < 2; ++rt)
+            *reinterpret_cast<v4f*>(partial + s * a.H + n0 + rt * 16 + 4 * c) = acc[rt][tt] * w;
+        }
       }
-    }
+    });
   }
 }
 
@@ -329,59 +480,88 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, const float* __
     const int s = t * a.k + j, id = a.ids[s];
     if (id >= 0 && id < a.E) v += *reinterpret_cast<const v4f*>(partial + (int64_t)s * a.H + n);
   }
-  if (a.out.f32)
-    *reinterpret_cast<v4f*>(static_cast<float*>(a.out.y) + (int64_t)t * a.H + n) = v;
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.y) + (int64_t)t * a.H + n) =
-        make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+  store4(a.out, (int64_t)t * a.H + n, v);
 }
 
-template <int W, int TT, class S>
-hipError_t experts(const MoeArgs& a, uint16_t* h, float* partial, hipStream_t stream) {
-  hipLaunchKernelGGL((gate_up_kernel<W, TT, S>), dim3(a.I / 16, a.E), dim3(64 * W), W * 2 * TT * 64 * sizeof(v4f),
-                     stream, a, h);
+// The launches of up to kFew tokens, and of more.
+struct MoeBuffers {
+  float* logits;  // null where ids and weights are given
+  uint8_t *qx, *h;
+  float *sx, *sh, *partial;
+};
+
+// `reached`: about how many experts the tokens reach.
+template <int XL, bool RAW, class S>
+hipError_t down_few(const MoeArgs& a, const MoeBuffers& b, double reached, hipStream_t stream) {
+  constexpr int W = XL == 1 && RAW ? 16 : 8, D = RAW ? 2 : 1, lds = W * D * rows_stage_bytes<1, 1, RAW, XL>();
+  static_assert(lds >= W * 1024, "the waves' sums fit");
+  static std::atomic<uint64_t> raised{0};
+  const auto k = &down_few_kernel<W, XL, D, RAW, S>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), lds, &raised)) return e;
+  const double blocks = reached * (a.I / 128) * (a.H / 16);  // of 2 KiB
+  int parts = (int)(blocks / 12000);
+  parts = parts < 1 ? 1 : parts > kParts ? kParts : parts;
+  hipLaunchKernelGGL(k, dim3(a.H / 16, parts), dim3(64 * W), lds, stream, a, b.h, b.sh, b.partial);
+  if (parts == 1) return hipGetLastError();
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL((down_kernel<W, 2, TT, S>), dim3(a.H / 32, a.E), dim3(64 * W), W * 2 * TT * 64 * sizeof(v4f),
-                     stream, a, h, partial);
-  if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL(combine_kernel, dim3((a.T * (a.H / 4) + 255) / 256), dim3(256), 0, stream, a, partial);
+  hipLaunchKernelGGL(sum_parts_kernel, dim3((a.T * (a.H / 4) + 255) / 256), dim3(256), 0, stream, a, b.partial, parts);
   return hipGetLastError();
 }
 
-template <class S>
-hipError_t experts_by_tokens(const MoeArgs& a, uint16_t* h, float* partial, hipStream_t stream) {
-  if (a.T <= 16) return experts<8, 1, S>(a, h, partial, stream);
-  if (a.T <= 32) return experts<8, 2, S>(a, h, partial, stream);
-  return experts<4, 4, S>(a, h, partial, stream);
+template <int XL, class S>
+hipError_t moe_few(const MoeArgs& a, const MoeBuffers& b, double reached, hipStream_t stream) {
+  constexpr int W = 8, D = 1, lds = W * D * rows_stage_bytes<2, 1, true, XL>();
+  static_assert(lds >= W * 2 * 1024, "the waves' sums fit");
+  static std::atomic<uint64_t> raised[2];
+  const auto k = b.logits ? &gate_up_few_kernel<W, XL, D, true, S> : &gate_up_few_kernel<W, XL, D, false, S>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), lds, &raised[b.logits != nullptr])) return e;
+  const int most = a.T * a.k < a.E ? a.T * a.k : a.E;  // experts reached
+  hipLaunchKernelGGL(k, dim3(a.I / 16, most), dim3(64 * W), lds, stream, a, b.logits, reinterpret_cast<uint16_t*>(b.h));
+  if (hipError_t e = hipGetLastError()) return e;
+  return down_few<XL, true, S>(a, b, reached, stream);
 }
 
 template <int TT, class S>
-hipError_t experts_wide(const MoeArgs& a, const uint8_t* qx, const float* sx, uint8_t* qh, float* sh, float* partial,
-                        hipStream_t stream) {
-  const size_t lds = (size_t)a.T * a.k * sizeof(uint16_t);
-  hipLaunchKernelGGL((gate_up_wide_kernel<TT, S>), dim3(a.I / 128, a.E), dim3(512), lds, stream, a, qx, sx, qh, sh);
+hipError_t gate_up_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
+  static std::atomic<uint64_t> raised{0};
+  const auto k = &gate_up_wide_kernel<TT, S>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), kRing<TT> + kMostRows * 2, &raised)) return e;
+  hipLaunchKernelGGL(k, dim3(a.I / 128, a.E), dim3(512), kRing<TT> + a.T * a.k * 2, stream, a, b.qx, b.sx, b.h, b.sh);
+  return hipGetLastError();
+}
+
+template <int TT, class S>
+hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
+  if (hipError_t e = gate_up_wide<TT, S>(a, b, stream)) return e;
+  static std::atomic<uint64_t> raised{0};
+  const auto k = &down_wide_kernel<TT>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), kRing<TT> + kMostRows * 2, &raised)) return e;
+  hipLaunchKernelGGL(k, dim3((a.H + 255) / 256, a.E), dim3(512), kRing<TT> + a.T * a.k * 2, stream, a, b.h, b.sh,
+                     b.partial);
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL((down_wide_kernel<2, TT>), dim3((a.H + 255) / 256, a.E), dim3(512), lds, stream, a, qh, sh,
-                     partial);
-  if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL(combine_kernel, dim3((a.T * (a.H / 4) + 255) / 256), dim3(256), 0, stream, a, partial);
+  hipLaunchKernelGGL(combine_kernel, dim3((a.T * (a.H / 4) + 255) / 256), dim3(256), 0, stream, a, b.partial);
   return hipGetLastError();
 }
 
 template <class S>
-hipError_t moe_wide(const MoeArgs& a, const MoeWorkspace& w, const float* logits, hipStream_t stream) {
-  char* ws = static_cast<char*>(a.ws);
-  uint8_t* qx = reinterpret_cast<uint8_t*>(ws + w.qx);
-  float* sx = reinterpret_cast<float*>(ws + w.sx);
-  uint8_t* qh = reinterpret_cast<uint8_t*>(ws + w.h);
-  float* sh = reinterpret_cast<float*>(ws + w.sh);
-  float* partial = reinterpret_cast<float*>(ws + w.partial);
-  hipLaunchKernelGGL(prepare_kernel<S>, dim3(a.T), dim3(256), 0, stream, a, logits, qx, sx);
+hipError_t moe(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
+  // how many experts the tokens reach, if each expert is as likely as the next
+  double missed = 1.0;
+  for (int t = 0; t < a.T; ++t) missed *= 1.0 - (double)a.k / a.E;
+  const double reached = a.E * (1.0 - missed);
+  if (a.T <= 8 || (a.T <= kFew && reached * (a.I / 128) < 192)) {
+    if (a.T <= 4) return moe_few<1, S>(a, b, reached, stream);
+    return a.T <= 8 ? moe_few<2, S>(a, b, reached, stream) : moe_few<4, S>(a, b, reached, stream);
+  }
+  hipLaunchKernelGGL(prepare_kernel<S>, dim3(a.T), dim3(256), 0, stream, a, b.logits, b.qx, b.sx);
   if (hipError_t e = hipGetLastError()) return e;
-  const int rows = a.T * a.k / a.E;
-  if (rows <= 8) return experts_wide<1, S>(a, qx, sx, qh, sh, partial, stream);
-  if (rows <= 20) return experts_wide<2, S>(a, qx, sx, qh, sh, partial, stream);
-  return experts_wide<4, S>(a, qx, sx, qh, sh, partial, stream);
+  if (a.T <= kFew) {
+    if (hipError_t e = gate_up_wide<1, S>(a, b, stream)) return e;
+    return a.T <= 8 ? down_few<1, false, S>(a, b, reached, stream) : down_few<2, false, S>(a, b, reached, stream);
+  }
+  const int rows = a.T * a.k / a.E;  // of an expert, on average
+  if (rows <= 8) return moe_wide<1, S>(a, b, stream);
+  return rows <= 20 ? moe_wide<2, S>(a, b, stream) : moe_wide<4, S>(a, b, stream);
 }
 
 }  // namespace
@@ -389,20 +569,15 @@ hipError_t moe_wide(const MoeArgs& a, const MoeWorkspace& w, const float* logits
 hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
   const MoeWorkspace w = moe_workspace(a.T, a.H, a.I, a.E, a.k);
   char* ws = static_cast<char*>(a.ws);
-  uint16_t* h = reinterpret_cast<uint16_t*>(ws + w.h);
-  float* partial = reinterpret_cast<float*>(ws + w.partial);
-  float* const logits = a.wr ? reinterpret_cast<float*>(ws + w.logits) : nullptr;
+  const auto f32 = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
+  const MoeBuffers b{a.wr ? f32(w.logits) : nullptr, reinterpret_cast<uint8_t*>(ws + w.qx),
+                     reinterpret_cast<uint8_t*>(ws + w.h), f32(w.sx), f32(w.sh), f32(w.partial)};
   if (a.wr) {
-    hipLaunchKernelGGL(logits_kernel, dim3((a.E + 15) / 16, (a.T + 15) / 16), dim3(64 * kWaves), 0, stream, a.T, a.E,
-                       a.H, a.x, a.ld_x, a.wr, logits);
+    hipLaunchKernelGGL(logits_kernel, dim3((a.E + 15) / 16, (a.T + 15) / 16), dim3(64 * kLogitsWaves), 0, stream, a.T, a.E,
+                       a.H, a.x, a.ld_x, a.wr, b.logits);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  if (a.T > 16)
-    return a.fp32_scale ? moe_wide<Fp32Scale>(a, w, logits, stream) : moe_wide<Pow2Scale>(a, w, logits, stream);
-  if (a.wr)
-    if (hipError_t e = launch_moe_route(a.T, a.E, a.k, logits, true, a.E, a.renorm, a.ids, a.weights, stream)) return e;
-  return a.fp32_scale ? experts_by_tokens<Fp32Scale>(a, h, partial, stream)
-                      : experts_by_tokens<Pow2Scale>(a, h, partial, stream);
+  return a.fp32_scale ? moe<Fp32Scale>(a, b, stream) : moe<Pow2Scale>(a, b, stream);
 }
 
 }  // namespace fp8blk

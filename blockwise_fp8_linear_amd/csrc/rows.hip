@@ -1,4 +1,5 @@
 // y = x W^T for a few rows of x (fp8_linear), gfx950.
+#include "fp8blk_launch.h"
 #include "fp8moe_launch.h"
 #include "fp8rows_device.h"
 
@@ -6,35 +7,48 @@ namespace fp8blk {
 
 namespace {
 
-template <int W, int RT, int TT, int D, class S>
-__global__ __launch_bounds__(64 * W) void linear_rows_kernel(int64_t M, int64_t N, int64_t K, const uint16_t* __restrict__ x, int64_t ld_x,
-                                   const uint8_t* __restrict__ qw, const float* __restrict__ sw, RowsOut out) {
-  extern __shared__ v4f red[];  // [waves][RT * TT][64]
-  const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+// One workgroup: 16 RT columns of y, 16 TT rows, the W waves splitting the
+// reduction.  RAW: xv is x in bf16 (ld_x elements apart) and quantized here;
+// otherwise its codes [M][K], with the scales transposed, xs[K / 128][M].
+template <int W, int RT, int TT, int XL, int D, bool RAW, class S>
+__global__ __launch_bounds__(64 * W) void linear_rows_kernel(int64_t M, int64_t N, int64_t K, const uint8_t* xv,
+                                                             int64_t row_bytes, const float* __restrict__ xs,
+                                                             const uint8_t* __restrict__ qw,
+                                                             const float* __restrict__ sw, RowsOut out) {
+  extern __shared__ uint8_t lds[];  // the waves' areas; then their sums, [W][RT * TT][64] v4f
+  const uint32_t lane = threadIdx.x & 63, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * (16 * RT), m0 = (int64_t)blockIdx.y * (16 * TT);
-  const int nkb = (int)(K / 128);
+  const int nkb = (int)(K / 128), rows = (int)(M - m0 < 16 * TT ? M - m0 : 16 * TT);
 
   const uint8_t* wp[RT];
   const float* sp[RT];
-  const uint16_t* xp[TT];
+  const float* xsp[TT];
+  uint32_t xoff[TT][XL];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    wp[rt] = qw + (n0 + rt * 16 + r) * K + c * 16;
+    wp[rt] = qw + (n0 + rt * 16) * K;
     sp[rt] = sw + (n0 + rt * 16) / 128 * nkb;
   }
 #pragma unroll
   for (int tt = 0; tt < TT; ++tt) {
-    const int64_t m = m0 + tt * 16 + r;
-    xp[tt] = x + (m < M ? m : M - 1) * ld_x + c * 16;
+#pragma unroll
+    for (int u = 0; u < XL; ++u) {
+      const int row = tt * 16 + (int)(RAW ? raw_row(lane, u) : code_row(lane, u));
+      xoff[tt][u] = (uint32_t)(min(row, rows - 1) * row_bytes) + (RAW ? (lane & 15) * 16 : code_chunk(lane, u));
+    }
+    xsp[tt] = RAW ? nullptr : xs + m0 + min(tt * 16 + (int)r, rows - 1);
   }
   v4f acc[RT][TT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = v4f{};
-  rows_product<RT, TT, D, S>(wp, sp, xp, wave * nkb / W, (wave + 1) * nkb / W, acc);
+  rows_product<RT, TT, XL, D, RAW, S>(lds + wave * D * rows_stage_bytes<RT, TT, RAW, XL>(), wp, sp, K, xv + m0 * row_bytes,
+                                      xoff, xsp, M, wave * nkb / W, (wave + 1) * nkb / W, acc);
 
+  v4f* red = reinterpret_cast<v4f*>(lds);
+  __syncthreads();
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -56,46 +70,89 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(int64_t M, int64_t 
   }
 }
 
-template <int W, int RT, int TT, int D, class S>
-hipError_t launch(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
-                  const float* sw, RowsOut out, hipStream_t stream) {
+template <int W, int RT, int TT, int XL, int D, bool RAW, class S>
+hipError_t launch(int64_t M, int64_t N, int64_t K, const void* x, int64_t row_bytes, const float* xs,
+                  const uint8_t* qw, const float* sw, RowsOut out, hipStream_t stream) {
   const dim3 grid((uint32_t)(N / (16 * RT)), (uint32_t)((M + 16 * TT - 1) / (16 * TT)));
-  hipLaunchKernelGGL((linear_rows_kernel<W, RT, TT, D, S>), grid, dim3(64 * W), W * RT * TT * 64 * sizeof(v4f),
-                     stream, M, N, K, x, ld_x, qw, sw, out);
+  constexpr int area = D * rows_stage_bytes<RT, TT, RAW, XL>(), sums = RT * TT * 64 * (int)sizeof(v4f);
+  constexpr int lds = W * (area > sums ? area : sums);
+  static std::atomic<uint64_t> raised{0};
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&linear_rows_kernel<W, RT, TT, XL, D, RAW, S>), lds,
+                                      &raised))
+    return e;
+  hipLaunchKernelGGL((linear_rows_kernel<W, RT, TT, XL, D, RAW, S>), grid, dim3(64 * W), lds, stream, M, N, K,
+                     static_cast<const uint8_t*>(x), row_bytes, xs, qw, sw, out);
   return hipGetLastError();
 }
 
-template <int RT, int TT, class S>
-hipError_t launch_tile(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
-                       const float* sw, RowsOut out, hipStream_t stream) {
-  constexpr int W = RT * TT > 6 ? 4 : 8;
-  return launch<W, RT, TT, 1, S>(M, N, K, x, ld_x, qw, sw, out, stream);
+// ---------------------------------------------------------------------------
+// Codes of all rows of x, with the scales transposed ([K / 128][M]): what the
+// tiles of several rows load.  16 lanes per group of 128.
+// ---------------------------------------------------------------------------
+template <class S>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t M, int nkb, const uint16_t* __restrict__ x,
+                                                            int64_t ld_x, uint8_t* __restrict__ q,
+                                                            float* __restrict__ s) {
+  const int64_t u = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4), m = u / nkb;
+  const int l16 = threadIdx.x & 15, g = (int)(u - m * nkb);
+  if (m >= M) return;
+  const u32x4 v = *reinterpret_cast<const u32x4*>(x + m * ld_x + g * 128 + l16 * 8);
+  uint32_t a = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
+  a = row16_max(max(a & 0xFFFFu, a >> 16));
+  const S sc(a);
+  *reinterpret_cast<uint2*>(q + (m * nkb + g) * 128 + l16 * 8) =
+      make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
+  if (l16 == 0) s[g * M + m] = sc.s;
 }
 
-template <int TT, class S>
-hipError_t launch_tokens(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
-                         const float* sw, RowsOut out, hipStream_t stream) {
-  const int64_t tiles = N / 16;
-  if (tiles >= 1024) return launch_tile<4, TT, S>(M, N, K, x, ld_x, qw, sw, out, stream);
-  if (tiles >= 768 && tiles % 3 == 0) return launch_tile<3, TT, S>(M, N, K, x, ld_x, qw, sw, out, stream);
-  if (tiles >= 512) return launch_tile<2, TT, S>(M, N, K, x, ld_x, qw, sw, out, stream);
-  return launch_tile<1, TT, S>(M, N, K, x, ld_x, qw, sw, out, stream);
+// The rows of x that one launch quantizes as it multiplies (kRawRows, in
+// fp8moe_launch.h): each workgroup takes 16 of them, and as many columns as
+// leave about one workgroup per CU.  Measured at 2048 reduction values, us as
+// a graph node (2.1 of which an empty one takes too), 1 / 2 / 3 / 4 tiles of
+// 16 columns: 1 row x 4096 4.3 / 4.7 / - / -; 16 x 12288 - / 9.3 / 7.7 / 8.0;
+// 64 x 4096 - / 6.6 / - / 5.9.
+template <int XL, class S>
+hipError_t launch_raw(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
+                      const float* sw, RowsOut out, hipStream_t stream) {
+  const int64_t tiles = N / 16, per_cu = tiles * ((M + 15) / 16) / 256;
+#define FP8_RAW(W, RT) launch<W, RT, 1, XL, 1, true, S>(M, N, K, x, ld_x * 2, nullptr, qw, sw, out, stream)
+  if (per_cu <= 1) return tiles * ((M + 15) / 16) <= 128 && K >= 4096 ? FP8_RAW(16, 1) : FP8_RAW(8, 1);
+  if (per_cu >= 4) return per_cu >= 8 ? FP8_RAW(4, 4) : FP8_RAW(8, 4);
+  if (per_cu == 3 && tiles % 3 == 0) return FP8_RAW(8, 3);
+  return FP8_RAW(8, 2);
+#undef FP8_RAW
 }
 
 template <class S>
 hipError_t launch_scale(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
-                        const float* sw, RowsOut out, hipStream_t stream) {
-  if (M <= 16) return launch_tokens<1, S>(M, N, K, x, ld_x, qw, sw, out, stream);
-  if (M <= 32) return launch_tokens<2, S>(M, N, K, x, ld_x, qw, sw, out, stream);
-  return launch_tokens<3, S>(M, N, K, x, ld_x, qw, sw, out, stream);
+                        const float* sw, RowsOut out, void* ws, hipStream_t stream) {
+  if (M <= kRawRows) {
+    if (M <= 4) return launch_raw<1, S>(M, N, K, x, ld_x, qw, sw, out, stream);
+    if (M <= 8) return launch_raw<2, S>(M, N, K, x, ld_x, qw, sw, out, stream);
+    return launch_raw<4, S>(M, N, K, x, ld_x, qw, sw, out, stream);
+  }
+  const int nkb = (int)(K / 128);
+  uint8_t* q = static_cast<uint8_t*>(ws);
+  float* s = reinterpret_cast<float*>(q + rows_scales_at(M, K));
+  hipLaunchKernelGGL(quantize_rows_kernel<S>, dim3((uint32_t)((M * nkb + 15) / 16)), dim3(256), 0, stream, M, nkb, x,
+                     ld_x, q, s);
+  if (hipError_t e = hipGetLastError()) return e;
+  // the largest tile that leaves most CUs a workgroup
+  const int64_t n64 = N / 64, m64 = (M + 63) / 64;
+#define FP8_CODES(W, RT, TT) launch<W, RT, TT, 2, 1, false, Pow2Scale>(M, N, K, q, K, s, qw, sw, out, stream)
+  if (n64 * m64 >= 384) return FP8_CODES(4, 4, 4);
+  if (n64 * m64 >= 192) return FP8_CODES(8, 4, 4);
+  if (2 * n64 * m64 >= 192) return FP8_CODES(8, 2, 4);
+  return 4 * n64 * m64 >= 192 ? FP8_CODES(8, 2, 2) : FP8_CODES(8, 1, 2);
+#undef FP8_CODES
 }
 
 }  // namespace
 
 hipError_t launch_linear_rows(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
-                              const float* sw, RowsOut out, bool fp32_scale, hipStream_t stream) {
-  return fp32_scale ? launch_scale<Fp32Scale>(M, N, K, x, ld_x, qw, sw, out, stream)
-                    : launch_scale<Pow2Scale>(M, N, K, x, ld_x, qw, sw, out, stream);
+                              const float* sw, RowsOut out, bool fp32_scale, void* ws, hipStream_t stream) {
+  return fp32_scale ? launch_scale<Fp32Scale>(M, N, K, x, ld_x, qw, sw, out, ws, stream)
+                    : launch_scale<Pow2Scale>(M, N, K, x, ld_x, qw, sw, out, ws, stream);
 }
 
 }  // namespace fp8blk
