@@ -17,11 +17,13 @@ constexpr int64_t kMaxStride = int64_t(1) << 26;
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // The rows that the GEMMs of fp8blk.h take: none where their 256x256 tiles
-// would leave most CUs idle, else the multiples of 128.  kGemmOutputs outputs are where
-// the two paths take the same time.
-constexpr int64_t kGemmOutputs = 3500000;
+// would leave most CUs idle, else the multiples of 128.  At K = 2048 the GEMM
+// takes 25 us for anything up to 256 tiles, after 3.5 for the quantizer; the
+// kernels for fewer rows take about 6.6 us per million outputs, and the GEMM's
+// remaining rows go through them too (about 8 us more).
 int64_t gemm_rows(int64_t M, int64_t N) {
-  return M <= FP8_LINEAR_FP32_ROWS || M * N <= kGemmOutputs ? 0 : M / kGroup * kGroup;
+  if (M <= FP8_LINEAR_FP32_ROWS || M * N <= (M % kGroup ? 4500000 : 3500000)) return 0;
+  return M / kGroup * kGroup;
 }
 // Their codes and scales in the workspace, in front of the other rows'.
 size_t codes_bytes(int64_t rows, int64_t K) { return up256((size_t)(rows * K)); }

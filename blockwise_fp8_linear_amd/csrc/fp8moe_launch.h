@@ -17,12 +17,17 @@ struct RowsOut {
 };
 
 // y = x W^T for M rows; x is quantized on the way (fp32_scale: amax / 448).
-// Above kRawRows rows through the workspace: codes, and from rows_scales_at on
-// their scales.
-constexpr int64_t kRawRows = 64;
+// Above raw_rows() rows through the workspace: codes, and from rows_scales_at
+// on their scales.  The limit is where quantizing once pays for its launch, at
+// 12288 x 2048: power-of-two scales 48 rows 11.8 and 11.6 us, 64 rows 13.7 and
+// 12.4; amax / 448 scales, whose quotients cost more, 16 x 2048 x 6144 15.2 and
+// 10.4, 8 rows 10.8 and 10.2.
+inline int64_t raw_rows(bool fp32_scale) { return fp32_scale ? 8 : 48; }
 inline size_t rows_scales_at(int64_t M, int64_t K) { return ((size_t)(M * K) + 255) & ~size_t(255); }
+// (whichever the scales, so that a caller need not say)
 inline size_t rows_workspace_bytes(int64_t M, int64_t K) {
-  return M <= kRawRows ? 0 : rows_scales_at(M, K) + (((size_t)(M * (K / 128)) * sizeof(float) + 255) & ~size_t(255));
+  return M <= raw_rows(true) ? 0
+                             : rows_scales_at(M, K) + (((size_t)(M * (K / 128)) * sizeof(float) + 255) & ~size_t(255));
 }
 hipError_t launch_linear_rows(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
                               const float* sw, RowsOut out, bool fp32_scale, void* ws, hipStream_t stream);

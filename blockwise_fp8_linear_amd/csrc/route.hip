@@ -65,9 +65,12 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(int64_t T, int
     gs[i] = 0.0f;
     chosen[i] = false;
   }
+  // lane j brings the j-th choice; the others get it from there
+  const int mine = lane < k ? ids[tt * k + lane] : -1;
+  const float gmine = lane < k ? g[tt * k + lane] : 0.0f;
   for (int j = 0; j < k; ++j) {
-    const int id = ids[tt * k + j];
-    const float gj = g[tt * k + j];
+    const int id = __shfl(mine, j, LANES);
+    const float gj = __shfl(gmine, j, LANES);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       if (id == lane + i * LANES && id < E && v[i] > -INFINITY) {

@@ -105,28 +105,55 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t M, int nkb, 
   if (l16 == 0) s[g * M + m] = sc.s;
 }
 
-// The rows of x that one launch quantizes as it multiplies (kRawRows, in
-// fp8moe_launch.h): each workgroup takes 16 of them, and as many columns as
-// leave about one workgroup per CU.  Measured at 2048 reduction values, us as
-// a graph node (2.1 of which an empty one takes too), 1 / 2 / 3 / 4 tiles of
-// 16 columns: 1 row x 4096 4.3 / 4.7 / - / -; 16 x 12288 - / 9.3 / 7.7 / 8.0;
-// 64 x 4096 - / 6.6 / - / 5.9.
+// Tiles are chosen so that a launch has about one workgroup of eight waves per
+// CU: a smaller tile loads the tokens more often, a larger one leaves CUs
+// idle.  Times below are us as a graph node at K = 2048 (an empty node takes
+// 2.1), power-of-two scales.
+
+// Up to raw_rows(): one launch that quantizes as it multiplies.  16 tokens per
+// workgroup (more rows per tile only pay at large N: 32 x 12288 9.7 with two
+// tiles of tokens, 10.3 with one).  1, 2, 3, 4 tiles of columns:
+//   16 x 4096   4.9  5.2   -    -       24 x 4096   6.1  5.2   -    -
+//   64 x 4096   -    6.7   -   6.3      16 x 12288  9.7  9.7  8.0  8.2
+//   24 x 12288  -   10.2 10.2   -  (four tiles: 1.5 rounds of one workgroup per CU, 13.4)
+// 16 waves for one tile: 16 x 4096 4.7 instead of 4.9, 16 x 2048 (K 6144) 9.2
+// instead of 10.1; a single row is no faster with them at K = 2048.
 template <int XL, class S>
 hipError_t launch_raw(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
                       const float* sw, RowsOut out, hipStream_t stream) {
-  const int64_t tiles = N / 16, per_cu = tiles * ((M + 15) / 16) / 256;
+  const int64_t tiles = N / 16, all = tiles * ((M + 15) / 16);
 #define FP8_RAW(W, RT) launch<W, RT, 1, XL, 1, true, S>(M, N, K, x, ld_x * 2, nullptr, qw, sw, out, stream)
-  if (per_cu <= 1) return tiles * ((M + 15) / 16) <= 128 && K >= 4096 ? FP8_RAW(16, 1) : FP8_RAW(8, 1);
-  if (per_cu >= 4) return per_cu >= 8 ? FP8_RAW(4, 4) : FP8_RAW(8, 4);
-  if (per_cu == 3 && tiles % 3 == 0) return FP8_RAW(8, 3);
-  return FP8_RAW(8, 2);
+  if (all <= 256) return XL > 1 || K >= 4096 ? FP8_RAW(16, 1) : FP8_RAW(8, 1);
+  if (all <= 512) return FP8_RAW(8, 2);
+  if (tiles % 3 == 0 && all <= 1536) return FP8_RAW(8, 3);
+  if (all <= 1024) return FP8_RAW(8, 4);
+  return tiles % 3 == 0 ? FP8_RAW(4, 3) : FP8_RAW(4, 2);
 #undef FP8_RAW
+}
+
+// More rows: x quantized once (2.2 us), then tiles of codes.  The smallest of
+// (tiles of columns, of tokens) (1, 1), (2, 1), (2, 2), (4, 2), (4, 4) that
+// has at most 256 workgroups: 24 x 4096 (2, 1) 4.1; 64 x 4096 (2, 2) 4.9 and
+// (4, 1) 5.1; 128 x 4096 (4, 2) 6.0 and (2, 2) 6.6; 256 x 4096 (4, 4) 8.2 and
+// (4, 2) 9.9.  Where all have more, smaller workgroups of (3, 2): 64 x 12288
+// 10.4 and (4, 4) 11.4; 256 x 12288 22.7 and (4, 4) 23.7.
+hipError_t launch_codes(int64_t M, int64_t N, int64_t K, const uint8_t* q, const float* s, const uint8_t* qw,
+                        const float* sw, RowsOut out, hipStream_t stream) {
+  const int64_t tiles = N / 16, m1 = (M + 15) / 16, m2 = (M + 31) / 32, m4 = (M + 63) / 64;
+#define FP8_CODES(W, RT, TT) launch<W, RT, TT, 2, 1, false, Pow2Scale>(M, N, K, q, K, s, qw, sw, out, stream)
+  if (tiles * m1 <= 256) return FP8_CODES(16, 1, 1);
+  if (tiles / 2 * m1 <= 256) return FP8_CODES(8, 2, 1);
+  if (tiles / 2 * m2 <= 256) return FP8_CODES(8, 2, 2);
+  if (tiles / 4 * m2 <= 256) return FP8_CODES(8, 4, 2);
+  if (tiles / 4 * m4 <= 256 && M > 64) return FP8_CODES(8, 4, 4);
+  return tiles % 3 == 0 ? FP8_CODES(4, 3, 2) : FP8_CODES(4, 4, 2);
+#undef FP8_CODES
 }
 
 template <class S>
 hipError_t launch_scale(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
-                        const float* sw, RowsOut out, void* ws, hipStream_t stream) {
-  if (M <= kRawRows) {
+                        const float* sw, RowsOut out, int64_t raw_rows, void* ws, hipStream_t stream) {
+  if (M <= raw_rows) {
     if (M <= 4) return launch_raw<1, S>(M, N, K, x, ld_x, qw, sw, out, stream);
     if (M <= 8) return launch_raw<2, S>(M, N, K, x, ld_x, qw, sw, out, stream);
     return launch_raw<4, S>(M, N, K, x, ld_x, qw, sw, out, stream);
@@ -137,22 +164,15 @@ hipError_t launch_scale(int64_t M, int64_t N, int64_t K, const uint16_t* x, int6
   hipLaunchKernelGGL(quantize_rows_kernel<S>, dim3((uint32_t)((M * nkb + 15) / 16)), dim3(256), 0, stream, M, nkb, x,
                      ld_x, q, s);
   if (hipError_t e = hipGetLastError()) return e;
-  // the largest tile that leaves most CUs a workgroup
-  const int64_t n64 = N / 64, m64 = (M + 63) / 64;
-#define FP8_CODES(W, RT, TT) launch<W, RT, TT, 2, 1, false, Pow2Scale>(M, N, K, q, K, s, qw, sw, out, stream)
-  if (n64 * m64 >= 384) return FP8_CODES(4, 4, 4);
-  if (n64 * m64 >= 192) return FP8_CODES(8, 4, 4);
-  if (2 * n64 * m64 >= 192) return FP8_CODES(8, 2, 4);
-  return 4 * n64 * m64 >= 192 ? FP8_CODES(8, 2, 2) : FP8_CODES(8, 1, 2);
-#undef FP8_CODES
+  return launch_codes(M, N, K, q, s, qw, sw, out, stream);
 }
 
 }  // namespace
 
 hipError_t launch_linear_rows(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
                               const float* sw, RowsOut out, bool fp32_scale, void* ws, hipStream_t stream) {
-  return fp32_scale ? launch_scale<Fp32Scale>(M, N, K, x, ld_x, qw, sw, out, ws, stream)
-                    : launch_scale<Pow2Scale>(M, N, K, x, ld_x, qw, sw, out, ws, stream);
+  return fp32_scale ? launch_scale<Fp32Scale>(M, N, K, x, ld_x, qw, sw, out, raw_rows(true), ws, stream)
+                    : launch_scale<Pow2Scale>(M, N, K, x, ld_x, qw, sw, out, raw_rows(false), ws, stream);
 }
 
 }  // namespace fp8blk

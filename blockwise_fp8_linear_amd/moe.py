@@ -56,46 +56,54 @@ def _functions():
     return lib
 
 
-def _device(x, name):
-    """The device a call runs on: its first operand's, which has to be the
-    current one (the library launches there)."""
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# torch's own raw-handle query where it has one: the public one builds a Stream
+# object, 2 us a call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _stream(stream, index):
+    return _raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _index(x, name):
+    """The device a call runs on, by number: its first operand's, which has to
+    be the current one (the library launches there)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    d = x.device
-    if d.type != "cuda":
+    index = x.get_device()
+    if index < 0:
         raise ValueError(f"{name}: must be a device tensor")
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {d}, but the library launches on the current device "
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {x.device}, but the library launches on the current device "
                          f"cuda:{torch.cuda.current_device()}")
-    return d
+    return index
 
 
-def _stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _new(shape, dtype, device, stream):
-    """torch.empty whose memory belongs to the stream the call launches on."""
+def _new(like, shape, dtype, stream):
+    """A new tensor on `like`'s device whose memory belongs to the stream the
+    call launches on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _fb._new(shape, dtype, device, stream)
+        return like.new_empty(shape, dtype=dtype)
+    return _fb._new(shape, dtype, like.device, stream)
 
 
-def _operand(t, dtype, shape, name, device, strided=False):
-    """Check one tensor: a device tensor of this dtype and shape, dense (or,
+def _operand(t, dtype, shape, name, index, strided=False):
+    """Check one tensor: on this device, of this dtype and shape, dense (or,
     `strided`, with a contiguous last dimension).  Returns its address."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, but the call runs on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, but the call runs on cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if strided:
-        if t.stride(-1) != 1:
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
     elif not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
@@ -106,39 +114,42 @@ def _matrix(x, dtypes, name):
     """The first operand: a matrix of one of these types, rows any distance
     apart.  Returns its device, sizes and row stride (a single row has none
     that matters)."""
-    device = _device(x, name)
+    index = _index(x, name)
     if x.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
     if x.dim() != 2:
         raise ValueError(f"{name}: expected 2 dims, got {x.dim()}")
     rows, cols = x.shape
-    if x.stride(1) != 1 and cols > 1:
+    down, right = x.stride()
+    if right != 1 and cols > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return device, rows, cols, x.stride(0) if rows > 1 else cols
+    return index, rows, cols, down if rows > 1 else cols
 
 
-def _result(out, shape, dtype, name, device, stream):
+def _result(out, like, shape, dtype, name, index, stream):
+    """(the output, new or the caller's, and its address)."""
     if out is None:
-        return _new(shape, dtype, device, stream)
-    _operand(out, dtype, shape, name, device)
-    return out
+        out = _new(like, shape, dtype, stream)
+        return out, out.data_ptr()
+    return out, _operand(out, dtype, shape, name, index)
 
 
-def _scratch(need, workspace, device, stream):
-    """(the workspace, to be kept until the call has been made, its address and size)."""
-    if need == 0:
+def _scratch(need, workspace, like, index, stream):
+    """(the workspace, to be kept until the call has been made, its address and
+    size); nothing where the shape needs none or is refused."""
+    if need == 0 or _invalid(need):
         return None, None, 0
     if workspace is None:
         # belongs to `stream`: freed when the call returns, its memory is
         # reused only by work queued behind the kernels that use it
-        workspace = _new((need,), torch.uint8, device, stream)
-    else:
-        if not isinstance(workspace, torch.Tensor):
-            raise TypeError("workspace: expected a torch.Tensor")
-        if workspace.device != device:
-            raise ValueError(f"workspace: on {workspace.device}, but the call runs on {device}")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace: must be contiguous")
+        workspace = _new(like, (need,), torch.uint8, stream)
+        return workspace, workspace.data_ptr(), need
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
+    if workspace.get_device() != index:
+        raise ValueError(f"workspace: on {workspace.device}, but the call runs on cuda:{index}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -160,23 +171,23 @@ def fp8_linear(x, qw, sw, out_dtype=None, out=None, workspace=None, stream=None,
     or fp32.  x is quantized on the way by scale_mode's rule, the one that made
     sw.  accumulate: out += result in fp32 (out_dtype float32, `out` given)."""
     bf16 = torch.bfloat16
-    device, M, K, ld = _matrix(x, (bf16,), "x")
+    index, M, K, ld = _matrix(x, (bf16,), "x")
     if not isinstance(qw, torch.Tensor) or qw.dim() != 2:
         raise ValueError("qw: expected a 2-dim tensor")
     N = qw.shape[0]
-    pqw = _operand(qw, torch.uint8, (N, K), "qw", device)
-    psw = _operand(sw, torch.float32, (N // 128, K // 128), "sw", device)
+    pqw = _operand(qw, torch.uint8, (N, K), "qw", index)
+    psw = _operand(sw, torch.float32, (N // 128, K // 128), "sw", index)
     odt = _fb.FP8BLK_OUT_BF16
     if out_dtype is None:
         out_dtype = bf16
     if accumulate or out_dtype is not bf16:
         odt = _fb._odt(out_dtype, accumulate, out)
     lib = _functions()
-    need = lib.fp8_linear_workspace_size(M, N, K)
-    keep, ws, size = (None, None, 0) if _invalid(need) else _scratch(need, workspace, device, stream)
-    y = _result(out, (M, N), out_dtype, "out", device, stream)
-    _fb._check(lib.fp8_linear(M, N, K, x.data_ptr(), ld, pqw, psw, y.data_ptr(), odt, scale_mode, ws, size,
-                              _stream(stream, device)))
+    keep, ws, size = _scratch(lib.fp8_linear_workspace_size(M, N, K), workspace, x, index, stream)
+    y, py = _result(out, x, (M, N), out_dtype, "out", index, stream)
+    rc = lib.fp8_linear(M, N, K, x.data_ptr(), ld, pqw, psw, py, odt, scale_mode, ws, size, _stream(stream, index))
+    if rc:
+        _fb._check(rc)
     return y
 
 
@@ -192,13 +203,14 @@ def fp8_moe_route(logits, topk, renormalize=True, ids=None, weights=None, stream
     softmax weights -- over the chosen ones (renormalize) or over all.  Experts
     whose logit is -inf or NaN are masked out; where fewer than topk are left
     the rest of the row is id -1, weight 0."""
-    device, T, E, ld = _matrix(logits, _LOGITS, "logits")
-    ids = _result(ids, (T, topk), torch.int32, "ids", device, stream)
-    weights = _result(weights, (T, topk), torch.float32, "weights", device, stream)
-    _fb._check(_functions().fp8_moe_route(T, E, topk, logits.data_ptr(),
-                                          FP8MOE_FP32 if logits.dtype is torch.float32 else FP8MOE_BF16, ld,
-                                          int(bool(renormalize)), ids.data_ptr(), weights.data_ptr(),
-                                          _stream(stream, device)))
+    index, T, E, ld = _matrix(logits, _LOGITS, "logits")
+    ids, pids = _result(ids, logits, (T, topk), torch.int32, "ids", index, stream)
+    weights, pw = _result(weights, logits, (T, topk), torch.float32, "weights", index, stream)
+    rc = _functions().fp8_moe_route(T, E, topk, logits.data_ptr(),
+                                    FP8MOE_FP32 if logits.dtype is torch.float32 else FP8MOE_BF16, ld,
+                                    1 if renormalize else 0, pids, pw, _stream(stream, index))
+    if rc:
+        _fb._check(rc)
     return ids, weights
 
 
@@ -206,20 +218,24 @@ def fp8_moe_route_backward(logits, ids, dweights, renormalize=True, dlogits=None
     """Gradient of fp8_moe_route's weights: logits and ids as it took and gave
     them, dweights fp32 [T,topk] -> dlogits [T,E] in the logits' type (or into
     `dlogits`, whose row stride may exceed E)."""
-    device, T, E, ld = _matrix(logits, _LOGITS, "logits")
+    index, T, E, ld = _matrix(logits, _LOGITS, "logits")
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids: expected a 2-dim tensor")
     k = ids.shape[1]
-    pids = _operand(ids, torch.int32, (T, k), "ids", device)
-    pg = _operand(dweights, torch.float32, (T, k), "dweights", device)
+    pids = _operand(ids, torch.int32, (T, k), "ids", index)
+    pg = _operand(dweights, torch.float32, (T, k), "dweights", index)
+    dtype = logits.dtype
     if dlogits is None:
-        dlogits = _new((T, E), logits.dtype, device, stream)
+        dlogits, ld_d = _new(logits, (T, E), dtype, stream), E
     else:
-        _operand(dlogits, logits.dtype, (T, E), "dlogits", device, strided=True)
-    _fb._check(_functions().fp8_moe_route_backward(T, E, k, logits.data_ptr(),
-                                                   FP8MOE_FP32 if logits.dtype is torch.float32 else FP8MOE_BF16, ld,
-                                                   pids, pg, int(bool(renormalize)), dlogits.data_ptr(),
-                                                   dlogits.stride(0) if T > 1 else E, _stream(stream, device)))
+        _operand(dlogits, dtype, (T, E), "dlogits", index, strided=True)
+        ld_d = dlogits.stride(0) if T > 1 else E
+    rc = _functions().fp8_moe_route_backward(T, E, k, logits.data_ptr(),
+                                             FP8MOE_FP32 if dtype is torch.float32 else FP8MOE_BF16, ld, pids, pg,
+                                             1 if renormalize else 0, dlogits.data_ptr(), ld_d,
+                                             _stream(stream, index))
+    if rc:
+        _fb._check(rc)
     return dlogits
 
 
@@ -229,23 +245,15 @@ def fp8_moe_workspace_size(T: int, H: int, I: int, E: int, topk: int) -> int:
     return int(_functions().fp8_moe_workspace_size(T, H, I, E, topk))
 
 
-def _experts(qw1, sw1, qw2, sw2, H, device):
+def _experts(qw1, sw1, qw2, sw2, H, index):
     """(E, I, the four addresses) of the experts' weights for a hidden size H."""
     if not isinstance(qw1, torch.Tensor) or qw1.dim() != 3 or qw1.shape[1] % 2:
         raise ValueError("qw1: expected a 3-dim tensor [E, 2 I, H]")
     E, I = qw1.shape[0], qw1.shape[1] // 2
-    return (E, I, _operand(qw1, torch.uint8, (E, 2 * I, H), "qw1", device),
-            _operand(sw1, torch.float32, (E, 2 * I // 128, H // 128), "sw1", device),
-            _operand(qw2, torch.uint8, (E, H, I), "qw2", device),
-            _operand(sw2, torch.float32, (E, H // 128, I // 128), "sw2", device))
-
-
-def _moe_out(T, H, I, E, k, out_dtype, out, workspace, device, stream):
-    """(output, its type code, workspace to keep, its address and size)."""
-    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    need = _functions().fp8_moe_workspace_size(T, H, I, E, k)
-    keep, ws, size = (None, None, 0) if _invalid(need) else _scratch(need, workspace, device, stream)
-    return _result(out, (T, H), out_dtype, "out", device, stream), _fb._odt(out_dtype), keep, ws, size
+    return (E, I, _operand(qw1, torch.uint8, (E, 2 * I, H), "qw1", index),
+            _operand(sw1, torch.float32, (E, 2 * I // 128, H // 128), "sw1", index),
+            _operand(qw2, torch.uint8, (E, H, I), "qw2", index),
+            _operand(sw2, torch.float32, (E, H // 128, I // 128), "sw2", index))
 
 
 def fp8_moe_experts(x, ids, weights, qw1, sw1, qw2, sw2, out_dtype=None, out=None, workspace=None, stream=None,
@@ -258,16 +266,22 @@ def fp8_moe_experts(x, ids, weights, qw1, sw1, qw2, sw2, out_dtype=None, out=Non
     [E,H/128,I/128], each as fp8_quantize_block quantizes the stacked matrix
     -> y [T,H] bf16 or fp32.  Activations are quantized by scale_mode's rule,
     the one that made the weights' scales."""
-    device, T, H, ld = _matrix(x, (torch.bfloat16,), "x")
-    E, I, pq1, ps1, pq2, ps2 = _experts(qw1, sw1, qw2, sw2, H, device)
+    index, T, H, ld = _matrix(x, (torch.bfloat16,), "x")
+    E, I, pq1, ps1, pq2, ps2 = _experts(qw1, sw1, qw2, sw2, H, index)
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids: expected a 2-dim tensor")
     k = ids.shape[1]
-    pids = _operand(ids, torch.int32, (T, k), "ids", device)
-    pw = _operand(weights, torch.float32, (T, k), "weights", device)
-    y, odt, keep, ws, size = _moe_out(T, H, I, E, k, out_dtype, out, workspace, device, stream)
-    _fb._check(_functions().fp8_moe_experts(T, H, I, E, k, x.data_ptr(), ld, pids, pw, pq1, ps1, pq2, ps2,
-                                            y.data_ptr(), odt, scale_mode, ws, size, _stream(stream, device)))
+    pids = _operand(ids, torch.int32, (T, k), "ids", index)
+    pw = _operand(weights, torch.float32, (T, k), "weights", index)
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    odt = _fb._odt(out_dtype)
+    lib = _functions()
+    keep, ws, size = _scratch(lib.fp8_moe_workspace_size(T, H, I, E, k), workspace, x, index, stream)
+    y, py = _result(out, x, (T, H), out_dtype, "out", index, stream)
+    rc = lib.fp8_moe_experts(T, H, I, E, k, x.data_ptr(), ld, pids, pw, pq1, ps1, pq2, ps2, py, odt, scale_mode, ws,
+                             size, _stream(stream, index))
+    if rc:
+        _fb._check(rc)
     return y
 
 
@@ -277,13 +291,18 @@ def fp8_moe_layer(x, wr, qw1, sw1, qw2, sw2, topk, renormalize=True, out_dtype=N
     (wr bf16 [E,H]), fp8_moe_route's choice of topk experts, fp8_moe_experts of
     it.  `ids` (int32) and `weights` (fp32) [T,topk], where given, get the
     choice."""
-    device, T, H, ld = _matrix(x, (torch.bfloat16,), "x")
-    E, I, pq1, ps1, pq2, ps2 = _experts(qw1, sw1, qw2, sw2, H, device)
-    pwr = _operand(wr, torch.bfloat16, (E, H), "wr", device)
-    pids = None if ids is None else _operand(ids, torch.int32, (T, topk), "ids", device)
-    pw = None if weights is None else _operand(weights, torch.float32, (T, topk), "weights", device)
-    y, odt, keep, ws, size = _moe_out(T, H, I, E, topk, out_dtype, out, workspace, device, stream)
-    _fb._check(_functions().fp8_moe_layer(T, H, I, E, topk, int(bool(renormalize)), x.data_ptr(), ld, pwr, pq1, ps1,
-                                          pq2, ps2, y.data_ptr(), odt, scale_mode, pids, pw, ws, size,
-                                          _stream(stream, device)))
+    index, T, H, ld = _matrix(x, (torch.bfloat16,), "x")
+    E, I, pq1, ps1, pq2, ps2 = _experts(qw1, sw1, qw2, sw2, H, index)
+    pwr = _operand(wr, torch.bfloat16, (E, H), "wr", index)
+    pids = None if ids is None else _operand(ids, torch.int32, (T, topk), "ids", index)
+    pw = None if weights is None else _operand(weights, torch.float32, (T, topk), "weights", index)
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    odt = _fb._odt(out_dtype)
+    lib = _functions()
+    keep, ws, size = _scratch(lib.fp8_moe_workspace_size(T, H, I, E, topk), workspace, x, index, stream)
+    y, py = _result(out, x, (T, H), out_dtype, "out", index, stream)
+    rc = lib.fp8_moe_layer(T, H, I, E, topk, 1 if renormalize else 0, x.data_ptr(), ld, pwr, pq1, ps1, pq2, ps2, py,
+                           odt, scale_mode, pids, pw, ws, size, _stream(stream, index))
+    if rc:
+        _fb._check(rc)
     return y

@@ -42,7 +42,7 @@ enum fp8moe_dtype { FP8MOE_BF16 = 0, FP8MOE_FP32 = 1 };
  *   scale_mode: the rule that made sw, and the rule x is quantized by.
  *   N, K positive multiples of 128; x, qw, y 16-byte aligned.
  *   workspace: at least fp8_linear_workspace_size(M, N, K) bytes, 16-byte
- *     aligned; may be NULL when that size is 0 (it is for small M).
+ *     aligned; may be NULL when that size is 0 (it is up to 8 rows).
  * Up to FP8_LINEAR_FP32_ROWS rows the call is bound by reading the weights; it
  * quantizes x on the way and sums the products with fp32 faithfulness.  Above,
  * x is quantized into the workspace first and the multiples of 128 rows go
