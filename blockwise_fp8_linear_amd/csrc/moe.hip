@@ -85,23 +85,38 @@ __global__ __launch_bounds__(256) void prepare_kernel(MoeArgs a, const float* __
 }
 
 // The rows t k + j (j-th choice of token t) that chose expert e, in order, into
-// `list`; their number.  Every thread of the workgroup calls it.
+// `list`; their number.  Every thread of a workgroup of 512
+// calls it.
 __device__ __forceinline__ int rows_of_expert(const int32_t* __restrict__ ids, int n, int e, uint16_t* list,
                                               int* scratch) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  constexpr int N = 4;  // places per thread and round, loaded together
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int found = 0;
-  for (int s0 = 0; s0 < n; s0 += blockDim.x) {
-    const int s = s0 + threadIdx.x;
-    const bool hit = s < n && ids[s] == e;
-    const uint64_t mask = __ballot(hit);
-    if (lane == 0) scratch[wave] = __popcll(mask);
-    __syncthreads();
-    int before = found;
-    for (int w = 0; w < waves; ++w) {
-      if (w < wave) before += scratch[w];
-      found += scratch[w];
+  for (int s0 = 0; s0 < n; s0 += 512 * N) {
+    uint64_t mask[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int s = s0 + i * 512 + threadIdx.x;
+      mask[i] = __ballot(ids[min(s, n - 1)] == e && s < n);
     }
-    if (hit) list[before + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)s;
+    if (lane < N) {
+      int count = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) count = lane == i ? __popcll(mask[i]) : count;
+      scratch[lane * 8 + wave] = count;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      int before = found;
+      for (int w = 0; w < 8; ++w) {
+        const int count = scratch[i * 8 + w];
+        before += w < wave ? count : 0;
+        found += count;
+      }
+      if ((mask[i] >> lane) & 1)
+        list[before + __popcll(mask[i] & ((1ull << lane) - 1))] = (uint16_t)(s0 + i * 512 + threadIdx.x);
+    }
     __syncthreads();
   }
   return found;
@@ -363,21 +378,20 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(MoeArgs a, const float* 
 // through the caches.  128 columns of I in one workgroup are one group of h,
 // so h leaves quantized.
 // ---------------------------------------------------------------------------
-template <int TT>
 constexpr int kSlots = 2;
 // Dynamic LDS: the ring for the most tiles, then the list of rows.
 constexpr int kMostRows = 8192;  // T k
-template <int TMAX>
-constexpr int kRing = rows_ring_bytes<2, TMAX, kSlots<TMAX>>();
+template <int RT, int TMAX>
+constexpr int kRing = rows_ring_bytes<RT, TMAX, kSlots>();
 
 template <int TMAX, class S>
 __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint8_t* __restrict__ qx,
                                                            const float* __restrict__ sx, uint8_t* __restrict__ qh,
                                                            float* __restrict__ sh) {
   extern __shared__ uint8_t lds[];
-  __shared__ int scratch[8];
+  __shared__ int scratch[4 * 8];
   __shared__ uint32_t amax[8][16 * TMAX];
-  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<TMAX>);
+  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<2, TMAX>);
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = blockIdx.y, n0 = blockIdx.x * 128 + wave * 16, nkb = a.H / 128;
@@ -395,7 +409,7 @@ __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint
       v4f acc[2][TT];
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) acc[0][tt] = acc[1][tt] = v4f{};
-      rows_ring<2, TT, kSlots<TMAX>>(
+      rows_ring<2, TT, kSlots>(
           lds, wp, sp, a.H, qx, xoff,
           [&](int i, int b) { return sx[(int64_t)b * a.T + list[min(r0 + i, rows - 1)] / a.k]; }, nkb, acc);
       uint32_t h[TT][2];
@@ -426,32 +440,39 @@ __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint
   }
 }
 
-template <int TMAX>
+template <int RT, int TMAX>
 __global__ __launch_bounds__(512) void down_wide_kernel(MoeArgs a, const uint8_t* __restrict__ qh,
                                                         const float* __restrict__ sh, float* __restrict__ partial) {
   extern __shared__ uint8_t lds[];
-  __shared__ int scratch[8];
-  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<TMAX>);
+  __shared__ int scratch[4 * 8];
+  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<RT, TMAX>);
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int e = blockIdx.y, n0 = (blockIdx.x * 8 + wave) * 32, nkb = a.I / 128;
+  const int e = blockIdx.y, n0 = (blockIdx.x * 8 + wave) * 16 * RT, nkb = a.I / 128;
   // waves past the last column (H may be an odd number of 128s) repeat it: they pass the barriers and store nothing
-  const int n = min(n0, a.H - 32);
+  const int n = min(n0, a.H - 16 * RT);
   const int rows = rows_of_expert(a.ids, a.T * a.k, e, list, scratch);
 
   const uint8_t* base = a.qw2 + ((int64_t)e * a.H + n) * a.I;
   const float* s = a.sw2 + ((int64_t)e * (a.H / 128) + n / 128) * nkb;
-  const uint8_t* const wp[2] = {base, base + (int64_t)16 * a.I};
-  const float* const sp[2] = {s, s};
+  const uint8_t* wp[RT];
+  const float* sp[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    wp[rt] = base + (int64_t)rt * 16 * a.I;
+    sp[rt] = s;
+  }
   for (int r0 = 0; r0 < rows; r0 += 16 * TMAX) {
     with_tiles<TMAX>(rows - r0, [&](auto tag) {
       constexpr int TT = decltype(tag)::value;
       const int load = wave % (2 * TT), row = r0 + (load >> 1) * 16 + code_row(lane, load & 1);
       const uint32_t xoff = (uint32_t)list[min(row, rows - 1)] * a.I + code_chunk(lane, load & 1);
-      v4f acc[2][TT];
+      v4f acc[RT][TT];
 #pragma unroll
-      for (int tt = 0; tt < TT; ++tt) acc[0][tt] = acc[1][tt] = v4f{};
-      rows_ring<2, TT, kSlots<TMAX>>(
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = v4f{};
+      rows_ring<RT, TT, kSlots>(
           lds, wp, sp, a.I, qh, xoff,
           [&](int i, int b) { return sh[(int64_t)b * (a.T * a.k) + list[min(r0 + i, rows - 1)]]; }, nkb, acc);
 #pragma unroll
@@ -461,7 +482,7 @@ __global__ __launch_bounds__(512) void down_wide_kernel(MoeArgs a, const uint8_t
           const int64_t s = list[row];
           const float w = a.weights[s];
 #pragma unroll
-          for (int rt = 0; rt < 2; ++rt)
+          for (int rt = 0; rt < RT; ++rt)
             *reinterpret_cast<v4f*>(partial + s * a.H + n0 + rt * 16 + 4 * c) = acc[rt][tt] * w;
         }
       }
@@ -476,9 +497,15 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, const float* __
   const int t = u / per, n = (u - t * per) * 4;
   if (t >= a.T) return;
   v4f v{};
-  for (int j = 0; j < a.k; ++j) {
-    const int s = t * a.k + j, id = a.ids[s];
-    if (id >= 0 && id < a.E) v += *reinterpret_cast<const v4f*>(partial + (int64_t)s * a.H + n);
+  for (int j0 = 0; j0 < a.k; j0 += 4) {  // the terms of four choices are loaded together
+    v4f term[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int s = t * a.k + min(j0 + j, a.k - 1), id = a.ids[s];
+      term[j] = j0 + j < a.k && id >= 0 && id < a.E ? *reinterpret_cast<const v4f*>(partial + (int64_t)s * a.H + n) : v4f{};
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v += term[j];
   }
   store4(a.out, (int64_t)t * a.H + n, v);
 }
@@ -493,7 +520,7 @@ struct MoeBuffers {
 // `reached`: about how many experts the tokens reach.
 template <int XL, bool RAW, class S>
 hipError_t down_few(const MoeArgs& a, const MoeBuffers& b, double reached, hipStream_t stream) {
-  constexpr int W = XL == 1 && RAW ? 16 : 8, D = RAW ? 2 : 1, lds = W * D * rows_stage_bytes<1, 1, RAW, XL>();
+  constexpr int W = RAW && XL <= 2 ? 16 : 8, D = RAW && XL != 2 ? 2 : 1, lds = W * D * rows_stage_bytes<1, 1, RAW, XL>();
   static_assert(lds >= W * 1024, "the waves' sums fit");
   static std::atomic<uint64_t> raised{0};
   const auto k = &down_few_kernel<W, XL, D, RAW, S>;
@@ -525,8 +552,9 @@ template <int TT, class S>
 hipError_t gate_up_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
   static std::atomic<uint64_t> raised{0};
   const auto k = &gate_up_wide_kernel<TT, S>;
-  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), kRing<TT> + kMostRows * 2, &raised)) return e;
-  hipLaunchKernelGGL(k, dim3(a.I / 128, a.E), dim3(512), kRing<TT> + a.T * a.k * 2, stream, a, b.qx, b.sx, b.h, b.sh);
+  constexpr int ring = kRing<2, TT>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), ring + kMostRows * 2, &raised)) return e;
+  hipLaunchKernelGGL(k, dim3(a.I / 128, a.E), dim3(512), ring + a.T * a.k * 2, stream, a, b.qx, b.sx, b.h, b.sh);
   return hipGetLastError();
 }
 
@@ -534,10 +562,11 @@ template <int TT, class S>
 hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
   if (hipError_t e = gate_up_wide<TT, S>(a, b, stream)) return e;
   static std::atomic<uint64_t> raised{0};
-  const auto k = &down_wide_kernel<TT>;
-  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), kRing<TT> + kMostRows * 2, &raised)) return e;
-  hipLaunchKernelGGL(k, dim3((a.H + 255) / 256, a.E), dim3(512), kRing<TT> + a.T * a.k * 2, stream, a, b.h, b.sh,
-                     b.partial);
+  constexpr int RT = TT == 1 ? 2 : 1, ring = kRing<RT, TT>;
+  const auto k = &down_wide_kernel<RT, TT>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), ring + kMostRows * 2, &raised)) return e;
+  hipLaunchKernelGGL(k, dim3((a.H + 128 * RT - 1) / (128 * RT), a.E), dim3(512), ring + a.T * a.k * 2, stream, a, b.h,
+                     b.sh, b.partial);
   if (hipError_t e = hipGetLastError()) return e;
   hipLaunchKernelGGL(combine_kernel, dim3((a.T * (a.H / 4) + 255) / 256), dim3(256), 0, stream, a, b.partial);
   return hipGetLastError();
@@ -549,7 +578,7 @@ hipError_t moe(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
   double missed = 1.0;
   for (int t = 0; t < a.T; ++t) missed *= 1.0 - (double)a.k / a.E;
   const double reached = a.E * (1.0 - missed);
-  if (a.T <= 8 || (a.T <= kFew && reached * (a.I / 128) < 192)) {
+  if (a.T <= (a.fp32_scale ? 4 : 8) || (a.T <= kFew && reached * (a.I / 128) < 192)) {
     if (a.T <= 4) return moe_few<1, S>(a, b, reached, stream);
     return a.T <= 8 ? moe_few<2, S>(a, b, reached, stream) : moe_few<4, S>(a, b, reached, stream);
   }
