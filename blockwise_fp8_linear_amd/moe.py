@@ -11,6 +11,7 @@ function and the stream is taken as a raw handle.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -28,6 +29,7 @@ FP8MOE_MAX_TOPK = 16
 FP8MOE_MAX_TOKENS = 512
 
 _FUNCTIONS = None
+_REFUSED = ctypes.c_size_t(-1).value
 
 
 def _functions():
@@ -86,9 +88,10 @@ def _index(x, name):
 def _new(like, shape, dtype, stream):
     """A new tensor on `like`'s device whose memory belongs to the stream the
     call launches on."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    return _fb._new(shape, dtype, like.device, stream)
+    if stream is not None:
+        return _fb._new(shape, dtype, like.device, stream)
+    # dense; the strided form of torch.empty takes the least time of them
+    return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=like.device)
 
 
 def _operand(t, dtype, shape, name, index, strided=False):
@@ -153,9 +156,19 @@ def _scratch(need, workspace, like, index, stream):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+@functools.lru_cache(maxsize=4096)
+def _linear_need(M, N, K):
+    return _functions().fp8_linear_workspace_size(M, N, K)
+
+
+@functools.lru_cache(maxsize=4096)
+def _moe_need(T, H, I, E, k):
+    return _functions().fp8_moe_workspace_size(T, H, I, E, k)
+
+
 def _invalid(need):
     """Whether a workspace query refused the shape (the call then says why)."""
-    return need == ctypes.c_size_t(-1).value
+    return need == _REFUSED
 
 
 # ------------------------------------------------------------------- linear --
@@ -183,7 +196,7 @@ def fp8_linear(x, qw, sw, out_dtype=None, out=None, workspace=None, stream=None,
     if accumulate or out_dtype is not bf16:
         odt = _fb._odt(out_dtype, accumulate, out)
     lib = _functions()
-    keep, ws, size = _scratch(lib.fp8_linear_workspace_size(M, N, K), workspace, x, index, stream)
+    keep, ws, size = _scratch(_linear_need(M, N, K), workspace, x, index, stream)
     y, py = _result(out, x, (M, N), out_dtype, "out", index, stream)
     rc = lib.fp8_linear(M, N, K, x.data_ptr(), ld, pqw, psw, py, odt, scale_mode, ws, size, _stream(stream, index))
     if rc:
@@ -276,7 +289,7 @@ def fp8_moe_experts(x, ids, weights, qw1, sw1, qw2, sw2, out_dtype=None, out=Non
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     odt = _fb._odt(out_dtype)
     lib = _functions()
-    keep, ws, size = _scratch(lib.fp8_moe_workspace_size(T, H, I, E, k), workspace, x, index, stream)
+    keep, ws, size = _scratch(_moe_need(T, H, I, E, k), workspace, x, index, stream)
     y, py = _result(out, x, (T, H), out_dtype, "out", index, stream)
     rc = lib.fp8_moe_experts(T, H, I, E, k, x.data_ptr(), ld, pids, pw, pq1, ps1, pq2, ps2, py, odt, scale_mode, ws,
                              size, _stream(stream, index))
@@ -299,7 +312,7 @@ def fp8_moe_layer(x, wr, qw1, sw1, qw2, sw2, topk, renormalize=True, out_dtype=N
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     odt = _fb._odt(out_dtype)
     lib = _functions()
-    keep, ws, size = _scratch(lib.fp8_moe_workspace_size(T, H, I, E, topk), workspace, x, index, stream)
+    keep, ws, size = _scratch(_moe_need(T, H, I, E, topk), workspace, x, index, stream)
     y, py = _result(out, x, (T, H), out_dtype, "out", index, stream)
     rc = lib.fp8_moe_layer(T, H, I, E, topk, 1 if renormalize else 0, x.data_ptr(), ld, pwr, pq1, ps1, pq2, ps2, py,
                            odt, scale_mode, pids, pw, ws, size, _stream(stream, index))

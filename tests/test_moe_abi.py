@@ -209,6 +209,8 @@ class NoLibrary:
 @pytest.fixture
 def host_stand_ins(monkeypatch):
     monkeypatch.setattr(moe, "_functions", NoLibrary)
+    monkeypatch.setattr(moe, "_linear_need", lambda *a: 64)
+    monkeypatch.setattr(moe, "_moe_need", lambda *a: 64)
     monkeypatch.setattr(moe, "_index", lambda x, name: -1 if isinstance(x, torch.Tensor) else pytest.fail(name))
     monkeypatch.setattr(moe, "_raw_stream", lambda index: 0)
 
