@@ -11,7 +11,8 @@ using namespace fp8blk;
 
 namespace {
 
-// The kernels hold the offset of a row within 16 of them in 32 bits.
+// The kernels hold byte offsets from a wave's base in 31 bits: of a row among 16
+// of x, among 64 of its codes, among all T k rows of h.
 constexpr int64_t kMaxStride = int64_t(1) << 26;
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -36,7 +37,7 @@ size_t linear_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 bool linear_limits(int64_t M, int64_t N, int64_t K) {
-  return N / kGroup < (1 << 20) && K / kGroup < (1 << 19) && M < (int64_t(1) << 27) && prod_le(M, N, kMaxElems) &&
+  return N / kGroup < (1 << 20) && K / kGroup < (1 << 18) && M < (int64_t(1) << 27) && prod_le(M, N, kMaxElems) &&
          prod_le(M, K, kMaxElems) && prod_le(N, K, kMaxElems) && prod_lt(M, K / kGroup, int64_t(1) << 31);
 }
 
@@ -56,7 +57,7 @@ int check_route(int64_t T, int64_t E, int k, const void* logits, int dtype, int6
 int check_moe_shape(int64_t T, int64_t H, int64_t I, int64_t E, int k) {
   if (T <= 0 || E <= 0 || k <= 0 || !mult128(H) || !mult128(I)) return FP8BLK_ERR_DIM;
   if (T > FP8MOE_MAX_TOKENS || E > FP8MOE_MAX_EXPERTS || k > FP8MOE_MAX_TOPK || k > E || H > (1 << 20) ||
-      I > (1 << 20) || !prod_le(H, I, kMaxElems / (2 * FP8MOE_MAX_EXPERTS)) || !prod_lt(T * k, I, int64_t(1) << 32))
+      I > (1 << 20) || !prod_le(H, I, kMaxElems / (2 * FP8MOE_MAX_EXPERTS)) || !prod_lt(T * k, I, int64_t(1) << 31))
     return FP8BLK_ERR_ARG;
   return FP8BLK_OK;
 }

@@ -158,7 +158,8 @@ def _case(T, H, I, E, k, seed, mode, ids=None):
 
 EXPERTS = [(1, 256, 128, 4, 2), (1, 128, 384, 16, 16), (2, 384, 256, 3, 3), (15, 256, 128, 5, 2), (16, 128, 128, 8, 4),
            (17, 256, 256, 4, 1), (31, 128, 128, 2, 2), (33, 384, 128, 6, 3), (64, 256, 384, 3, 2), (65, 128, 128, 1, 1),
-           (130, 256, 128, 2, 1), (200, 128, 256, 40, 5), (512, 128, 128, 3, 2)]
+           (130, 256, 128, 2, 1), (200, 128, 256, 40, 5), (512, 128, 128, 3, 2),
+           (20, 384, 128, 40, 2), (20, 128, 256, 64, 4), (12, 128, 512, 64, 8), (6, 128, 768, 64, 8), (40, 128, 128, 1024, 16)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", EXPERTS)
@@ -214,6 +215,18 @@ def _exact_case(T, E, k, seed, H=256, I=256):
 def test_experts_exact(T, E, k):
     import torch
     args, y = _exact_case(T, E, k, T)
+    assert np.array_equal(host(fb.fp8_moe_experts(*args, out_dtype=torch.float32)).astype(np.float64), y)
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(8, 4096, 512, 32, 8), (3, 8960, 256, 3, 2), (3, 256, 8448, 3, 2),
+                                       (20, 8960, 256, 5, 2), (20, 256, 8448, 5, 2), (20, 384, 8448, 3, 3),
+                                       (14, 256, 8448, 4, 2), (70, 8448, 128, 2, 1)])
+def test_experts_exact_long(T, H, I, E, k):
+    """Reductions longer than the scales that are kept at a time, and long
+    enough for several workgroups to share a column."""
+    import torch
+    args, y = _exact_case(T, E, k, 500 + T, H, I)
+    assert np.abs(y).max() < 2 ** 24
     assert np.array_equal(host(fb.fp8_moe_experts(*args, out_dtype=torch.float32)).astype(np.float64), y)
 
 

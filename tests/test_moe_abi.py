@@ -63,7 +63,7 @@ def test_linear_errors(lib):
         assert call(odt=odt) in NOGPU
     assert call(mode=1) in NOGPU
     for kw in ({"odt": 3}, {"odt": -1}, {"mode": 2}, {"mode": -1}, {"ld": 256}, {"ld": 1 << 27},
-               {"K": 128 << 19, "ld": 128 << 19}, {"M": 1 << 27}, {"N": 1 << 30, "M": 1 << 20}):
+               {"K": 128 << 18, "ld": 128 << 18}, {"M": 1 << 27}, {"N": 1 << 30, "M": 1 << 20}):
         assert call(**kw) == EARG, kw
     for n in ("x", "qw", "sw", "y"):
         assert call(**{n: None}) == ENULL, n
@@ -81,7 +81,7 @@ def test_linear_errors(lib):
 def test_linear_workspace(lib):
     q = lib.fp8_linear_workspace_size
     assert q(1, 128, 128) == 0 and q(8, 12288, 2048) == 0
-    for bad in ((0, 128, 128), (1, 100, 128), (1, 128, 100), (1 << 27, 128, 128), (1, 128, 128 << 19), (1 << 62, 128, 128)):
+    for bad in ((0, 128, 128), (1, 100, 128), (1, 128, 100), (1 << 27, 128, 128), (1, 128, 128 << 18), (1 << 62, 128, 128)):
         assert q(*bad) == BAD, bad
     # codes and scales of every row that is quantized first, whichever kernel takes it
     for M, N, K in ((49, 128, 128), (127, 256, 640), (333, 2048, 2048), (4133, 4096, 2048), (1100, 4096, 128)):
@@ -124,7 +124,7 @@ def test_moe_errors(lib):
     assert call() in NOGPU and call(odt=1, mode=1, re=0, ids=P[8], w=P[9], ld=264) in NOGPU
     for kw in ({"odt": 2}, {"odt": 5}, {"mode": 3}, {"re": -1}, {"T": 513}, {"E": 1025}, {"k": 9}, {"E": 64, "k": 17},
                {"ld": 248}, {"ld": 1 << 27}, {"H": 1 << 21, "ld": 1 << 21}, {"I": 1 << 21},
-               {"H": 1 << 20, "I": 1 << 20, "ld": 1 << 20}, {"T": 512, "E": 64, "k": 16, "I": 1 << 19}):
+               {"H": 1 << 20, "I": 1 << 20, "ld": 1 << 20}, {"T": 512, "E": 64, "k": 16, "I": 1 << 18}):
         assert call(**kw) == EARG, kw
     for n in ("x", "wr", "q1", "s1", "q2", "s2", "y"):
         assert call(**{n: None}) == ENULL, n
