@@ -231,11 +231,13 @@ __device__ __forceinline__ void rows_product(uint8_t* lds, const uint8_t* const 
 // acc[rt][tt] += all blocks of RT 16-row weight tiles (each wave its own) times
 // the TT 16-token tiles that the workgroup's eight waves share.  Every thread
 // of the workgroup calls it, with the same x, xs and nkb.
-//   The blocks go through a ring of D slots in LDS, filled D - 1 blocks ahead;
-// each wave loads its own weight tiles and an eighth of the tokens' codes (some
-// twice where there are fewer loads than waves, so that every wave has the same
-// number in flight).  One barrier per block says that the block has landed for
-// everyone and that the slot before it may be filled again.
+//   The blocks go through two slots in LDS, one multiplied while the other
+// fills: each wave loads its own weight tiles and an eighth of the tokens'
+// codes (some twice where there are fewer loads than waves).  One barrier per
+// block says that the block has landed for everyone and that the slot before it
+// may be filled again.  (Three or four slots measured slower at every size:
+// 256 tokens through 64 experts 139 instead of 124 us.  The loads of one block
+// and CU are 32 KiB, and more LDS leaves fewer workgroups per CU.)
 //   Scales: the weights' in registers, lane i holding block i's; the tokens' in
 // LDS, [block][token]; both for 64 blocks at a time.
 //   xoff: the byte offset, from x, of the row of this lane's load;
@@ -243,21 +245,20 @@ __device__ __forceinline__ void rows_product(uint8_t* lds, const uint8_t* const 
 // ---------------------------------------------------------------------------
 constexpr int kPanel = 64;
 
-template <int RT, int TT, int D>
+template <int RT, int TT>
 __device__ __host__ constexpr int rows_ring_bytes() {
-  return D * (8 * RT + TT) * kCodeTile + kPanel * 16 * TT * 4;
+  return 2 * (8 * RT + TT) * kCodeTile + kPanel * 16 * TT * 4;
 }
 
-template <int RT, int TT, int D, class XScale>
+template <int RT, int TT, class XScale>
 __device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w)[RT], const float* const (&sw)[RT],
                                           int64_t K, const uint8_t* x, uint32_t xoff, XScale xscale, int nkb,
                                           v4f (&acc)[RT][TT]) {
-  constexpr int SLOT = (8 * RT + TT) * kCodeTile, PER = 2 * RT + 1;
-  static_assert(D == 2 || D == 3 || D == 4, "the waits below");
+  constexpr int SLOT = (8 * RT + TT) * kCodeTile;
   const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), xload = wave % (2 * TT);
   const uint32_t at = lds_offset(lds);
-  float* const scales = reinterpret_cast<float*>(lds + D * SLOT);
+  float* const scales = reinterpret_cast<float*>(lds + 2 * SLOT);
   const uint32_t woff[2] = {(uint32_t)(code_row(lane, 0) * K) + code_chunk(lane, 0),
                             (uint32_t)(code_row(lane, 1) * K) + code_chunk(lane, 1)};
   for (int p0 = 0; p0 < nkb; p0 += kPanel) {
@@ -265,11 +266,8 @@ __device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w
     float s[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) s[rt] = sw[rt][p0 + min((int)lane, nb - 1)];
-    __syncthreads();  // the scales and slots before have been read
-    for (int i = threadIdx.x; i < nb * 16 * TT; i += 512) scales[i] = xscale(i % (16 * TT), p0 + i / (16 * TT));
-
     const auto issue = [&](int b) {
-      const uint32_t slot = at + (b % D) * SLOT;
+      const uint32_t slot = at + (b & 1) * SLOT;
       const int64_t k = (int64_t)(p0 + b) * 128;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
@@ -278,20 +276,15 @@ __device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w
       }
       dma16(x + k, xoff, slot + 8 * RT * kCodeTile + xload * 1024);
     };
-    __syncthreads();  // the scales are there (and every load known to the compiler has landed)
-#pragma unroll
-    for (int b = 0; b < D - 1; ++b)
-      if (b < nb) issue(b);
+    __syncthreads();  // the scales and slots before have been read
+    issue(0);
+    // the tokens' scales come while the first block does
+    for (int i = threadIdx.x; i < nb * 16 * TT; i += 512) scales[i] = xscale(i % (16 * TT), p0 + i / (16 * TT));
     for (int b = 0; b < nb; ++b) {
-      if (D > 3 && b + 2 < nb)
-        wait_vmcnt<(D > 3 ? 2 : 0) * PER>();
-      else if (D > 2 && b + 1 < nb)
-        wait_vmcnt<(D > 2 ? 1 : 0) * PER>();
-      else
-        wait_vmcnt<0>();
+      wait_vmcnt<0>();
       lds_barrier();
-      if (b + D - 1 < nb) issue(b + D - 1);
-      const uint8_t* slot = lds + (b % D) * SLOT;
+      if (b + 1 < nb) issue(b + 1);
+      const uint8_t* slot = lds + (b & 1) * SLOT;
       BfFrag wf[RT];
       float sb[RT];
 #pragma unroll

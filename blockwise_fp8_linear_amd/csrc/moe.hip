@@ -378,11 +378,10 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(MoeArgs a, const float* 
 // through the caches.  128 columns of I in one workgroup are one group of h,
 // so h leaves quantized.
 // ---------------------------------------------------------------------------
-constexpr int kSlots = 2;
 // Dynamic LDS: the ring for the most tiles, then the list of rows.
 constexpr int kMostRows = 8192;  // T k
 template <int RT, int TMAX>
-constexpr int kRing = rows_ring_bytes<RT, TMAX, kSlots>();
+constexpr int kRing = rows_ring_bytes<RT, TMAX>();
 
 template <int TMAX, class S>
 __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint8_t* __restrict__ qx,
@@ -409,7 +408,7 @@ __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint
       v4f acc[2][TT];
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) acc[0][tt] = acc[1][tt] = v4f{};
-      rows_ring<2, TT, kSlots>(
+      rows_ring<2, TT>(
           lds, wp, sp, a.H, qx, xoff,
           [&](int i, int b) { return sx[(int64_t)b * a.T + list[min(r0 + i, rows - 1)] / a.k]; }, nkb, acc);
       uint32_t h[TT][2];
@@ -472,7 +471,7 @@ __global__ __launch_bounds__(512) void down_wide_kernel(MoeArgs a, const uint8_t
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = v4f{};
-      rows_ring<RT, TT, kSlots>(
+      rows_ring<RT, TT>(
           lds, wp, sp, a.I, qh, xoff,
           [&](int i, int b) { return sh[(int64_t)b * (a.T * a.k) + list[min(r0 + i, rows - 1)]]; }, nkb, acc);
 #pragma unroll
