@@ -1,4 +1,10 @@
-// A mixture-of-experts layer for a few tokens (include/fp8moe.h), gfx950.
+// A mixture-of-experts layer for a few tokens (include/fp8moe.h), gfx950:
+//   y[t] = sum_i w[t][i] Wd[e] q(bf16(silu(G[e] x) * (U[e] x))), e = ids[t][i],
+// q the quantizer in groups of 128.  Bound by reading the weights of the
+// experts reached, 3 H I bytes each; everything else is small beside it, or
+// (for one token) a chain of short launches.  Up to kFew tokens: logits, the
+// choice and gate/up, down.  More: logits, the choice and x's codes, gate/up,
+// down, the sum over a token's choices.
 #include "fp8blk_launch.h"
 #include "fp8moe_launch.h"
 #include "fp8route_device.h"
@@ -10,12 +16,13 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Router logits x wr^T, fp32: 16 experts x 16 tokens per workgroup, the waves
-// split H.
+// split H.  Bound by the latency of its loads (64 experts x 2048: 4.3 us for one
+// token, 5.6 for 256; 8 waves instead of 16 0.8 us more).
 // ---------------------------------------------------------------------------
 constexpr int kLogitsWaves = 16;
 __global__ __launch_bounds__(64 * kLogitsWaves) void logits_kernel(int T, int E, int H, const uint16_t* __restrict__ x,
-                                                             int64_t ld_x, const uint16_t* __restrict__ wr,
-                                                             float* __restrict__ logits) {
+                                                                   int64_t ld_x, const uint16_t* __restrict__ wr,
+                                                                   float* __restrict__ logits) {
   __shared__ v4f red[kLogitsWaves][64];
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -60,7 +67,8 @@ __device__ __forceinline__ RouteChoice choose(const float* __restrict__ row, int
 
 // ---------------------------------------------------------------------------
 // One workgroup per token: its choice (where there are logits) and its row of
-// x quantized, 16 lanes per group of 128.
+// x quantized, 16 lanes per group of 128; the scales transposed, [H / 128][T].
+// Bound by latency: 4 us for 256 tokens of 2048 and 64 experts.
 // ---------------------------------------------------------------------------
 template <class S>
 __global__ __launch_bounds__(256) void prepare_kernel(MoeArgs a, const float* __restrict__ logits,
@@ -85,8 +93,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(MoeArgs a, const float* __
 }
 
 // The rows t k + j (j-th choice of token t) that chose expert e, in order, into
-// `list`; their number.  Every thread of a workgroup of 512
-// calls it.
+// `list`; their number.  Every thread of a workgroup of 512 calls it.
 __device__ __forceinline__ int rows_of_expert(const int32_t* __restrict__ ids, int n, int e, uint16_t* list,
                                               int* scratch) {
   constexpr int N = 4;  // places per thread and round, loaded together
@@ -136,7 +143,9 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // ---------------------------------------------------------------------------
 // Up to 16 tokens: the tokens themselves are the columns of the matrix
 // instruction, whichever expert is multiplied, and the waves of a workgroup
-// split the reduction, so that a few experts of one token fill the chip.
+// split the reduction, so that a few experts of one token fill the chip: 8 of
+// 64 experts of 1024 are 512 workgroups of gate/up, where the wide kernel below
+// has 64 (20 and 27 us for both products).
 // ---------------------------------------------------------------------------
 constexpr int kFew = 16;
 constexpr int kParts = 16;  // workgroups that share a column of y, at most
@@ -199,7 +208,9 @@ __device__ __forceinline__ int few_place(const FewChoice& f, int t, int k, int e
 }
 
 // h[place] = bf16(silu(G x) * (U x)): 16 columns of I of the blockIdx.y-th
-// expert reached.  XL loads bring x's rows of a block, 4 each.
+// expert reached.  XL loads bring x's rows of a block, 4 each.  H 2048, I 1024:
+// 9.7 us for one token's 8 experts (3.5 TB/s, a launch's start and two
+// latencies), 20.7 for the 28 experts of four (5.6 TB/s).
 template <int W, int XL, int D, bool ROUTE, class S>
 __global__ __launch_bounds__(64 * W) void gate_up_few_kernel(MoeArgs a, const float* __restrict__ logits,
                                                              uint16_t* __restrict__ h) {
@@ -253,7 +264,9 @@ __global__ __launch_bounds__(64 * W) void gate_up_few_kernel(MoeArgs a, const fl
 // split; a term's routing weight goes into its block's scale.  RAW: h is bf16
 // [place][I] and quantized here; otherwise it is codes, with the scales
 // sh[I / 128][place].  With several workgroups per column their sums go to
-// partial[blockIdx.y][t][H] instead of y.
+// partial[blockIdx.y][t][H] instead of y: H / 16 workgroups are too few to read
+// many blocks (9 tokens, 7 experts of 6144: 40 us, in three parts 22.6 or 4.2
+// TB/s, and 3.9 for the sum).
 template <int W, int XL, int D, bool RAW, class S>
 __global__ __launch_bounds__(64 * W) void down_few_kernel(MoeArgs a, const uint8_t* __restrict__ h,
                                                           const float* __restrict__ sh, float* __restrict__ partial) {
@@ -372,13 +385,16 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(MoeArgs a, const float* 
 }
 
 // ---------------------------------------------------------------------------
-// The same two products for many rows per launch: each wave owns 16 columns of
-// I (their G and their U rows), or 16 RT columns of H, over the whole
-// reduction, and the eight waves of a workgroup share the tokens' codes
-// through the caches.  128 columns of I in one workgroup are one group of h,
-// so h leaves quantized.
+// The same two products for more tokens: each wave owns 16 columns of I (their
+// G and their U rows), or 16 RT columns of H, over the whole reduction, and the
+// eight waves of a workgroup share the tokens' codes in LDS.  128 columns of I
+// in one workgroup are one group of h, so h leaves quantized.  TMAX tiles of 16
+// rows at once; an expert with more rows is read again (from L2 or the
+// memory-side cache) for the rest.
+//   40 tokens, 121 of 128 experts of 768 reached: gate/up 69 us (5.5 TB/s),
+//   down 35 (5.4); 256 tokens, 64 experts of 1024: 59 (4.5) and 35 (3.8).
 // ---------------------------------------------------------------------------
-// Dynamic LDS: the ring for the most tiles, then the list of rows.
+// Dynamic LDS: the two slots for the most tiles, then the list of rows.
 constexpr int kMostRows = 8192;  // T k
 template <int RT, int TMAX>
 constexpr int kRing = rows_ring_bytes<RT, TMAX>();
@@ -573,7 +589,10 @@ hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
 
 template <class S>
 hipError_t moe(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
-  // how many experts the tokens reach, if each expert is as likely as the next
+  // how many experts the tokens reach, if each is as likely as the next; with fewer than 192 workgroups the wide kernel
+  // leaves CUs idle.  Up to 8 tokens the narrow one is as fast at any number (8 tokens, 128 experts of 768: 60 us, wide
+  // 67; 16 tokens, 64 experts of 1024: 112 and 93), but it quantizes x again for each 16 columns, which amax / 448
+  // scales make dearer (8 tokens 73 us, wide 64; 4 tokens 44 and 58)
   double missed = 1.0;
   for (int t = 0; t < a.T; ++t) missed *= 1.0 - (double)a.k / a.E;
   const double reached = a.E * (1.0 - missed);
@@ -587,7 +606,9 @@ hipError_t moe(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
     if (hipError_t e = gate_up_wide<1, S>(a, b, stream)) return e;
     return a.T <= 8 ? down_few<1, false, S>(a, b, reached, stream) : down_few<2, false, S>(a, b, reached, stream);
   }
-  const int rows = a.T * a.k / a.E;  // of an expert, on average
+  // of an expert, on average: tiles for about twice as many, for few experts have more (64 experts, k 8; one, two, four
+  // tiles at most: 64 tokens 90, 97, - us; 100 tokens 119, 107, 107; 200 tokens -, 115, 104)
+  const int rows = a.T * a.k / a.E;
   if (rows <= 8) return moe_wide<1, S>(a, b, stream);
   return rows <= 20 ? moe_wide<2, S>(a, b, stream) : moe_wide<4, S>(a, b, stream);
 }

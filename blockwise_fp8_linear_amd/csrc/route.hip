@@ -9,7 +9,10 @@
 // share a token (16 up to 256 experts, so that a wave takes four tokens and
 // its reductions stay within a DPP row; the whole wave beyond), each with NI
 // logits in registers: the logits are read once, in one pass, and the k
-// rounds of the selection run on registers.
+// rounds of the selection run on registers: a maximum of the lane's logits, one
+// across the lanes, and the same again for the lowest index that has it.
+//   16384 x 128 fp32, k 8: 8.0 us forward (1.1 TB/s; the rounds are what it
+//   spends its time on), 10.1 backward; 4095 x 60 bf16, k 4: 3.2 and 4.0.
 #include "fp8blk_device.h"
 #include "fp8moe_launch.h"
 #include "fp8route_device.h"
