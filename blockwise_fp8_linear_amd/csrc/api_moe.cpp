@@ -17,14 +17,18 @@ constexpr int64_t kMaxStride = int64_t(1) << 26;
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
+static_assert(kExactRows == FP8_LINEAR_FP32_ROWS, "the header's promise");
+
 // The rows that the GEMMs of fp8blk.h take: none where their 256x256 tiles
-// would leave most CUs idle, else the multiples of 128.  At K = 2048 the GEMM
-// takes 25 us for anything up to 256 tiles, after 3.5 for the quantizer; the
-// kernels for fewer rows take about 6.6 us per million outputs, and the GEMM's
-// remaining rows go through them too (about 8 us more).
-int64_t gemm_rows(int64_t M, int64_t N) {
-  if (M <= FP8_LINEAR_FP32_ROWS || M * N <= (M % kGroup ? 4500000 : 3500000)) return 0;
-  return M / kGroup * kGroup;
+// would leave many CUs idle, else the multiples of 128.  At K = 2048 the GEMM
+// takes 26 us for anything up to 256 tiles (2048 x 4096: 26.7), after 3.5 for
+// its quantizer, and the rows beyond about 7 more; the kernels for fewer rows
+// take 3.7 us per million outputs, after 2.2 (2048 x 4096: 30.8).  Where K / 128
+// is not a multiple of 4 the GEMM is the general one and slower (1617 x 7680 x
+// 384 26.5 us, the other 18.5).
+int64_t gemm_rows(int64_t M, int64_t N, int64_t K) {
+  const int64_t most = (K / kGroup % 4 ? 14000000 : 7500000) + (M % kGroup ? 2000000 : 0);
+  return M <= FP8_LINEAR_FP32_ROWS || M * N <= most ? 0 : M / kGroup * kGroup;
 }
 // Their codes and scales in the workspace, in front of the other rows'.
 size_t codes_bytes(int64_t rows, int64_t K) { return up256((size_t)(rows * K)); }
@@ -32,7 +36,7 @@ size_t gemm_bytes(int64_t rows, int64_t K) {
   return rows ? codes_bytes(rows, K) + up256((size_t)(rows * (K / kGroup)) * sizeof(float)) : 0;
 }
 size_t linear_bytes(int64_t M, int64_t N, int64_t K) {
-  const int64_t main = gemm_rows(M, N);
+  const int64_t main = gemm_rows(M, N, K);
   return gemm_bytes(main, K) + rows_workspace_bytes(M - main, K);
 }
 
@@ -140,7 +144,7 @@ int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x,
   if (need > 0 && !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
   if (int rc = check_device()) return rc;
   const bool f32 = out_dtype != FP8BLK_OUT_BF16, fp32_scale = scale_mode == FP8BLK_SCALE_FP32;
-  const int64_t main = gemm_rows(M, N);
+  const int64_t main = gemm_rows(M, N, K);
   if (main > 0) {
     uint8_t* q = static_cast<uint8_t*>(workspace);
     float* s = reinterpret_cast<float*>(q + codes_bytes(main, K));

@@ -22,6 +22,8 @@ struct RowsOut {
 // 12288 x 2048: power-of-two scales 48 rows 11.8 and 11.6 us, 64 rows 13.7 and
 // 12.4; amax / 448 scales, whose quotients cost more, 16 x 2048 x 6144 15.2 and
 // 10.4, 8 rows 10.8 and 10.2.
+// Up to so many rows the sums are fp32-faithful (FP8_LINEAR_FP32_ROWS).
+constexpr int64_t kExactRows = 127;
 inline int64_t raw_rows(bool fp32_scale) { return fp32_scale ? 8 : 48; }
 inline size_t rows_scales_at(int64_t M, int64_t K) { return ((size_t)(M * K) + 255) & ~size_t(255); }
 // (whichever the scales, so that a caller need not say)

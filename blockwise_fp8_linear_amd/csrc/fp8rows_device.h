@@ -68,6 +68,16 @@ __device__ __forceinline__ v4f block_product(const BfFrag& a, const BfFrag& b) {
   return p;
 }
 
+// The same on the fp8 matrix instruction, straight from the codes: a quarter of
+// the instructions and no conversions, for where the fp8 GEMMs' accuracy does
+// (1.5e-5 of the result's norm; each operand's own scale is 2^0).
+__device__ __forceinline__ v4f block_product_fp8(const CodeFrag& a, const CodeFrag& b) {
+  typedef int v8i_t __attribute__((ext_vector_type(8)));
+  const v8i_t x{(int)a.lo[0], (int)a.lo[1], (int)a.lo[2], (int)a.lo[3], (int)a.hi[0], (int)a.hi[1], (int)a.hi[2], (int)a.hi[3]};
+  const v8i_t y{(int)b.lo[0], (int)b.lo[1], (int)b.lo[2], (int)b.lo[3], (int)b.hi[0], (int)b.hi[1], (int)b.hi[2], (int)b.hi[3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, v4f{}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+}
+
 // Largest of the four lanes l, l ^ 16, l ^ 32, l ^ 48 (those that share an
 // operand row), in every lane.  v_permlane*_swap exchanges whole 16- or
 // 32-lane halves between its two operands; given the same value twice, the
@@ -238,9 +248,11 @@ __device__ __forceinline__ void rows_product(uint8_t* lds, const uint8_t* const 
 // may be filled again.  (Three or four slots measured slower at every size:
 // 256 tokens through 64 experts 139 instead of 124 us.  The loads of one block
 // and CU are 32 KiB, and more LDS leaves fewer workgroups per CU.)
+//   FP8: on the fp8 matrix instruction instead of the bf16 one.
 //   Scales: the weights' in registers, lane i holding block i's; the tokens' in
 // LDS, [block][token]; both for 64 blocks at a time.
-//   xoff: the byte offset, from x, of the row of this lane's load;
+//   xoff: the byte offset, from x, of the chunk that this lane's load brings:
+// load wave % (2 TT) of the tokens' codes, two of them to a tile;
 //   xscale(token of the TT tiles, block) gives a scale from memory.
 // ---------------------------------------------------------------------------
 constexpr int kPanel = 64;
@@ -250,7 +262,7 @@ __device__ __host__ constexpr int rows_ring_bytes() {
   return 2 * (8 * RT + TT) * kCodeTile + kPanel * 16 * TT * 4;
 }
 
-template <int RT, int TT, class XScale>
+template <int RT, int TT, bool FP8 = false, class XScale>
 __device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w)[RT], const float* const (&sw)[RT],
                                           int64_t K, const uint8_t* x, uint32_t xoff, XScale xscale, int nkb,
                                           v4f (&acc)[RT][TT]) {
@@ -285,20 +297,26 @@ __device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w
       lds_barrier();
       if (b + 1 < nb) issue(b + 1);
       const uint8_t* slot = lds + (b & 1) * SLOT;
-      BfFrag wf[RT];
+      const auto operand = [&](const uint8_t* tile) {
+        if constexpr (FP8) return read_codes(tile, r, c);
+        else return decode(read_codes(tile, r, c));
+      };
+      decltype(operand(slot)) wf[RT];
       float sb[RT];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        wf[rt] = decode(read_codes(slot + (wave * RT + rt) * kCodeTile, r, c));
+        wf[rt] = operand(slot + (wave * RT + rt) * kCodeTile);
         sb[rt] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s[rt]), b));
       }
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) {
-        const BfFrag xf = decode(read_codes(slot + (8 * RT + tt) * kCodeTile, r, c));
+        const auto xf = operand(slot + (8 * RT + tt) * kCodeTile);
         const float m = scales[b * 16 * TT + tt * 16 + r];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const v4f p = block_product(wf[rt], xf);
+          v4f p;
+          if constexpr (FP8) p = block_product_fp8(wf[rt], xf);
+          else p = block_product(wf[rt], xf);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[rt][tt][i] = __builtin_fmaf(p[i], m * sb[rt], acc[rt][tt][i]);
         }

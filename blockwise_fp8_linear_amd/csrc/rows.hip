@@ -10,6 +10,17 @@ namespace fp8blk {
 
 namespace {
 
+// Four neighbouring elements of y.
+__device__ __forceinline__ void store_rows(const RowsOut& out, int64_t at, const v4f& v) {
+  if (out.f32) {
+    v4f* y = reinterpret_cast<v4f*>(static_cast<float*>(out.y) + at);
+    *y = out.accumulate ? *y + v : v;
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out.y) + at) =
+        make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+  }
+}
+
 // One workgroup: 16 RT columns of y, 16 TT rows, the W waves splitting the
 // reduction (K / 128 blocks are few: two per wave at 2048, all in flight at
 // once).  RAW: xv is x in bf16 (ld_x elements apart) and quantized here;
@@ -64,13 +75,7 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(int64_t M, int64_t 
     const int tile = u >> 6, l = u & 63;
     const int64_t m = m0 + (tile % TT) * 16 + (l & 15), n = n0 + (tile / TT) * 16 + 4 * (l >> 4);
     if (m >= M) continue;
-    if (out.f32) {
-      v4f* y = reinterpret_cast<v4f*>(static_cast<float*>(out.y) + m * N + n);
-      *y = out.accumulate ? *y + v : v;
-    } else {
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out.y) + m * N + n) =
-          make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
-    }
+    store_rows(out, m * N + n, v);
   }
 }
 
@@ -87,6 +92,34 @@ hipError_t launch(int64_t M, int64_t N, int64_t K, const void* x, int64_t row_by
   hipLaunchKernelGGL((linear_rows_kernel<W, RT, TT, XL, D, RAW, S>), grid, dim3(64 * W), lds, stream, M, N, K,
                      static_cast<const uint8_t*>(x), row_bytes, xs, qw, sw, out);
   return hipGetLastError();
+}
+
+// Many rows, but too few for the GEMMs' 256x256 tiles: 128 columns of y and 64
+// rows per workgroup, whole reduction, x's codes shared in LDS, the fp8 matrix
+// instruction.  Bound by what the tiles load from L2 (192 bytes per 8192
+// multiply-adds) and by one block's latency.  (Columns x rows) 128 x 32, 128 x
+// 128, 256 x 64 and 256 x 128 measured slower: 1024 x 4096 x 2048 16.9 us, and
+// 23.1, 18.6, 20.2, 28.7.
+constexpr int kWideTiles = 4;
+__global__ __launch_bounds__(512) void linear_wide_kernel(int64_t M, int64_t N, int64_t K, const uint8_t* __restrict__ q,
+                                                          const float* __restrict__ xs, const uint8_t* __restrict__ qw,
+                                                          const float* __restrict__ sw, RowsOut out) {
+  extern __shared__ uint8_t lds[];
+  constexpr int TT = kWideTiles;
+  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = ((int64_t)blockIdx.x * 8 + wave) * 16, m0 = (int64_t)blockIdx.y * 16 * TT;
+  const int nkb = (int)(K / 128), rows = (int)(M - m0 < 16 * TT ? M - m0 : 16 * TT);
+  const uint8_t* const wp[1] = {qw + n0 * K};
+  const float* const sp[1] = {sw + n0 / 128 * nkb};
+  const int load = wave % (2 * TT), row = (load >> 1) * 16 + (int)code_row(lane, load & 1);
+  const uint32_t xoff = (uint32_t)(min(row, rows - 1) * K) + code_chunk(lane, load & 1);
+  v4f acc[1][TT] = {};
+  rows_ring<1, TT, true>(
+      lds, wp, sp, K, q + m0 * K, xoff, [&](int i, int b) { return xs[b * M + m0 + min(i, rows - 1)]; }, nkb, acc);
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt)
+    if (tt * 16 + r < rows) store_rows(out, (m0 + tt * 16 + r) * N + n0 + 4 * c, acc[0][tt]);
 }
 
 // ---------------------------------------------------------------------------
@@ -135,15 +168,28 @@ hipError_t launch_raw(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_
 #undef FP8_RAW
 }
 
+hipError_t launch_wide(int64_t M, int64_t N, int64_t K, const uint8_t* q, const float* s, const uint8_t* qw,
+                       const float* sw, RowsOut out, hipStream_t stream) {
+  constexpr int lds = rows_ring_bytes<1, kWideTiles>();
+  static std::atomic<uint64_t> raised{0};
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&linear_wide_kernel), lds, &raised)) return e;
+  const dim3 grid((uint32_t)(N / 128), (uint32_t)((M + 16 * kWideTiles - 1) / (16 * kWideTiles)));
+  hipLaunchKernelGGL(linear_wide_kernel, grid, dim3(512), lds, stream, M, N, K, q, s, qw, sw, out);
+  return hipGetLastError();
+}
+
 // More rows: x quantized once (2.2 us), then tiles of codes.  The smallest of
 // (tiles of columns, of tokens) (1, 1), (2, 1), (2, 2), (4, 2), (4, 4) that
 // has at most 256 workgroups: 24 x 4096 (2, 1) 4.1; 64 x 4096 (2, 2) 4.9 and
 // (4, 1) 5.1; 128 x 4096 (4, 2) 6.0 and (2, 2) 6.6; 256 x 4096 (4, 4) 8.2 and
 // (4, 2) 9.9.  Where all have more, smaller workgroups of (3, 2): 64 x 12288
-// 10.4 and (4, 4) 11.4; 256 x 12288 22.7 and (4, 4) 23.7.
+// 10.4 and (4, 4) 11.4; 96 x 12288 12.0 and (4, 2) 13.3.  Above kExactRows
+// rows, and with 200 workgroups of it, the wide kernel: 512 x 4096 12.8 and 16.6, 1467
+// x 2560 (K 6400) 44 and 73; with fewer, 333 x 2048 11.4 and 8.3.
 hipError_t launch_codes(int64_t M, int64_t N, int64_t K, const uint8_t* q, const float* s, const uint8_t* qw,
                         const float* sw, RowsOut out, hipStream_t stream) {
   const int64_t tiles = N / 16, m1 = (M + 15) / 16, m2 = (M + 31) / 32, m4 = (M + 63) / 64;
+  if (M > kExactRows && tiles / 8 * m4 >= 200) return launch_wide(M, N, K, q, s, qw, sw, out, stream);
 #define FP8_CODES(W, RT, TT) launch<W, RT, TT, 2, 1, false, Pow2Scale>(M, N, K, q, K, s, qw, sw, out, stream)
   if (tiles * m1 <= 256) return FP8_CODES(16, 1, 1);
   if (tiles / 2 * m1 <= 256) return FP8_CODES(8, 2, 1);

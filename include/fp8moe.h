@@ -43,10 +43,9 @@ enum fp8moe_dtype { FP8MOE_BF16 = 0, FP8MOE_FP32 = 1 };
  *   N, K positive multiples of 128; x, qw, y 16-byte aligned.
  *   workspace: at least fp8_linear_workspace_size(M, N, K) bytes, 16-byte
  *     aligned; may be NULL when that size is 0 (it is up to 8 rows).
- * Up to FP8_LINEAR_FP32_ROWS rows the call is bound by reading the weights; it
- * quantizes x on the way and sums the products with fp32 faithfulness.  Above,
- * x is quantized into the workspace first and the multiples of 128 rows go
- * through the GEMMs of fp8blk.h, with their accuracy.
+ * Up to FP8_LINEAR_FP32_ROWS rows the products are summed with fp32
+ * faithfulness; above, with the accuracy of the GEMMs of fp8blk.h, which take
+ * the multiples of 128 rows of large products.
  */
 int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t *x, int64_t ld_x,
                const uint8_t *qw, const float *sw, void *y, int out_dtype, int scale_mode,

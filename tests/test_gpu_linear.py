@@ -36,7 +36,8 @@ def _run(M, N, K, mode, x=None, seed=0, ld=None):
 M_ALL = [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 96, 100, 127, 128, 129, 200, 255, 256, 257, 383, 513, 700]
 SHAPES = [(1, 128, 128), (5, 128, 1152), (3, 1152, 128), (16, 256, 2048), (1, 2048, 6144), (40, 384, 768),
           (7, 8192, 256), (20, 12288, 128), (33, 16384, 256), (64, 640, 384), (130, 8192, 128),
-          (700, 8192, 128), (475, 8192, 256), (1100, 4096, 128), (2048, 2048, 128)]
+          (700, 8192, 128), (475, 8192, 256), (1100, 4096, 128), (2048, 2048, 128),
+          (1500, 8192, 512), (1200, 8192, 512), (2300, 8192, 128), (513, 3328, 640), (128, 25600, 128)]
 
 
 @pytest.mark.parametrize("M,N,K,mode", [(m, 256, 384, POW2) for m in M_ALL] + [(m, 384, 256, FP32) for m in M_ALL[::3]] +
@@ -99,7 +100,7 @@ def test_equals_the_quantizer_and_fprop():
     """Multiples of 128 rows that fill the GEMM's tiles are the library's own
     quantizer and GEMM, bit for bit."""
     import torch
-    M, N, K = 4096, 2048, 256
+    M, N, K = 4096, 2048, 512
     x, w = dev_bf16(synth.normal_bf16((M, K), 1.0, 66)), dev_bf16(synth.normal_bf16((N, K), 0.02, 67))
     qw, _, sw = fb.fp8_quantize_block(w, transpose=False)
     qx, sx = fb.fp8_quantize_rowgroup(x)
