@@ -148,6 +148,9 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // has 64 (20 and 27 us for both products).
 // ---------------------------------------------------------------------------
 constexpr int kFew = 16;
+// About the most workgroups of gate/up; beyond, each takes several columns, so that its start counts less (4 tokens, 18
+// experts of 1408 x 256: 44 us without, 35 with; at 768 as well, but 8 tokens, 51 experts of 768 x 2048 60 and 62).
+constexpr int kFewGrid = 2304;
 constexpr int kParts = 16;  // workgroups that share a column of y, at most
 
 // The choice of the whole call in LDS, and the experts it reaches, in the order
@@ -217,7 +220,7 @@ __global__ __launch_bounds__(64 * W) void gate_up_few_kernel(MoeArgs a, const fl
   extern __shared__ uint8_t lds[];  // the waves' areas; then their sums, [W][2][64] v4f
   __shared__ FewChoice f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * 16, nkb = a.H / 128, n = a.T * a.k;
+  const int nkb = a.H / 128, n = a.T * a.k;
   few_choice<ROUTE>(a, logits, f);
   if (ROUTE && blockIdx.x == 0 && blockIdx.y == 0) {
     for (int s = threadIdx.x; s < n; s += 64 * W) {
@@ -230,32 +233,34 @@ __global__ __launch_bounds__(64 * W) void gate_up_few_kernel(MoeArgs a, const fl
 
   const uint8_t* base = a.qw1 + (int64_t)e * 2 * a.I * a.H;
   const float* sbase = a.sw1 + (int64_t)e * (2 * a.I / 128) * nkb;
-  const uint8_t* const wp[2] = {base + (int64_t)n0 * a.H, base + (int64_t)(a.I + n0) * a.H};
-  const float* const sp[2] = {sbase + n0 / 128 * nkb, sbase + (a.I + n0) / 128 * nkb};
   const float* const none[1] = {nullptr};
   uint32_t xoff[1][XL];
 #pragma unroll
   for (int u = 0; u < XL; ++u)
     xoff[0][u] = (uint32_t)(min((int)raw_row(lane, u), a.T - 1) * a.ld_x * 2) + (lane & 15) * 16;
-  v4f acc[2][1] = {};
-  rows_product<2, 1, XL, D, true, S>(lds + wave * D * rows_stage_bytes<2, 1, true, XL>(), wp, sp, a.H,
-                                     reinterpret_cast<const uint8_t*>(a.x), xoff, none, 0, wave * nkb / W,
-                                     (wave + 1) * nkb / W, acc);
   v4f* red = reinterpret_cast<v4f*>(lds);
-  __syncthreads();
-  red[(wave * 2) * 64 + lane] = acc[0][0];
-  red[(wave * 2 + 1) * 64 + lane] = acc[1][0];
-  __syncthreads();
-  if (wave == 0 && (lane & 15) < a.T) {
-    v4f g = red[lane], u = red[64 + lane];
-    for (int w = 1; w < W; ++w) {
-      g += red[w * 128 + lane];
-      u += red[w * 128 + 64 + lane];
-    }
-    const int place = few_place(f, lane & 15, a.k, e);
-    if (place >= 0)
+  const int place = wave == 0 && (lane & 15) < a.T ? few_place(f, lane & 15, a.k, e) : -1;
+  for (int n0 = blockIdx.x * 16; n0 < a.I; n0 += gridDim.x * 16) {
+    const uint8_t* const wp[2] = {base + (int64_t)n0 * a.H, base + (int64_t)(a.I + n0) * a.H};
+    const float* const sp[2] = {sbase + n0 / 128 * nkb, sbase + (a.I + n0) / 128 * nkb};
+    v4f acc[2][1] = {};
+    rows_product<2, 1, XL, D, true, S>(lds + wave * D * rows_stage_bytes<2, 1, true, XL>(), wp, sp, a.H,
+                                       reinterpret_cast<const uint8_t*>(a.x), xoff, none, 0, wave * nkb / W,
+                                       (wave + 1) * nkb / W, acc);
+    __syncthreads();
+    red[(wave * 2) * 64 + lane] = acc[0][0];
+    red[(wave * 2 + 1) * 64 + lane] = acc[1][0];
+    __syncthreads();
+    if (place >= 0) {
+      v4f g = red[lane], u = red[64 + lane];
+      for (int w = 1; w < W; ++w) {
+        g += red[w * 128 + lane];
+        u += red[w * 128 + 64 + lane];
+      }
       *reinterpret_cast<uint2*>(h + (int64_t)place * a.I + n0 + 4 * (lane >> 4)) =
           make_uint2(bf16x2_rne(silu(g[0]) * u[0], silu(g[1]) * u[1]), bf16x2_rne(silu(g[2]) * u[2], silu(g[3]) * u[3]));
+    }
+    __syncthreads();  // before the sums are overwritten
   }
 }
 
@@ -540,8 +545,11 @@ hipError_t down_few(const MoeArgs& a, const MoeBuffers& b, double reached, hipSt
   static std::atomic<uint64_t> raised{0};
   const auto k = &down_few_kernel<W, XL, D, RAW, S>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), lds, &raised)) return e;
-  const double blocks = reached * (a.I / 128) * (a.H / 16);  // of 2 KiB
-  int parts = (int)(blocks / 12000);
+  // as many parts as leave a wave a few rounds of loads, up to one workgroup per CU where only one fits, else two (four
+  // tokens, 28 experts of 1024: 2 parts 42 us, 3 parts 47; 16 tokens, 56 experts: 4 parts 80, 5 parts 84, 6 parts 82)
+  const int columns = a.H / 16, most = (RAW && XL == 1 ? 256 : 512) / columns;
+  int parts = (int)(reached * (a.I / 128) / (W * D * (W == 16 ? 2 : 4)));
+  if (parts > most) parts = most;
   parts = parts < 1 ? 1 : parts > kParts ? kParts : parts;
   hipLaunchKernelGGL(k, dim3(a.H / 16, parts), dim3(64 * W), lds, stream, a, b.h, b.sh, b.partial);
   if (parts == 1) return hipGetLastError();
@@ -558,7 +566,9 @@ hipError_t moe_few(const MoeArgs& a, const MoeBuffers& b, double reached, hipStr
   const auto k = b.logits ? &gate_up_few_kernel<W, XL, D, true, S> : &gate_up_few_kernel<W, XL, D, false, S>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), lds, &raised[b.logits != nullptr])) return e;
   const int most = a.T * a.k < a.E ? a.T * a.k : a.E;  // experts reached
-  hipLaunchKernelGGL(k, dim3(a.I / 16, most), dim3(64 * W), lds, stream, a, b.logits, reinterpret_cast<uint16_t*>(b.h));
+  int across = a.I / 16;
+  if (across * most > kFewGrid) across = (kFewGrid + most - 1) / most;
+  hipLaunchKernelGGL(k, dim3(across, most), dim3(64 * W), lds, stream, a, b.logits, reinterpret_cast<uint16_t*>(b.h));
   if (hipError_t e = hipGetLastError()) return e;
   return down_few<XL, true, S>(a, b, reached, stream);
 }
@@ -589,14 +599,14 @@ hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
 
 template <class S>
 hipError_t moe(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
-  // how many experts the tokens reach, if each is as likely as the next; with fewer than 192 workgroups the wide kernel
-  // leaves CUs idle.  Up to 8 tokens the narrow one is as fast at any number (8 tokens, 128 experts of 768: 60 us, wide
+  // how many experts the tokens reach, if each is as likely as the next; with fewer than 64 workgroups the wide
+  // gate/up kernel leaves too many CUs idle (14 tokens, 9 experts of 1664 x 256: narrow 43 us, wide 24).  Up to 8 tokens the narrow one is as fast at any number (8 tokens, 128 experts of 768: 60 us, wide
   // 67; 16 tokens, 64 experts of 1024: 112 and 93), but it quantizes x again for each 16 columns, which amax / 448
   // scales make dearer (8 tokens 73 us, wide 64; 4 tokens 44 and 58)
   double missed = 1.0;
   for (int t = 0; t < a.T; ++t) missed *= 1.0 - (double)a.k / a.E;
   const double reached = a.E * (1.0 - missed);
-  if (a.T <= (a.fp32_scale ? 4 : 8) || (a.T <= kFew && reached * (a.I / 128) < 192)) {
+  if (a.T <= (a.fp32_scale ? 4 : 8) || (a.T <= kFew && reached * (a.I / 128) < 64)) {
     if (a.T <= 4) return moe_few<1, S>(a, b, reached, stream);
     return a.T <= 8 ? moe_few<2, S>(a, b, reached, stream) : moe_few<4, S>(a, b, reached, stream);
   }
