@@ -73,9 +73,12 @@ __device__ __forceinline__ v4f block_product(const BfFrag& a, const BfFrag& b) {
 // (1.5e-5 of the result's norm; each operand's own scale is 2^0).
 __device__ __forceinline__ v4f block_product_fp8(const CodeFrag& a, const CodeFrag& b) {
   typedef int v8i_t __attribute__((ext_vector_type(8)));
-  const v8i_t x{(int)a.lo[0], (int)a.lo[1], (int)a.lo[2], (int)a.lo[3], (int)a.hi[0], (int)a.hi[1], (int)a.hi[2], (int)a.hi[3]};
-  const v8i_t y{(int)b.lo[0], (int)b.lo[1], (int)b.lo[2], (int)b.lo[3], (int)b.hi[0], (int)b.hi[1], (int)b.hi[2], (int)b.hi[3]};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, v4f{}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+  const auto join = [](const CodeFrag& q) {
+    return v8i_t{(int)q.lo[0], (int)q.lo[1], (int)q.lo[2], (int)q.lo[3],
+                 (int)q.hi[0], (int)q.hi[1], (int)q.hi[2], (int)q.hi[3]};
+  };
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(a), join(b), v4f{}, 0, 0, 0, 0x7F7F7F7F, 0,
+                                                          0x7F7F7F7F);
 }
 
 // Largest of the four lanes l, l ^ 16, l ^ 32, l ^ 48 (those that share an

@@ -66,28 +66,69 @@ __device__ __forceinline__ RouteChoice choose(const float* __restrict__ row, int
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup per token: its choice (where there are logits) and its row of
-// x quantized, 16 lanes per group of 128; the scales transposed, [H / 128][T].
-// Bound by latency: 4 us for 256 tokens of 2048 and 64 experts.
+// One workgroup per token: its choice, and (where qx is given) its row of x
+// quantized, 16 lanes per group of 128, the scales transposed, [H / 128][T].
+//   WR: the logits are found here too, a wave taking four experts at a time,
+// each lane 8 neighbouring values of every 512: whole lines, fp32 sums of exact
+// products.  One CU reads all of wr for its token: faster than a launch of its
+// own for the logits while wr is small (40 tokens, 32 experts x 1024: 28.2
+// instead of 29.2 us for a layer, and one launch of the host's less), slower
+// when it is not (512 tokens, 64 x 2048: 95.7 and 88.9; one token: 27.5 and
+// 25.1).  Otherwise the choice is from `logits`, if there are any.
+//   Bound by latency: 4 us for 256 tokens of 2048 with 64 logits.
 // ---------------------------------------------------------------------------
-template <class S>
-__global__ __launch_bounds__(256) void prepare_kernel(MoeArgs a, const float* __restrict__ logits,
-                                                      uint8_t* __restrict__ qx, float* __restrict__ sx) {
-  const int t = blockIdx.x, l16 = threadIdx.x & 15;
-  for (int g = threadIdx.x >> 4; g < a.H / 128; g += 16) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(a.x + t * a.ld_x + g * 128 + l16 * 8);
-    uint32_t m = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
-    m = row16_max(max(m & 0xFFFFu, m >> 16));
-    const S sc(m);
-    *reinterpret_cast<uint2*>(qx + (int64_t)t * a.H + g * 128 + l16 * 8) =
-        make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
-    if (l16 == 0) sx[(int64_t)g * a.T + t] = sc.s;
+constexpr int64_t kTokenLogits = 64 * 1024;  // E H, at most
+
+template <bool WR>
+constexpr int kTokenThreads = WR ? 1024 : 256;
+
+template <bool WR, class S>
+__global__ __launch_bounds__(kTokenThreads<WR>) void token_kernel(MoeArgs a, const float* __restrict__ logits,
+                                                                  uint8_t* __restrict__ qx, float* __restrict__ sx) {
+  __shared__ float row[WR ? 1024 : 1];
+  const int t = blockIdx.x, l16 = threadIdx.x & 15, lane = threadIdx.x & 63;
+  const uint16_t* x = a.x + t * a.ld_x;
+  if constexpr (WR) {
+    const int wave = threadIdx.x >> 6;
+    for (int e0 = wave * 4; e0 < a.E; e0 += 64) {
+      float sum[4] = {};
+#pragma unroll 4
+      for (int h = lane * 8; h < a.H; h += 512) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(x + h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const u32x4 w = *reinterpret_cast<const u32x4*>(a.wr + (int64_t)min(e0 + i, a.E - 1) * a.H + h);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sum[i] = __builtin_fmaf(bf16_lo(w[j]), bf16_lo(v[j]), sum[i]);
+            sum[i] = __builtin_fmaf(bf16_hi(w[j]), bf16_hi(v[j]), sum[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float s = lanes_sum<64>(sum[i]);
+        if (lane == 0 && e0 + i < a.E) row[e0 + i] = s;
+      }
+    }
   }
-  if (logits && threadIdx.x < 64) {
-    const RouteChoice c = choose(logits + (int64_t)t * a.E, a.E, a.k, a.renorm, threadIdx.x);
-    if ((int)threadIdx.x < a.k) {
-      a.ids[t * a.k + threadIdx.x] = c.id;
-      a.weights[t * a.k + threadIdx.x] = c.weight;
+  if (qx) {
+    for (int g = threadIdx.x >> 4; g < a.H / 128; g += kTokenThreads<WR> / 16) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(x + g * 128 + l16 * 8);
+      uint32_t m = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
+      m = row16_max(max(m & 0xFFFFu, m >> 16));
+      const S sc(m);
+      *reinterpret_cast<uint2*>(qx + (int64_t)t * a.H + g * 128 + l16 * 8) =
+          make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
+      if (l16 == 0) sx[(int64_t)g * a.T + t] = sc.s;
+    }
+  }
+  if constexpr (WR) __syncthreads();
+  if ((WR || logits) && threadIdx.x < 64) {
+    const RouteChoice c = choose(WR ? row : logits + (int64_t)t * a.E, a.E, a.k, a.renorm, lane);
+    if (lane < a.k) {
+      a.ids[t * a.k + lane] = c.id;
+      a.weights[t * a.k + lane] = c.weight;
     }
   }
 }
@@ -346,8 +387,8 @@ __global__ __launch_bounds__(64 * W) void down_few_kernel(MoeArgs a, const uint8
         if (b + d >= end) break;
 #pragma unroll
         for (int u = 0; u < XL; ++u)
-          quantize_into<S>(area + d * SB + kCodeTile, reinterpret_cast<float*>(area + d * SB + kCodeTile + TILE), v[d][u],
-                           lane, u);
+          quantize_into<S>(area + d * SB + kCodeTile, reinterpret_cast<float*>(area + d * SB + kCodeTile + TILE),
+                           v[d][u], lane, u);
       }
     }
     loads_landed();
@@ -522,7 +563,8 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, const float* __
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int s = t * a.k + min(j0 + j, a.k - 1), id = a.ids[s];
-      term[j] = j0 + j < a.k && id >= 0 && id < a.E ? *reinterpret_cast<const v4f*>(partial + (int64_t)s * a.H + n) : v4f{};
+      const bool is = j0 + j < a.k && id >= 0 && id < a.E;
+      term[j] = is ? *reinterpret_cast<const v4f*>(partial + (int64_t)s * a.H + n) : v4f{};
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) v += term[j];
@@ -532,7 +574,7 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, const float* __
 
 // The launches of up to kFew tokens, and of more.
 struct MoeBuffers {
-  float* logits;  // null where ids and weights are given
+  float* logits;  // null where ids and weights are there already
   uint8_t *qx, *h;
   float *sx, *sh, *partial;
 };
@@ -598,20 +640,39 @@ hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
 }
 
 template <class S>
-hipError_t moe(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
-  // how many experts the tokens reach, if each is as likely as the next; with fewer than 64 workgroups the wide
-  // gate/up kernel leaves too many CUs idle (14 tokens, 9 experts of 1664 x 256: narrow 43 us, wide 24).  Up to 8 tokens the narrow one is as fast at any number (8 tokens, 128 experts of 768: 60 us, wide
-  // 67; 16 tokens, 64 experts of 1024: 112 and 93), but it quantizes x again for each 16 columns, which amax / 448
-  // scales make dearer (8 tokens 73 us, wide 64; 4 tokens 44 and 58)
+hipError_t moe(const MoeArgs& a, MoeBuffers b, hipStream_t stream) {
+  // how many experts the tokens reach, if each is as likely as the next; with fewer than 64 workgroups the wide gate/up
+  // kernel leaves too many CUs idle (14 tokens, 9 experts of 1664 x 256, 88 workgroups: narrow 43 us, wide 24).  Up to 8
+  // tokens the narrow one is as fast at any number (8 tokens, 128 experts of 768: 60 us, wide 67; 16 tokens, 64 experts
+  // of 1024: 112 and 93), but it quantizes x again for each 16 columns, which amax / 448 scales make dearer (8 tokens
+  // 73 us, wide 64)
   double missed = 1.0;
   for (int t = 0; t < a.T; ++t) missed *= 1.0 - (double)a.k / a.E;
   const double reached = a.E * (1.0 - missed);
-  if (a.T <= (a.fp32_scale ? 4 : 8) || (a.T <= kFew && reached * (a.I / 128) < 64)) {
+  const bool few = a.T <= (a.fp32_scale ? 4 : 8) || (a.T <= kFew && reached * (a.I / 128) < 64);
+  // the choice: with its logits where wr is small, else from the logits' own launch, by the narrow gate/up itself or
+  // with x's codes
+  if (a.wr && a.E * (int64_t)a.H <= kTokenLogits) {
+    hipLaunchKernelGGL((token_kernel<true, S>), dim3(a.T), dim3(kTokenThreads<true>), 0, stream, a, nullptr,
+                       few ? nullptr : b.qx, b.sx);
+    if (hipError_t e = hipGetLastError()) return e;
+    b.logits = nullptr;
+  } else {
+    if (a.wr) {
+      hipLaunchKernelGGL(logits_kernel, dim3((a.E + 15) / 16, (a.T + 15) / 16), dim3(64 * kLogitsWaves), 0, stream, a.T,
+                         a.E, a.H, a.x, a.ld_x, a.wr, b.logits);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+    if (!few) {
+      hipLaunchKernelGGL((token_kernel<false, S>), dim3(a.T), dim3(kTokenThreads<false>), 0, stream, a, b.logits, b.qx,
+                         b.sx);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+  }
+  if (few) {
     if (a.T <= 4) return moe_few<1, S>(a, b, reached, stream);
     return a.T <= 8 ? moe_few<2, S>(a, b, reached, stream) : moe_few<4, S>(a, b, reached, stream);
   }
-  hipLaunchKernelGGL(prepare_kernel<S>, dim3(a.T), dim3(256), 0, stream, a, b.logits, b.qx, b.sx);
-  if (hipError_t e = hipGetLastError()) return e;
   if (a.T <= kFew) {
     if (hipError_t e = gate_up_wide<1, S>(a, b, stream)) return e;
     return a.T <= 8 ? down_few<1, false, S>(a, b, reached, stream) : down_few<2, false, S>(a, b, reached, stream);
@@ -631,11 +692,6 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
   const auto f32 = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
   const MoeBuffers b{a.wr ? f32(w.logits) : nullptr, reinterpret_cast<uint8_t*>(ws + w.qx),
                      reinterpret_cast<uint8_t*>(ws + w.h), f32(w.sx), f32(w.sh), f32(w.partial)};
-  if (a.wr) {
-    hipLaunchKernelGGL(logits_kernel, dim3((a.E + 15) / 16, (a.T + 15) / 16), dim3(64 * kLogitsWaves), 0, stream, a.T, a.E,
-                       a.H, a.x, a.ld_x, a.wr, b.logits);
-    if (hipError_t e = hipGetLastError()) return e;
-  }
   return a.fp32_scale ? moe<Fp32Scale>(a, b, stream) : moe<Pow2Scale>(a, b, stream);
 }
 

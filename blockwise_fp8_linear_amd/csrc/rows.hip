@@ -59,8 +59,8 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(int64_t M, int64_t 
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = v4f{};
-  rows_product<RT, TT, XL, D, RAW, S>(lds + wave * D * rows_stage_bytes<RT, TT, RAW, XL>(), wp, sp, K, xv + m0 * row_bytes,
-                                      xoff, xsp, M, wave * nkb / W, (wave + 1) * nkb / W, acc);
+  rows_product<RT, TT, XL, D, RAW, S>(lds + wave * D * rows_stage_bytes<RT, TT, RAW, XL>(), wp, sp, K,
+                                      xv + m0 * row_bytes, xoff, xsp, M, wave * nkb / W, (wave + 1) * nkb / W, acc);
 
   v4f* red = reinterpret_cast<v4f*>(lds);
   __syncthreads();

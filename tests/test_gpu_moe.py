@@ -159,7 +159,8 @@ def _case(T, H, I, E, k, seed, mode, ids=None):
 EXPERTS = [(1, 256, 128, 4, 2), (1, 128, 384, 16, 16), (2, 384, 256, 3, 3), (15, 256, 128, 5, 2), (16, 128, 128, 8, 4),
            (17, 256, 256, 4, 1), (31, 128, 128, 2, 2), (33, 384, 128, 6, 3), (64, 256, 384, 3, 2), (65, 128, 128, 1, 1),
            (130, 256, 128, 2, 1), (200, 128, 256, 40, 5), (512, 128, 128, 3, 2),
-           (20, 384, 128, 40, 2), (20, 128, 256, 64, 4), (12, 128, 512, 64, 8), (6, 128, 768, 64, 8), (40, 128, 128, 1024, 16)]
+           (20, 384, 128, 40, 2), (20, 128, 256, 64, 4), (12, 128, 512, 64, 8), (6, 128, 768, 64, 8),
+           (40, 128, 128, 1024, 16)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", EXPERTS)
@@ -207,8 +208,8 @@ def _exact_case(T, E, k, seed, H=256, I=256):
     for t in range(T):
         for j, e in enumerate(ids[t]):
             y[t] += float(w[t, j]) * (Wd[e].astype(np.float64) @ ((G[e] @ x[t]).astype(np.float64) * (Uw[e] @ x[t])))
-    return (dev_bf16(bits(x)), dev(ids), dev(w), dev(q1.reshape(E, 2 * I, H)), dev(s1.reshape(E, 2 * I // 128, H // 128)),
-            dev(q2.reshape(E, H, I)), dev(s2.reshape(E, H // 128, I // 128))), y
+    return (dev_bf16(bits(x)), dev(ids), dev(w), dev(q1.reshape(E, 2 * I, H)),
+            dev(s1.reshape(E, 2 * I // 128, H // 128)), dev(q2.reshape(E, H, I)), dev(s2.reshape(E, H // 128, I // 128))), y
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 3, 2), (7, 9, 4), (16, 2, 2), (40, 5, 3), (100, 1, 1), (300, 4, 2)])
@@ -266,8 +267,9 @@ def test_experts_one_token_does_not_reach_another(T):
 
 # ------------------------------------------------------------ a whole layer --
 
-@pytest.mark.parametrize("T,H,I,E,k", [(1, 256, 128, 8, 2), (6, 384, 128, 17, 3), (16, 128, 256, 4, 4), (20, 256, 128, 70, 8),
-                                       (100, 128, 128, 9, 2)])
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 256, 128, 8, 2), (6, 384, 128, 17, 3), (16, 128, 256, 4, 4),
+                                       (20, 256, 128, 70, 8), (100, 128, 128, 9, 2), (3, 1024, 128, 70, 5),
+                                       (20, 1024, 128, 70, 5), (12, 640, 128, 20, 3)])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_layer_is_route_and_experts(T, H, I, E, k, renorm):
     import torch

@@ -81,7 +81,8 @@ def test_linear_errors(lib):
 def test_linear_workspace(lib):
     q = lib.fp8_linear_workspace_size
     assert q(1, 128, 128) == 0 and q(8, 12288, 2048) == 0
-    for bad in ((0, 128, 128), (1, 100, 128), (1, 128, 100), (1 << 27, 128, 128), (1, 128, 128 << 18), (1 << 62, 128, 128)):
+    for bad in ((0, 128, 128), (1, 100, 128), (1, 128, 100), (1 << 27, 128, 128), (1, 128, 128 << 18),
+                (1 << 62, 128, 128)):
         assert q(*bad) == BAD, bad
     # codes and scales of every row that is quantized first, whichever kernel takes it
     for M, N, K in ((49, 128, 128), (127, 256, 640), (333, 2048, 2048), (4133, 4096, 2048), (1100, 4096, 128)):
@@ -145,8 +146,8 @@ def test_moe_errors(lib):
 
 def test_moe_workspace(lib):
     q = lib.fp8_moe_workspace_size
-    for bad in ((0, 128, 128, 1, 1), (1, 100, 128, 1, 1), (1, 128, 100, 1, 1), (513, 128, 128, 1, 1), (1, 128, 128, 1025, 1),
-                (1, 128, 128, 4, 5), (1, 128, 128, 4, 0), (1, 1 << 62, 128, 4, 1)):
+    for bad in ((0, 128, 128, 1, 1), (1, 100, 128, 1, 1), (1, 128, 100, 1, 1), (513, 128, 128, 1, 1),
+                (1, 128, 128, 1025, 1), (1, 128, 128, 4, 5), (1, 128, 128, 4, 0), (1, 1 << 62, 128, 4, 1)):
         assert q(*bad) == BAD, bad
     for T, H, I, E, k in ((1, 128, 128, 1, 1), (16, 2048, 1024, 64, 16), (17, 2048, 6144, 8, 2), (512, 256, 128, 1024, 16)):
         # logits, choice, x's codes and scales, h, its scales, partial results (16 workgroups a column at most, few tokens)
