@@ -328,8 +328,7 @@ __device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w
   }
 }
 
-// f(tag) for the number of 16-row tiles that hold
-// `rows` rows, at most MAX.
+// f(tag) for the number of 16-row tiles that hold `rows` rows, at most MAX.
 template <int V>
 struct Tiles {
   static constexpr int value = V;

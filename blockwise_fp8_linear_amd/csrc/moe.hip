@@ -2,9 +2,11 @@
 //   y[t] = sum_i w[t][i] Wd[e] q(bf16(silu(G[e] x) * (U[e] x))), e = ids[t][i],
 // q the quantizer in groups of 128.  Bound by reading the weights of the
 // experts reached, 3 H I bytes each; everything else is small beside it, or
-// (for one token) a chain of short launches.  Up to kFew tokens: logits, the
-// choice and gate/up, down.  More: logits, the choice and x's codes, gate/up,
-// down, the sum over a token's choices.
+// (for one token) a chain of short launches.  A few tokens: the logits (and,
+// of a small router, the choice), gate/up with the choice, down, and the sum of
+// its parts where there are several.  More: the logits, the choice with x's
+// codes (a small router: all three in one launch), gate/up, down, the sum over a
+// token's choices.
 #include "fp8blk_launch.h"
 #include "fp8moe_launch.h"
 #include "fp8route_device.h"
@@ -189,8 +191,9 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // has 64 (20 and 27 us for both products).
 // ---------------------------------------------------------------------------
 constexpr int kFew = 16;
-// About the most workgroups of gate/up; beyond, each takes several columns, so that its start counts less (4 tokens, 18
-// experts of 1408 x 256: 44 us without, 35 with; at 768 as well, but 8 tokens, 51 experts of 768 x 2048 60 and 62).
+// About the most workgroups of gate/up; beyond, each takes several columns, so
+// that its start counts less (4 tokens, 18 experts of 1408 x 256: 44 us without,
+// 35 with; at 768 as well, but 8 tokens, 51 experts of 768 x 2048 60 and 62).
 constexpr int kFewGrid = 2304;
 constexpr int kParts = 16;  // workgroups that share a column of y, at most
 
@@ -299,7 +302,8 @@ __global__ __launch_bounds__(64 * W) void gate_up_few_kernel(MoeArgs a, const fl
         u += red[w * 128 + 64 + lane];
       }
       *reinterpret_cast<uint2*>(h + (int64_t)place * a.I + n0 + 4 * (lane >> 4)) =
-          make_uint2(bf16x2_rne(silu(g[0]) * u[0], silu(g[1]) * u[1]), bf16x2_rne(silu(g[2]) * u[2], silu(g[3]) * u[3]));
+          make_uint2(bf16x2_rne(silu(g[0]) * u[0], silu(g[1]) * u[1]),
+                     bf16x2_rne(silu(g[2]) * u[2], silu(g[3]) * u[3]));
     }
     __syncthreads();  // before the sums are overwritten
   }
@@ -510,7 +514,8 @@ __global__ __launch_bounds__(512) void down_wide_kernel(MoeArgs a, const uint8_t
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = blockIdx.y, n0 = (blockIdx.x * 8 + wave) * 16 * RT, nkb = a.I / 128;
-  // waves past the last column (H may be an odd number of 128s) repeat it: they pass the barriers and store nothing
+  // waves past the last column (H may be an odd number of 128s) repeat it: they
+  // pass the barriers and store nothing
   const int n = min(n0, a.H - 16 * RT);
   const int rows = rows_of_expert(a.ids, a.T * a.k, e, list, scratch);
 
@@ -582,13 +587,15 @@ struct MoeBuffers {
 // `reached`: about how many experts the tokens reach.
 template <int XL, bool RAW, class S>
 hipError_t down_few(const MoeArgs& a, const MoeBuffers& b, double reached, hipStream_t stream) {
-  constexpr int W = RAW && XL <= 2 ? 16 : 8, D = RAW && XL != 2 ? 2 : 1, lds = W * D * rows_stage_bytes<1, 1, RAW, XL>();
+  constexpr int W = RAW && XL <= 2 ? 16 : 8, D = RAW && XL != 2 ? 2 : 1;
+  constexpr int lds = W * D * rows_stage_bytes<1, 1, RAW, XL>();
   static_assert(lds >= W * 1024, "the waves' sums fit");
   static std::atomic<uint64_t> raised{0};
   const auto k = &down_few_kernel<W, XL, D, RAW, S>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), lds, &raised)) return e;
-  // as many parts as leave a wave a few rounds of loads, up to one workgroup per CU where only one fits, else two (four
-  // tokens, 28 experts of 1024: 2 parts 42 us, 3 parts 47; 16 tokens, 56 experts: 4 parts 80, 5 parts 84, 6 parts 82)
+  // as many parts as leave a wave a few rounds of loads, up to one workgroup per
+  // CU where only one fits, else two (four tokens, 28 experts of 1024: 2 parts 42
+  // us, 3 parts 47; 16 tokens, 56 experts: 4 parts 80, 5 parts 84, 6 parts 82)
   const int columns = a.H / 16, most = (RAW && XL == 1 ? 256 : 512) / columns;
   int parts = (int)(reached * (a.I / 128) / (W * D * (W == 16 ? 2 : 4)));
   if (parts > most) parts = most;
@@ -641,11 +648,13 @@ hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
 
 template <class S>
 hipError_t moe(const MoeArgs& a, MoeBuffers b, hipStream_t stream) {
-  // how many experts the tokens reach, if each is as likely as the next; with fewer than 64 workgroups the wide gate/up
-  // kernel leaves too many CUs idle (14 tokens, 9 experts of 1664 x 256, 88 workgroups: narrow 43 us, wide 24).  Up to 8
-  // tokens the narrow one is as fast at any number (8 tokens, 128 experts of 768: 60 us, wide 67; 16 tokens, 64 experts
-  // of 1024: 112 and 93), but it quantizes x again for each 16 columns, which amax / 448 scales make dearer (8 tokens
-  // 73 us, wide 64)
+  // how many experts the tokens reach, if each is as likely as the next; with
+  // fewer than 64 workgroups the wide gate/up kernel leaves too many CUs idle
+  // (14 tokens, 9 experts of 1664 x 256, 88 workgroups: narrow 43 us, wide 24).
+  // Up to 8 tokens the narrow one is as fast at any number (8 tokens, 128 experts
+  // of 768: 60 us, wide 67; 16 tokens, 64 experts of 1024: 112 and 93), but it
+  // quantizes x again for each 16 columns, which amax / 448 scales make dearer
+  // (8 tokens 73 us, wide 64)
   double missed = 1.0;
   for (int t = 0; t < a.T; ++t) missed *= 1.0 - (double)a.k / a.E;
   const double reached = a.E * (1.0 - missed);
@@ -677,8 +686,9 @@ hipError_t moe(const MoeArgs& a, MoeBuffers b, hipStream_t stream) {
     if (hipError_t e = gate_up_wide<1, S>(a, b, stream)) return e;
     return a.T <= 8 ? down_few<1, false, S>(a, b, reached, stream) : down_few<2, false, S>(a, b, reached, stream);
   }
-  // of an expert, on average: tiles for about twice as many, for few experts have more (64 experts, k 8; one, two, four
-  // tiles at most: 64 tokens 90, 97, - us; 100 tokens 119, 107, 107; 200 tokens -, 115, 104)
+  // of an expert, on average: tiles for about twice as many, for few experts have
+  // more (64 experts, k 8; one, two, four tiles at most: 64 tokens 90, 97, - us;
+  // 100 tokens 119, 107, 107; 200 tokens -, 115, 104)
   const int rows = a.T * a.k / a.E;
   if (rows <= 8) return moe_wide<1, S>(a, b, stream);
   return rows <= 20 ? moe_wide<2, S>(a, b, stream) : moe_wide<4, S>(a, b, stream);

@@ -22,6 +22,7 @@ namespace fp8blk {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kLaunch = int64_t(1) << 24;  // tokens of one launch, which has fewer than 2^32 threads
 
 template <class T>
 __device__ __forceinline__ float to_f32(T v);
@@ -111,19 +112,27 @@ template <int LANES, int NI, class L>
 hipError_t forward(int64_t T, int E, int k, const void* logits, int64_t ld, bool renorm, int32_t* ids, float* weights,
                    hipStream_t stream) {
   constexpr int per = kThreads / LANES;
-  hipLaunchKernelGGL((route_kernel<LANES, NI, L>), dim3((uint32_t)((T + per - 1) / per)), dim3(kThreads), 0, stream, T,
-                     E, k, static_cast<const L*>(logits), ld, renorm, ids, weights);
-  return hipGetLastError();
+  for (int64_t t = 0; t < T; t += kLaunch) {
+    const int64_t n = T - t < kLaunch ? T - t : kLaunch;
+    hipLaunchKernelGGL((route_kernel<LANES, NI, L>), dim3((uint32_t)((n + per - 1) / per)), dim3(kThreads), 0, stream,
+                       n, E, k, static_cast<const L*>(logits) + t * ld, ld, renorm, ids + t * k, weights + t * k);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 template <int LANES, int NI, class L>
 hipError_t backward(int64_t T, int E, int k, const void* logits, int64_t ld, const int32_t* ids, const float* g,
                     bool renorm, void* dlogits, int64_t ld_d, hipStream_t stream) {
   constexpr int per = kThreads / LANES;
-  hipLaunchKernelGGL((route_backward_kernel<LANES, NI, L>), dim3((uint32_t)((T + per - 1) / per)), dim3(kThreads), 0,
-                     stream, T, E, k, static_cast<const L*>(logits), ld, ids, g, renorm, static_cast<L*>(dlogits),
-                     ld_d);
-  return hipGetLastError();
+  for (int64_t t = 0; t < T; t += kLaunch) {
+    const int64_t n = T - t < kLaunch ? T - t : kLaunch;
+    hipLaunchKernelGGL((route_backward_kernel<LANES, NI, L>), dim3((uint32_t)((n + per - 1) / per)), dim3(kThreads), 0,
+                       stream, n, E, k, static_cast<const L*>(logits) + t * ld, ld, ids + t * k, g + t * k, renorm,
+                       static_cast<L*>(dlogits) + t * ld_d, ld_d);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace

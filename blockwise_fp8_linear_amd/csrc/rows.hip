@@ -101,8 +101,9 @@ hipError_t launch(int64_t M, int64_t N, int64_t K, const void* x, int64_t row_by
 // 128, 256 x 64 and 256 x 128 measured slower: 1024 x 4096 x 2048 16.9 us, and
 // 23.1, 18.6, 20.2, 28.7.
 constexpr int kWideTiles = 4;
-__global__ __launch_bounds__(512) void linear_wide_kernel(int64_t M, int64_t N, int64_t K, const uint8_t* __restrict__ q,
-                                                          const float* __restrict__ xs, const uint8_t* __restrict__ qw,
+__global__ __launch_bounds__(512) void linear_wide_kernel(int64_t M, int64_t N, int64_t K,
+                                                          const uint8_t* __restrict__ q, const float* __restrict__ xs,
+                                                          const uint8_t* __restrict__ qw,
                                                           const float* __restrict__ sw, RowsOut out) {
   extern __shared__ uint8_t lds[];
   constexpr int TT = kWideTiles;
@@ -124,22 +125,26 @@ __global__ __launch_bounds__(512) void linear_wide_kernel(int64_t M, int64_t N, 
 
 // ---------------------------------------------------------------------------
 // Codes of all rows of x, with the scales transposed ([K / 128][M]): what the
-// tiles of several rows load.  16 lanes per group of 128.
+// tiles of several rows load.  16 lanes per group of 128, which take the next
+// ones where there are more than kQuantGrid workgroups' (a launch has fewer
+// than 2^32 threads).
 // ---------------------------------------------------------------------------
+constexpr int64_t kQuantGrid = 65536;
 template <class S>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t M, int nkb, const uint16_t* __restrict__ x,
                                                             int64_t ld_x, uint8_t* __restrict__ q,
                                                             float* __restrict__ s) {
-  const int64_t u = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4), m = u / nkb;
-  const int l16 = threadIdx.x & 15, g = (int)(u - m * nkb);
-  if (m >= M) return;
-  const u32x4 v = *reinterpret_cast<const u32x4*>(x + m * ld_x + g * 128 + l16 * 8);
-  uint32_t a = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
-  a = row16_max(max(a & 0xFFFFu, a >> 16));
-  const S sc(a);
-  *reinterpret_cast<uint2*>(q + (m * nkb + g) * 128 + l16 * 8) =
-      make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
-  if (l16 == 0) s[g * M + m] = sc.s;
+  const int l16 = threadIdx.x & 15;
+  for (int64_t u = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); u < M * nkb; u += (int64_t)gridDim.x * 16) {
+    const int64_t m = u / nkb;
+    const int g = (int)(u - m * nkb);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(x + m * ld_x + g * 128 + l16 * 8);
+    uint32_t a = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
+    a = row16_max(max(a & 0xFFFFu, a >> 16));
+    const S sc(a);
+    *reinterpret_cast<uint2*>(q + u * 128 + l16 * 8) = make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
+    if (l16 == 0) s[g * M + m] = sc.s;
+  }
 }
 
 // Tiles are chosen so that a launch has about one workgroup of eight waves per
@@ -184,8 +189,8 @@ hipError_t launch_wide(int64_t M, int64_t N, int64_t K, const uint8_t* q, const 
 // (4, 1) 5.1; 128 x 4096 (4, 2) 6.0 and (2, 2) 6.6; 256 x 4096 (4, 4) 8.2 and
 // (4, 2) 9.9.  Where all have more, smaller workgroups of (3, 2): 64 x 12288
 // 10.4 and (4, 4) 11.4; 96 x 12288 12.0 and (4, 2) 13.3.  Above kExactRows
-// rows, and with 200 workgroups of it, the wide kernel: 512 x 4096 12.8 and 16.6, 1467
-// x 2560 (K 6400) 44 and 73; with fewer, 333 x 2048 11.4 and 8.3.
+// rows, and with 200 workgroups of it, the wide kernel: 512 x 4096 12.8 and
+// 16.6, 1467 x 2560 (K 6400) 44 and 73; with fewer, 333 x 2048 11.4 and 8.3.
 hipError_t launch_codes(int64_t M, int64_t N, int64_t K, const uint8_t* q, const float* s, const uint8_t* qw,
                         const float* sw, RowsOut out, hipStream_t stream) {
   const int64_t tiles = N / 16, m1 = (M + 15) / 16, m2 = (M + 31) / 32, m4 = (M + 63) / 64;
@@ -211,8 +216,9 @@ hipError_t launch_scale(int64_t M, int64_t N, int64_t K, const uint16_t* x, int6
   const int nkb = (int)(K / 128);
   uint8_t* q = static_cast<uint8_t*>(ws);
   float* s = reinterpret_cast<float*>(q + rows_scales_at(M, K));
-  hipLaunchKernelGGL(quantize_rows_kernel<S>, dim3((uint32_t)((M * nkb + 15) / 16)), dim3(256), 0, stream, M, nkb, x,
-                     ld_x, q, s);
+  const int64_t grid = (M * nkb + 15) / 16;
+  hipLaunchKernelGGL(quantize_rows_kernel<S>, dim3((uint32_t)(grid < kQuantGrid ? grid : kQuantGrid)), dim3(256), 0,
+                     stream, M, nkb, x, ld_x, q, s);
   if (hipError_t e = hipGetLastError()) return e;
   return launch_codes(M, N, K, q, s, qw, sw, out, stream);
 }

@@ -33,14 +33,16 @@ def _run(M, N, K, mode, x=None, seed=0, ld=None):
     return wide[:, :K], (dev(qw), dev(sw)), host(y[:M]), (moe_ref.dequant_rows(x, mode), moe_ref.dequant_block(qw, sw))
 
 
-M_ALL = [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 96, 100, 127, 128, 129, 200, 255, 256, 257, 383, 513, 700]
+M_ALL = [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 96, 100, 127, 128, 129, 200, 255, 256, 257, 383, 513,
+         700]
 SHAPES = [(1, 128, 128), (5, 128, 1152), (3, 1152, 128), (16, 256, 2048), (1, 2048, 6144), (40, 384, 768),
           (7, 8192, 256), (20, 12288, 128), (33, 16384, 256), (64, 640, 384), (130, 8192, 128),
           (700, 8192, 128), (475, 8192, 256), (1100, 4096, 128), (2048, 2048, 128),
           (1500, 8192, 512), (1200, 8192, 512), (2300, 8192, 128), (513, 3328, 640), (128, 25600, 128)]
 
 
-@pytest.mark.parametrize("M,N,K,mode", [(m, 256, 384, POW2) for m in M_ALL] + [(m, 384, 256, FP32) for m in M_ALL[::3]] +
+@pytest.mark.parametrize("M,N,K,mode", [(m, 256, 384, POW2) for m in M_ALL] +
+                         [(m, 384, 256, FP32) for m in M_ALL[::3]] +
                          [(*s, mode) for s in SHAPES for mode in (POW2, FP32)])
 def test_linear(M, N, K, mode):
     import torch
@@ -94,6 +96,65 @@ def test_quantizes_as_the_quantizer(M, mode):
     y, want = np.where(over, 0, y), np.where(over, 0, want)
     # one product per output: the scale product's rounding and its own (an underflow is off by the least subnormal)
     assert np.all(np.abs(y - want) <= 4 * 2.0 ** -24 * np.abs(want) + 2.0 ** -149 * 448 * 448)
+
+
+def test_many_rows_of_few_columns():
+    """More groups than one launch of the quantizer has places for: the first
+    and the last rows against the product, and the last as a call of their
+    own."""
+    import torch
+    M, N, K = 45000, 128, 4096
+    x = synth.normal_bf16((64, K), 1.0, 70)
+    w = synth.normal_bf16((N, K), 0.02, 71)
+    qw, _, sw = oracle.quantize_block(w, transpose=False)
+    xt = torch.zeros((M, K), device="cuda", dtype=torch.bfloat16)
+    xt[:32], xt[-32:] = dev_bf16(x[:32]), dev_bf16(x[32:])
+    y = fb.fp8_linear(xt, dev(qw), dev(sw), out_dtype=torch.float32)
+    assert not bool(y[32:-32].any())
+    xd, wd = moe_ref.dequant_rows(x, POW2), moe_ref.dequant_block(qw, sw)
+    ref, _ = moe_ref.product(xd, wd)
+    bound = RTOL * (np.abs(xd) @ np.abs(wd).T)
+    assert np.all(np.abs(np.concatenate([host(y[:32]), host(y[-32:])]) - ref) <= bound)
+
+
+def test_two_threads_at_once():
+    """Calls from two host threads, each on its own stream with its own
+    workspaces, give what either gives alone."""
+    import threading
+    import torch
+    E, H, I, k = 12, 256, 384, 3
+    q1, _, s1 = fb.fp8_quantize_block(dev_bf16(synth.normal_bf16((E * 2 * I, H), 0.06, 72)), transpose=False)
+    q2, _, s2 = fb.fp8_quantize_block(dev_bf16(synth.normal_bf16((E * H, I), 0.06, 73)), transpose=False)
+    exps = (q1.view(E, 2 * I, H), s1.view(E, 2 * I // 128, H // 128), q2.view(E, H, I), s2.view(E, H // 128, I // 128))
+    qw, _, sw = fb.fp8_quantize_block(dev_bf16(synth.normal_bf16((512, H), 0.06, 74)), transpose=False)
+    wr = dev_bf16(synth.normal_bf16((E, H), 0.3, 75))
+    xs = [dev_bf16(synth.normal_bf16((T, H), 1.0, 76, T)) for T in (3, 12, 60, 200)]
+
+    def step(x):
+        lg = fb.fp8_linear(x, qw, sw, out_dtype=torch.float32)
+        ids, w = fb.fp8_moe_route(lg, 4)
+        return [lg, ids, w, fb.fp8_moe_route_backward(lg, ids, w), fb.fp8_moe_layer(x, wr, *exps, k)]
+
+    want = [step(x) for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def run(order):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = [(i, step(xs[i])) for i in order]
+                    torch.cuda.current_stream().synchronize()
+                    bad.extend(i for i, g in got if not all(torch.equal(a, b) for a, b in zip(g, want[i])))
+        except Exception as e:  # noqa: BLE001 -- reported by the test's own thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=run, args=(o,)) for o in ([0, 1, 2, 3], [3, 1, 0, 2])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert bad == []
 
 
 def test_equals_the_quantizer_and_fprop():

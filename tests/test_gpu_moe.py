@@ -112,6 +112,23 @@ def test_route_gradient_against_differences(renorm):
     assert np.all(np.abs(d - num) <= lim)
 
 
+def test_route_more_tokens_than_a_launch():
+    import torch
+    T, tail = 2 ** 24 + 5, slice(-40, None)
+    lg = torch.randn((T, 3), device="cuda", dtype=torch.bfloat16)
+    lg[5] = -torch.inf
+    ids, w = fb.fp8_moe_route(lg, 2, renormalize=False)
+    assert int(ids[5].max()) == -1
+    first = lg.float().argmax(1)                             # (of equal ones any)
+    rest = torch.arange(T, device="cuda") != 5
+    assert bool((lg.gather(1, ids.long().clamp(min=0))[:, 0] == lg.gather(1, first[:, None])[:, 0])[rest].all())
+    g = torch.randn((T, 2), device="cuda")
+    d = fb.fp8_moe_route_backward(lg, ids, g, renormalize=False)
+    alone = fb.fp8_moe_route(lg[tail], 2, renormalize=False)
+    assert torch.equal(ids[tail], alone[0]) and torch.equal(w[tail], alone[1])
+    assert torch.equal(d[tail], fb.fp8_moe_route_backward(lg[tail], *(t[tail] for t in (ids, g)), renormalize=False))
+
+
 def test_route_infinities_and_lowest():
     inf, low = np.inf, np.finfo(np.float32).min
     v = np.array([[inf, 1.0, inf, 0.0], [low, low, low, low], [low, 3.4e38, 0.0, -inf], [np.nan, inf, -inf, np.nan]],
@@ -209,7 +226,8 @@ def _exact_case(T, E, k, seed, H=256, I=256):
         for j, e in enumerate(ids[t]):
             y[t] += float(w[t, j]) * (Wd[e].astype(np.float64) @ ((G[e] @ x[t]).astype(np.float64) * (Uw[e] @ x[t])))
     return (dev_bf16(bits(x)), dev(ids), dev(w), dev(q1.reshape(E, 2 * I, H)),
-            dev(s1.reshape(E, 2 * I // 128, H // 128)), dev(q2.reshape(E, H, I)), dev(s2.reshape(E, H // 128, I // 128))), y
+            dev(s1.reshape(E, 2 * I // 128, H // 128)), dev(q2.reshape(E, H, I)),
+            dev(s2.reshape(E, H // 128, I // 128))), y
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 3, 2), (7, 9, 4), (16, 2, 2), (40, 5, 3), (100, 1, 1), (300, 4, 2)])

@@ -248,6 +248,8 @@ def test_binding_route(host_stand_ins):
     refused("ids: expected shape", fb.fp8_moe_route, lg, 2, ids=z((5, 3), i32))
     refused("ids: expected torch.int32", fb.fp8_moe_route, lg, 2, ids=z((5, 2), torch.int64))
     refused("weights: expected torch.float32", fb.fp8_moe_route, lg, 2, weights=z((5, 2), bf16))
+    refused("topk", fb.fp8_moe_route, lg, 2 ** 32 + 2)      # not the 2 that an int would keep of it
+    refused("topk", fb.fp8_moe_route_backward, lg, z((5, 1), i32).expand(5, 2 ** 32 + 2), z((5, 1), f32))
     ids, g = z((5, 2), i32), z((5, 2), f32)
     refused("ids: expected a 2-dim", fb.fp8_moe_route_backward, lg, z((10,), i32), g)
     refused("ids: expected shape", fb.fp8_moe_route_backward, lg, z((4, 2), i32), g)
@@ -260,7 +262,8 @@ def test_binding_route(host_stand_ins):
 def test_binding_experts(host_stand_ins):
     T, H, I, E, k = 3, 256, 128, 4, 2
     x, ids, w = z((T, H), bf16), z((T, k), i32), z((T, k), f32)
-    good = [z((E, 2 * I, H), u8), z((E, 2 * I // 128, H // 128), f32), z((E, H, I), u8), z((E, H // 128, I // 128), f32)]
+    good = [z((E, 2 * I, H), u8), z((E, 2 * I // 128, H // 128), f32), z((E, H, I), u8),
+            z((E, H // 128, I // 128), f32)]
     wrong = [z((E, 2 * I, H // 2), u8), z((E, 1, 2), f32), z((E, I, H), u8), z((E - 1, 2, 1), f32)]
     for i, name in enumerate(("qw1", "sw1", "qw2", "sw2")):
         e = list(good)
@@ -276,6 +279,7 @@ def test_binding_experts(host_stand_ins):
     refused("wr: expected shape", fb.fp8_moe_layer, x, z((E + 1, H), bf16), *good, k)
     refused("wr: expected torch.bfloat16", fb.fp8_moe_layer, x, z((E, H), f32), *good, k)
     refused("ids: expected shape", fb.fp8_moe_layer, x, z((E, H), bf16), *good, k, ids=z((T, k + 1), i32))
+    refused("topk", fb.fp8_moe_layer, x, z((E, H), bf16), *good, 2 ** 32 + k)
 
 
 def test_binding_refuses_host_tensors_and_other_devices():
