@@ -244,36 +244,39 @@ __device__ __forceinline__ void rows_product(uint8_t* lds, const uint8_t* const 
 // acc[rt][tt] += all blocks of RT 16-row weight tiles (each wave its own) times
 // the TT 16-token tiles that the workgroup's eight waves share.  Every thread
 // of the workgroup calls it, with the same x, xs and nkb.
-//   The blocks go through two slots in LDS, one multiplied while the other
-// fills: each wave loads its own weight tiles and an eighth of the tokens'
-// codes (some twice where there are fewer loads than waves).  One barrier per
-// block says that the block has landed for everyone and that the slot before it
-// may be filled again.  (Three or four slots measured slower at every size:
-// 256 tokens through 64 experts 139 instead of 124 us.  The loads of one block
-// and CU are 32 KiB, and more LDS leaves fewer workgroups per CU.)
+//   The blocks go through SLOTS slots in LDS, one multiplied while the others
+// fill: each wave loads its own weight tiles and an eighth of the tokens' codes
+// (some twice where there are fewer loads than waves).  One barrier per block
+// says that the block has landed for everyone and that the slot before it may be
+// filled again.  (More than two slots pay where a CU has one workgroup anyway:
+// the launchers' choice.)
 //   FP8: on the fp8 matrix instruction instead of the bf16 one.
-//   Scales: the weights' in registers, lane i holding block i's; the tokens' in
-// LDS, [block][token]; both for 64 blocks at a time.
+//   Scales, for kPanel blocks at a time: the weights' in registers, lane i
+// holding block i's; the tokens' in LDS, [block][token], by direct loads that
+// the first block's wait covers.  (For 64 blocks at a time two tiles of tokens
+// would not fit a CU twice: 150 tokens, 64 experts of 1024 101 us, so 94.)
 //   xoff: the byte offset, from x, of the chunk that this lane's load brings:
 // load wave % (2 TT) of the tokens' codes, two of them to a tile;
-//   xscale(token of the TT tiles, block) gives a scale from memory.
+//   xs: the tokens' scales in memory, that of token i of the tiles in block b at
+// b xs_b + xrow(i), which for kPanel blocks stays within 2^29.
 // ---------------------------------------------------------------------------
-constexpr int kPanel = 64;
+constexpr int kPanel = 32;
 
-template <int RT, int TT>
+template <int RT, int TT, int SLOTS>
 __device__ __host__ constexpr int rows_ring_bytes() {
-  return 2 * (8 * RT + TT) * kCodeTile + kPanel * 16 * TT * 4;
+  return SLOTS * (8 * RT + TT) * kCodeTile + kPanel * 16 * TT * 4;
 }
 
-template <int RT, int TT, bool FP8 = false, class XScale>
+template <int RT, int TT, int SLOTS, bool FP8 = false, class XRow>
 __device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w)[RT], const float* const (&sw)[RT],
-                                          int64_t K, const uint8_t* x, uint32_t xoff, XScale xscale, int nkb,
+                                          int64_t K, const uint8_t* x, uint32_t xoff, const float* xs,
+                                          int64_t xs_b, XRow xrow, int nkb,
                                           v4f (&acc)[RT][TT]) {
-  constexpr int SLOT = (8 * RT + TT) * kCodeTile;
+  constexpr int SLOT = (8 * RT + TT) * kCodeTile, LOADS = 2 * RT + 1;  // of a block and wave
   const uint32_t lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), xload = wave % (2 * TT);
   const uint32_t at = lds_offset(lds);
-  float* const scales = reinterpret_cast<float*>(lds + 2 * SLOT);
+  float* const scales = reinterpret_cast<float*>(lds + SLOTS * SLOT);
   const uint32_t woff[2] = {(uint32_t)(code_row(lane, 0) * K) + code_chunk(lane, 0),
                             (uint32_t)(code_row(lane, 1) * K) + code_chunk(lane, 1)};
   for (int p0 = 0; p0 < nkb; p0 += kPanel) {
@@ -282,7 +285,7 @@ __device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) s[rt] = sw[rt][p0 + min((int)lane, nb - 1)];
     const auto issue = [&](int b) {
-      const uint32_t slot = at + (b & 1) * SLOT;
+      const uint32_t slot = at + b % SLOTS * SLOT;
       const int64_t k = (int64_t)(p0 + b) * 128;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
@@ -291,15 +294,29 @@ __device__ __forceinline__ void rows_ring(uint8_t* lds, const uint8_t* const (&w
       }
       dma16(x + k, xoff, slot + 8 * RT * kCodeTile + xload * 1024);
     };
-    __syncthreads();  // the scales and slots before have been read
+    __syncthreads();  // the scales and slots before have been read, stores are done
     issue(0);
-    // the tokens' scales come while the first block does
-    for (int i = threadIdx.x; i < nb * 16 * TT; i += 512) scales[i] = xscale(i % (16 * TT), p0 + i / (16 * TT));
+    // the tokens' scales come with the first block
+    const uint8_t* const panel = reinterpret_cast<const uint8_t*>(xs + p0 * xs_b);
+    for (int i = wave * 64; i < nb * 16 * TT; i += 512) {
+      const int l = min(i + (int)lane, nb * 16 * TT - 1);
+      dma4(panel, (uint32_t)(l / (16 * TT) * xs_b + xrow(l % (16 * TT))) * 4, lds_offset(scales) + i * 4);
+    }
+#pragma unroll
+    for (int b = 1; b < SLOTS - 1; ++b)
+      if (b < nb) issue(b);
+    // the weights' scales are there before the loop, where the compiler's wait
+    // for them would be one for every load in flight
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) asm volatile("" ::"v"(s[rt]));
     for (int b = 0; b < nb; ++b) {
-      wait_vmcnt<0>();
+      if (SLOTS > 2 && b + SLOTS - 2 < nb)
+        wait_vmcnt<(SLOTS - 2) * LOADS>();  // the blocks after this one may still be on their way
+      else
+        wait_vmcnt<0>();
       lds_barrier();
-      if (b + 1 < nb) issue(b + 1);
-      const uint8_t* slot = lds + (b & 1) * SLOT;
+      if (b + SLOTS - 1 < nb) issue(b + SLOTS - 1);
+      const uint8_t* slot = lds + b % SLOTS * SLOT;
       const auto operand = [&](const uint8_t* tile) {
         if constexpr (FP8) return read_codes(tile, r, c);
         else return decode(read_codes(tile, r, c));

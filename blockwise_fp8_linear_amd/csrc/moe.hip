@@ -191,6 +191,7 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // has 64 (20 and 27 us for both products).
 // ---------------------------------------------------------------------------
 constexpr int kFew = 16;
+constexpr int kCus = 256;
 // About the most workgroups of gate/up; beyond, each takes several columns, so
 // that its start counts less (4 tokens, 18 experts of 1408 x 256: 44 us without,
 // 35 with; at 768 as well, but 8 tokens, 51 experts of 768 x 2048 60 and 62).
@@ -440,23 +441,23 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(MoeArgs a, const float* 
 // eight waves of a workgroup share the tokens' codes in LDS.  128 columns of I
 // in one workgroup are one group of h, so h leaves quantized.  TMAX tiles of 16
 // rows at once; an expert with more rows is read again (from L2 or the
-// memory-side cache) for the rest.
+// memory-side cache) for the rest, by the same workgroup or (gridDim.z) another.
 //   40 tokens, 121 of 128 experts of 768 reached: gate/up 69 us (5.5 TB/s),
 //   down 35 (5.4); 256 tokens, 64 experts of 1024: 59 (4.5) and 35 (3.8).
 // ---------------------------------------------------------------------------
 // Dynamic LDS: the two slots for the most tiles, then the list of rows.
 constexpr int kMostRows = 8192;  // T k
-template <int RT, int TMAX>
-constexpr int kRing = rows_ring_bytes<RT, TMAX>();
+template <int RT, int TMAX, int SLOTS>
+constexpr int kRing = rows_ring_bytes<RT, TMAX, SLOTS>();
 
-template <int TMAX, class S>
+template <int TMAX, int SLOTS, class S>
 __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint8_t* __restrict__ qx,
                                                            const float* __restrict__ sx, uint8_t* __restrict__ qh,
                                                            float* __restrict__ sh) {
   extern __shared__ uint8_t lds[];
   __shared__ int scratch[4 * 8];
   __shared__ uint32_t amax[8][16 * TMAX];
-  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<2, TMAX>);
+  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<2, TMAX, SLOTS>);
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = blockIdx.y, n0 = blockIdx.x * 128 + wave * 16, nkb = a.H / 128;
@@ -466,7 +467,7 @@ __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint
   const float* sbase = a.sw1 + (int64_t)e * (2 * a.I / 128) * nkb;
   const uint8_t* const wp[2] = {base + (int64_t)n0 * a.H, base + (int64_t)(a.I + n0) * a.H};
   const float* const sp[2] = {sbase + n0 / 128 * nkb, sbase + (a.I + n0) / 128 * nkb};
-  for (int r0 = 0; r0 < rows; r0 += 16 * TMAX) {
+  for (int r0 = blockIdx.z * 16 * TMAX; r0 < rows; r0 += gridDim.z * 16 * TMAX) {
     with_tiles<TMAX>(rows - r0, [&](auto tag) {
       constexpr int TT = decltype(tag)::value;
       const int load = wave % (2 * TT), row = r0 + (load >> 1) * 16 + code_row(lane, load & 1);
@@ -474,9 +475,8 @@ __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint
       v4f acc[2][TT];
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) acc[0][tt] = acc[1][tt] = v4f{};
-      rows_ring<2, TT>(
-          lds, wp, sp, a.H, qx, xoff,
-          [&](int i, int b) { return sx[(int64_t)b * a.T + list[min(r0 + i, rows - 1)] / a.k]; }, nkb, acc);
+      rows_ring<2, TT, SLOTS>(
+          lds, wp, sp, a.H, qx, xoff, sx, a.T, [&](int i) { return list[min(r0 + i, rows - 1)] / a.k; }, nkb, acc);
       uint32_t h[TT][2];
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) {
@@ -505,12 +505,12 @@ __global__ __launch_bounds__(512) void gate_up_wide_kernel(MoeArgs a, const uint
   }
 }
 
-template <int RT, int TMAX>
+template <int RT, int TMAX, int SLOTS>
 __global__ __launch_bounds__(512) void down_wide_kernel(MoeArgs a, const uint8_t* __restrict__ qh,
                                                         const float* __restrict__ sh, float* __restrict__ partial) {
   extern __shared__ uint8_t lds[];
   __shared__ int scratch[4 * 8];
-  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<RT, TMAX>);
+  uint16_t* const list = reinterpret_cast<uint16_t*>(lds + kRing<RT, TMAX, SLOTS>);
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = blockIdx.y, n0 = (blockIdx.x * 8 + wave) * 16 * RT, nkb = a.I / 128;
@@ -528,7 +528,7 @@ __global__ __launch_bounds__(512) void down_wide_kernel(MoeArgs a, const uint8_t
     wp[rt] = base + (int64_t)rt * 16 * a.I;
     sp[rt] = s;
   }
-  for (int r0 = 0; r0 < rows; r0 += 16 * TMAX) {
+  for (int r0 = blockIdx.z * 16 * TMAX; r0 < rows; r0 += gridDim.z * 16 * TMAX) {
     with_tiles<TMAX>(rows - r0, [&](auto tag) {
       constexpr int TT = decltype(tag)::value;
       const int load = wave % (2 * TT), row = r0 + (load >> 1) * 16 + code_row(lane, load & 1);
@@ -538,9 +538,9 @@ __global__ __launch_bounds__(512) void down_wide_kernel(MoeArgs a, const uint8_t
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = v4f{};
-      rows_ring<RT, TT>(
-          lds, wp, sp, a.I, qh, xoff,
-          [&](int i, int b) { return sh[(int64_t)b * (a.T * a.k) + list[min(r0 + i, rows - 1)]]; }, nkb, acc);
+      rows_ring<RT, TT, SLOTS>(
+          lds, wp, sp, a.I, qh, xoff, sh, a.T * a.k, [&](int i) { return (int)list[min(r0 + i, rows - 1)]; }, nkb,
+          acc);
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) {
         const int row = r0 + tt * 16 + r;
@@ -622,26 +622,75 @@ hipError_t moe_few(const MoeArgs& a, const MoeBuffers& b, double reached, hipStr
   return down_few<XL, true, S>(a, b, reached, stream);
 }
 
-template <int TT, class S>
-hipError_t gate_up_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
+// How a wide kernel's workgroups take the rows of an expert: `tiles` of 16 at a
+// time, `parts` workgroups in turn.
+struct RowSplit {
+  int tiles, parts;
+};
+// `columns`: workgroups of an expert's columns.  Tiles for about twice as many
+// rows as an expert has on average, since some have more (64 experts, k 8; one,
+// two, four tiles at most: 64 tokens 90, 97, - us; 100 tokens 119, 107, 107; 200
+// tokens -, 115, 104).  Where the columns leave CUs idle, fewer tiles in more
+// workgroups, which read the weights again, from a cache (256 tokens, 4 experts
+// of 512 x 1024: 80 us without, 26 with; 512 tokens, 64 of 256 x 2048 89 and 75).
+RowSplit row_split(const MoeArgs& a, int columns) {
+  const int mean = a.T * a.k / a.E, rows = 2 * mean < a.T ? 2 * mean : a.T;
+  const int most = mean <= 8 ? 1 : mean <= 20 ? 2 : 4, fit = kCus / (columns * a.E);
+  for (int tiles = 1;; tiles *= 2) {
+    const int parts = (rows + 16 * tiles - 1) / (16 * tiles);
+    if (parts <= fit) return RowSplit{tiles, parts < 1 ? 1 : parts};
+    if (tiles == most) return RowSplit{tiles, fit < 1 ? 1 : fit};
+  }
+}
+
+// Slots of the ring: as many as fit while each CU has one workgroup (17 tokens,
+// 8 experts of 6144: 86 us, with two slots 106); beyond, two (256 tokens, 64
+// experts of 1024, three slots of four tiles: 127 us, two 120).
+template <int TT, int SLOTS, class S>
+hipError_t gate_up_launch(const MoeArgs& a, const MoeBuffers& b, int parts, hipStream_t stream) {
   static std::atomic<uint64_t> raised{0};
-  const auto k = &gate_up_wide_kernel<TT, S>;
-  constexpr int ring = kRing<2, TT>;
+  const auto k = &gate_up_wide_kernel<TT, SLOTS, S>;
+  constexpr int ring = kRing<2, TT, SLOTS>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), ring + kMostRows * 2, &raised)) return e;
-  hipLaunchKernelGGL(k, dim3(a.I / 128, a.E), dim3(512), ring + a.T * a.k * 2, stream, a, b.qx, b.sx, b.h, b.sh);
+  hipLaunchKernelGGL(k, dim3(a.I / 128, a.E, parts), dim3(512), ring + a.T * a.k * 2, stream, a, b.qx, b.sx, b.h, b.sh);
   return hipGetLastError();
 }
 
 template <int TT, class S>
-hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
-  if (hipError_t e = gate_up_wide<TT, S>(a, b, stream)) return e;
+hipError_t gate_up_wide(const MoeArgs& a, const MoeBuffers& b, int parts, hipStream_t stream) {
+  if (a.I / 128 * (int64_t)a.E * parts > kCus) return gate_up_launch<TT, 2, S>(a, b, parts, stream);
+  return gate_up_launch<TT, TT == 1 ? 4 : 3, S>(a, b, parts, stream);
+}
+
+template <int RT, int TT, int SLOTS>
+hipError_t down_launch(const MoeArgs& a, const MoeBuffers& b, int parts, hipStream_t stream) {
   static std::atomic<uint64_t> raised{0};
-  constexpr int RT = TT == 1 ? 2 : 1, ring = kRing<RT, TT>;
-  const auto k = &down_wide_kernel<RT, TT>;
+  const auto k = &down_wide_kernel<RT, TT, SLOTS>;
+  constexpr int ring = kRing<RT, TT, SLOTS>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), ring + kMostRows * 2, &raised)) return e;
-  hipLaunchKernelGGL(k, dim3((a.H + 128 * RT - 1) / (128 * RT), a.E), dim3(512), ring + a.T * a.k * 2, stream, a, b.h,
-                     b.sh, b.partial);
-  if (hipError_t e = hipGetLastError()) return e;
+  hipLaunchKernelGGL(k, dim3((a.H + 128 * RT - 1) / (128 * RT), a.E, parts), dim3(512), ring + a.T * a.k * 2, stream, a,
+                     b.h, b.sh, b.partial);
+  return hipGetLastError();
+}
+
+template <int RT, int TT>
+hipError_t down_wide(const MoeArgs& a, const MoeBuffers& b, int parts, hipStream_t stream) {
+  const int columns = (a.H + 128 * RT - 1) / (128 * RT);
+  if (columns * (int64_t)a.E * parts > kCus) return down_launch<RT, TT, 2>(a, b, parts, stream);
+  return down_launch<RT, TT, RT == 1 ? 4 : 3>(a, b, parts, stream);
+}
+
+template <class S>
+hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
+  const RowSplit g = row_split(a, a.I / 128), d = row_split(a, a.H / 128);
+  if (hipError_t e = g.tiles == 1   ? gate_up_wide<1, S>(a, b, g.parts, stream)
+                     : g.tiles == 2 ? gate_up_wide<2, S>(a, b, g.parts, stream)
+                                    : gate_up_wide<4, S>(a, b, g.parts, stream))
+    return e;
+  if (hipError_t e = d.tiles == 1   ? down_wide<2, 1>(a, b, d.parts, stream)
+                     : d.tiles == 2 ? down_wide<1, 2>(a, b, d.parts, stream)
+                                    : down_wide<1, 4>(a, b, d.parts, stream))
+    return e;
   hipLaunchKernelGGL(combine_kernel, dim3((a.T * (a.H / 4) + 255) / 256), dim3(256), 0, stream, a, b.partial);
   return hipGetLastError();
 }
@@ -683,15 +732,10 @@ hipError_t moe(const MoeArgs& a, MoeBuffers b, hipStream_t stream) {
     return a.T <= 8 ? moe_few<2, S>(a, b, reached, stream) : moe_few<4, S>(a, b, reached, stream);
   }
   if (a.T <= kFew) {
-    if (hipError_t e = gate_up_wide<1, S>(a, b, stream)) return e;
+    if (hipError_t e = gate_up_wide<1, S>(a, b, 1, stream)) return e;
     return a.T <= 8 ? down_few<1, false, S>(a, b, reached, stream) : down_few<2, false, S>(a, b, reached, stream);
   }
-  // of an expert, on average: tiles for about twice as many, for few experts have
-  // more (64 experts, k 8; one, two, four tiles at most: 64 tokens 90, 97, - us;
-  // 100 tokens 119, 107, 107; 200 tokens -, 115, 104)
-  const int rows = a.T * a.k / a.E;
-  if (rows <= 8) return moe_wide<1, S>(a, b, stream);
-  return rows <= 20 ? moe_wide<2, S>(a, b, stream) : moe_wide<4, S>(a, b, stream);
+  return moe_wide<S>(a, b, stream);
 }
 
 }  // namespace

@@ -21,6 +21,25 @@ __device__ __forceinline__ void store_rows(const RowsOut& out, int64_t at, const
   }
 }
 
+// The tile that a workgroup of a launch of columns x rows tiles takes.
+// Consecutive workgroups go to the eight XCDs in turn, each with an L2 of its
+// own: here every XCD gets a contiguous range of tiles in the order in which
+// neighbours share the larger operand, W (rows first) or x.  (Where the columns
+// are a multiple of eight the launch's own order keeps a column on one XCD.)
+// 470 x 3712 (K 4352) 30.0 us without and 25.4 with, 200 x 3712 22.5 and 19.3;
+// 12288 columns, a multiple, 130 rows 17.0 and 18.5.
+struct TilePlace {
+  uint32_t column, row;
+};
+__device__ __forceinline__ TilePlace tile_place(bool share_w) {
+  constexpr uint32_t kXcds = 8;
+  const uint32_t columns = gridDim.x, rows = gridDim.y;
+  if (rows == 1 || (share_w && columns % kXcds == 0)) return {blockIdx.x, blockIdx.y};
+  const uint32_t id = blockIdx.y * columns + blockIdx.x, n = columns * rows, xcd = id % kXcds;
+  const uint32_t at = xcd * (n / kXcds) + min(xcd, n % kXcds) + id / kXcds;
+  return share_w ? TilePlace{at / rows, at % rows} : TilePlace{at % columns, at / columns};
+}
+
 // One workgroup: 16 RT columns of y, 16 TT rows, the W waves splitting the
 // reduction (K / 128 blocks are few: two per wave at 2048, all in flight at
 // once).  RAW: xv is x in bf16 (ld_x elements apart) and quantized here;
@@ -33,7 +52,8 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(int64_t M, int64_t 
   extern __shared__ uint8_t lds[];  // the waves' areas; then their sums, [W][RT * TT][64] v4f
   const uint32_t lane = threadIdx.x & 63, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT), m0 = (int64_t)blockIdx.y * (16 * TT);
+  const TilePlace place = tile_place(M < N);
+  const int64_t n0 = (int64_t)place.column * (16 * RT), m0 = (int64_t)place.row * (16 * TT);
   const int nkb = (int)(K / 128), rows = (int)(M - m0 < 16 * TT ? M - m0 : 16 * TT);
 
   const uint8_t* wp[RT];
@@ -101,6 +121,7 @@ hipError_t launch(int64_t M, int64_t N, int64_t K, const void* x, int64_t row_by
 // 128, 256 x 64 and 256 x 128 measured slower: 1024 x 4096 x 2048 16.9 us, and
 // 23.1, 18.6, 20.2, 28.7.
 constexpr int kWideTiles = 4;
+template <int SLOTS>
 __global__ __launch_bounds__(512) void linear_wide_kernel(int64_t M, int64_t N, int64_t K,
                                                           const uint8_t* __restrict__ q, const float* __restrict__ xs,
                                                           const uint8_t* __restrict__ qw,
@@ -109,15 +130,16 @@ __global__ __launch_bounds__(512) void linear_wide_kernel(int64_t M, int64_t N, 
   constexpr int TT = kWideTiles;
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = ((int64_t)blockIdx.x * 8 + wave) * 16, m0 = (int64_t)blockIdx.y * 16 * TT;
+  const TilePlace place = tile_place(M < N);
+  const int64_t n0 = ((int64_t)place.column * 8 + wave) * 16, m0 = (int64_t)place.row * 16 * TT;
   const int nkb = (int)(K / 128), rows = (int)(M - m0 < 16 * TT ? M - m0 : 16 * TT);
   const uint8_t* const wp[1] = {qw + n0 * K};
   const float* const sp[1] = {sw + n0 / 128 * nkb};
   const int load = wave % (2 * TT), row = (load >> 1) * 16 + (int)code_row(lane, load & 1);
   const uint32_t xoff = (uint32_t)(min(row, rows - 1) * K) + code_chunk(lane, load & 1);
   v4f acc[1][TT] = {};
-  rows_ring<1, TT, true>(
-      lds, wp, sp, K, q + m0 * K, xoff, [&](int i, int b) { return xs[b * M + m0 + min(i, rows - 1)]; }, nkb, acc);
+  rows_ring<1, TT, SLOTS, true>(
+      lds, wp, sp, K, q + m0 * K, xoff, xs + m0, M, [&](int i) { return min(i, rows - 1); }, nkb, acc);
 #pragma unroll
   for (int tt = 0; tt < TT; ++tt)
     if (tt * 16 + r < rows) store_rows(out, (m0 + tt * 16 + r) * N + n0 + 4 * c, acc[0][tt]);
@@ -173,13 +195,15 @@ hipError_t launch_raw(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_
 #undef FP8_RAW
 }
 
+template <int SLOTS>
 hipError_t launch_wide(int64_t M, int64_t N, int64_t K, const uint8_t* q, const float* s, const uint8_t* qw,
                        const float* sw, RowsOut out, hipStream_t stream) {
-  constexpr int lds = rows_ring_bytes<1, kWideTiles>();
+  constexpr int lds = rows_ring_bytes<1, kWideTiles, SLOTS>();
   static std::atomic<uint64_t> raised{0};
-  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&linear_wide_kernel), lds, &raised)) return e;
+  const auto k = &linear_wide_kernel<SLOTS>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), lds, &raised)) return e;
   const dim3 grid((uint32_t)(N / 128), (uint32_t)((M + 16 * kWideTiles - 1) / (16 * kWideTiles)));
-  hipLaunchKernelGGL(linear_wide_kernel, grid, dim3(512), lds, stream, M, N, K, q, s, qw, sw, out);
+  hipLaunchKernelGGL(k, grid, dim3(512), lds, stream, M, N, K, q, s, qw, sw, out);
   return hipGetLastError();
 }
 
@@ -191,10 +215,15 @@ hipError_t launch_wide(int64_t M, int64_t N, int64_t K, const uint8_t* q, const 
 // 10.4 and (4, 4) 11.4; 96 x 12288 12.0 and (4, 2) 13.3.  Above kExactRows
 // rows, and with 200 workgroups of it, the wide kernel: 512 x 4096 12.8 and
 // 16.6, 1467 x 2560 (K 6400) 44 and 73; with fewer, 333 x 2048 11.4 and 8.3.
+// Its slots: four while each CU has one workgroup, 1000 x 2048 (K 6400) 34.0 and
+// with two 37.4; beyond, two, so that two fit (1467 x 2560: 45.0, three 48.6).
 hipError_t launch_codes(int64_t M, int64_t N, int64_t K, const uint8_t* q, const float* s, const uint8_t* qw,
                         const float* sw, RowsOut out, hipStream_t stream) {
   const int64_t tiles = N / 16, m1 = (M + 15) / 16, m2 = (M + 31) / 32, m4 = (M + 63) / 64;
-  if (M > kExactRows && tiles / 8 * m4 >= 200) return launch_wide(M, N, K, q, s, qw, sw, out, stream);
+  const int64_t wide = tiles / 8 * m4;
+  if (M > kExactRows && wide >= 200)
+    return wide <= 256 ? launch_wide<4>(M, N, K, q, s, qw, sw, out, stream)
+                       : launch_wide<2>(M, N, K, q, s, qw, sw, out, stream);
 #define FP8_CODES(W, RT, TT) launch<W, RT, TT, 2, 1, false, Pow2Scale>(M, N, K, q, K, s, qw, sw, out, stream)
   if (tiles * m1 <= 256) return FP8_CODES(16, 1, 1);
   if (tiles / 2 * m1 <= 256) return FP8_CODES(8, 2, 1);

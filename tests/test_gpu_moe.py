@@ -203,7 +203,7 @@ def test_experts(T, H, I, E, k, mode):
     assert torch.equal(fb.fp8_moe_experts(*args, out_dtype=torch.float32, scale_mode=mode), y32)
 
 
-def _exact_case(T, E, k, seed, H=256, I=256):
+def _exact_case(T, E, k, seed, H=256, I=256, ids=None):
     """Whole numbers throughout: g = 32 or 64 exactly (its silu rounds to
     itself), u whole and at most 12, so every rounding on the way is exact and
     y is a whole number below 2^24."""
@@ -216,7 +216,8 @@ def _exact_case(T, E, k, seed, H=256, I=256):
     for n in range(4):
         np.put_along_axis(Uw, rng.integers(1, H, (E, I, 1)), rng.choice([-1.0, 1.0], (E, I, 1)), axis=2)
     Wd = rng.integers(-1, 2, (E, H, I)).astype(np.float32)
-    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    if ids is None:
+        ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
     w = rng.choice([0.5, 1.0, 2.0], (T, k)).astype(np.float32)
     bits = lambda a: oracle.bf16_rne(a.reshape(-1, a.shape[-1]))  # noqa: E731
     q1, _, s1 = oracle.quantize_block(bits(np.concatenate([G, Uw], 1)), transpose=False)
@@ -235,6 +236,21 @@ def test_experts_exact(T, E, k):
     import torch
     args, y = _exact_case(T, E, k, T)
     assert np.array_equal(host(fb.fp8_moe_experts(*args, out_dtype=torch.float32)).astype(np.float64), y)
+
+
+@pytest.mark.parametrize("T,E", [(14, 16), (40, 8), (200, 16), (512, 32)])
+def test_experts_one_has_all_the_tokens(T, E):
+    """Many times the rows that an expert has on average."""
+    import torch
+    ids = np.tile(np.array([[3, 5]], np.int32), (T, 1))
+    ids[T // 2:, 1] = -1
+    ids[0] = [6, 3]
+    args, y = _exact_case(T, E, 2, 900 + T, ids=np.maximum(ids, 0))
+    assert np.array_equal(host(fb.fp8_moe_experts(*args, out_dtype=torch.float32)).astype(np.float64), y)
+    want = fb.fp8_moe_experts(args[0], dev(ids), *args[2:], out_dtype=torch.float32)
+    alone = [fb.fp8_moe_experts(args[0][t:t + 1], dev(ids[t:t + 1]), args[2][t:t + 1], *args[3:],
+                                out_dtype=torch.float32) for t in (0, 1, T - 1)]
+    assert torch.equal(want[[0, 1, T - 1]], torch.cat(alone))
 
 
 @pytest.mark.parametrize("T,H,I,E,k", [(8, 4096, 512, 32, 8), (3, 8960, 256, 3, 2), (3, 256, 8448, 3, 2),
