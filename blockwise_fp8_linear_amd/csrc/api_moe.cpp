@@ -35,9 +35,9 @@ size_t codes_bytes(int64_t rows, int64_t K) { return up256((size_t)(rows * K)); 
 size_t gemm_bytes(int64_t rows, int64_t K) {
   return rows ? codes_bytes(rows, K) + up256((size_t)(rows * (K / kGroup)) * sizeof(float)) : 0;
 }
-size_t linear_bytes(int64_t M, int64_t N, int64_t K) {
+size_t linear_bytes(int64_t M, int64_t N, int64_t K, bool fp32_scale) {
   const int64_t main = gemm_rows(M, N, K);
-  return gemm_bytes(main, K) + rows_workspace_bytes(M - main, K);
+  return gemm_bytes(main, K) + rows_workspace_bytes(M - main, N, K, fp32_scale);
 }
 
 bool linear_limits(int64_t M, int64_t N, int64_t K) {
@@ -125,9 +125,9 @@ MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int k) {
 
 extern "C" {
 
-size_t fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
-  if (M <= 0 || !mult128(N) || !mult128(K) || !linear_limits(M, N, K)) return (size_t)-1;
-  return linear_bytes(M, N, K);
+size_t fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int scale_mode) {
+  if (!valid_scale_mode(scale_mode) || M <= 0 || !mult128(N) || !mult128(K) || !linear_limits(M, N, K)) return (size_t)-1;
+  return linear_bytes(M, N, K, scale_mode == FP8BLK_SCALE_FP32);
 }
 
 int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw, const float* sw,
@@ -139,11 +139,11 @@ int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x,
   if (M <= 0 || !mult128(N) || !mult128(K)) return FP8BLK_ERR_DIM;
   if (ld_x < K || ld_x > kMaxStride || !linear_limits(M, N, K) || !prod_le(M, ld_x, kMaxElems)) return FP8BLK_ERR_ARG;
   if (!aligned16(x) || ld_x % 8 || !aligned16(qw) || !aligned4(sw) || !aligned16(y)) return FP8BLK_ERR_ALIGN;
-  const size_t need = linear_bytes(M, N, K);
+  const bool f32 = out_dtype != FP8BLK_OUT_BF16, fp32_scale = scale_mode == FP8BLK_SCALE_FP32;
+  const size_t need = linear_bytes(M, N, K, fp32_scale);
   if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8BLK_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
   if (int rc = check_device()) return rc;
-  const bool f32 = out_dtype != FP8BLK_OUT_BF16, fp32_scale = scale_mode == FP8BLK_SCALE_FP32;
   const int64_t main = gemm_rows(M, N, K);
   if (main > 0) {
     uint8_t* q = static_cast<uint8_t*>(workspace);

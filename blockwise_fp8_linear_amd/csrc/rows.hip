@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t M, int nkb, 
 // idle.  Times below are us as a graph node at K = 2048 (an empty node takes
 // 2.1), power-of-two scales.
 
-// Up to raw_rows(): one launch that quantizes as it multiplies.  16 tokens per
+// rows_raw(): one launch that quantizes as it multiplies.  16 tokens per
 // workgroup (more rows per tile only pay at large N: 32 x 12288 9.7 with two
 // tiles of tokens, 10.3 with one).  1, 2, 3, 4 tiles of columns:
 //   16 x 4096   4.9  5.2   -    -       24 x 4096   6.1  5.2   -    -
@@ -236,8 +236,8 @@ hipError_t launch_codes(int64_t M, int64_t N, int64_t K, const uint8_t* q, const
 
 template <class S>
 hipError_t launch_scale(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
-                        const float* sw, RowsOut out, int64_t raw_rows, void* ws, hipStream_t stream) {
-  if (M <= raw_rows) {
+                        const float* sw, RowsOut out, bool raw, void* ws, hipStream_t stream) {
+  if (raw) {
     if (M <= 4) return launch_raw<1, S>(M, N, K, x, ld_x, qw, sw, out, stream);
     if (M <= 8) return launch_raw<2, S>(M, N, K, x, ld_x, qw, sw, out, stream);
     return launch_raw<4, S>(M, N, K, x, ld_x, qw, sw, out, stream);
@@ -256,8 +256,9 @@ hipError_t launch_scale(int64_t M, int64_t N, int64_t K, const uint16_t* x, int6
 
 hipError_t launch_linear_rows(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* qw,
                               const float* sw, RowsOut out, bool fp32_scale, void* ws, hipStream_t stream) {
-  return fp32_scale ? launch_scale<Fp32Scale>(M, N, K, x, ld_x, qw, sw, out, raw_rows(true), ws, stream)
-                    : launch_scale<Pow2Scale>(M, N, K, x, ld_x, qw, sw, out, raw_rows(false), ws, stream);
+  const bool raw = rows_raw(M, N, K, fp32_scale);
+  return fp32_scale ? launch_scale<Fp32Scale>(M, N, K, x, ld_x, qw, sw, out, raw, ws, stream)
+                    : launch_scale<Pow2Scale>(M, N, K, x, ld_x, qw, sw, out, raw, ws, stream);
 }
 
 }  // namespace fp8blk

@@ -50,7 +50,7 @@ def _functions():
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes, f.restype = args, i32
-    lib.fp8_linear_workspace_size.argtypes = [i64, i64, i64]
+    lib.fp8_linear_workspace_size.argtypes = [i64, i64, i64, i32]
     lib.fp8_linear_workspace_size.restype = sz
     lib.fp8_moe_workspace_size.argtypes = [i64, i64, i64, i64, i32]
     lib.fp8_moe_workspace_size.restype = sz
@@ -163,8 +163,8 @@ def _topk(k):
 
 
 @functools.lru_cache(maxsize=4096)
-def _linear_need(M, N, K):
-    return _functions().fp8_linear_workspace_size(M, N, K)
+def _linear_need(M, N, K, scale_mode):
+    return _functions().fp8_linear_workspace_size(M, N, K, scale_mode)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -179,8 +179,8 @@ def _invalid(need):
 
 # ------------------------------------------------------------------- linear --
 
-def fp8_linear_workspace_size(M: int, N: int, K: int) -> int:
-    return int(_functions().fp8_linear_workspace_size(M, N, K))
+def fp8_linear_workspace_size(M: int, N: int, K: int, scale_mode: int = _fb.FP8BLK_SCALE_POW2) -> int:
+    return int(_functions().fp8_linear_workspace_size(M, N, K, scale_mode))
 
 
 def fp8_linear(x, qw, sw, out_dtype=None, out=None, workspace=None, stream=None, accumulate=False,
@@ -202,7 +202,7 @@ def fp8_linear(x, qw, sw, out_dtype=None, out=None, workspace=None, stream=None,
     if accumulate or out_dtype is not bf16:
         odt = _fb._odt(out_dtype, accumulate, out)
     lib = _functions()
-    keep, ws, size = _scratch(_linear_need(M, N, K), workspace, x, index, stream)
+    keep, ws, size = _scratch(_linear_need(M, N, K, scale_mode), workspace, x, index, stream)
     y, py = _result(out, x, (M, N), out_dtype, "out", index, stream)
     rc = lib.fp8_linear(M, N, K, x.data_ptr(), ld, pqw, psw, py, odt, scale_mode, ws, size, _stream(stream, index))
     if rc:

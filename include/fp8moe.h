@@ -41,8 +41,9 @@ enum fp8moe_dtype { FP8MOE_BF16 = 0, FP8MOE_FP32 = 1 };
  *   y   [M][N] dense, bf16 or fp32 (FP8BLK_OUT_FP32_ACCUM adds to it)
  *   scale_mode: the rule that made sw, and the rule x is quantized by.
  *   N, K positive multiples of 128; x, qw, y 16-byte aligned.
- *   workspace: at least fp8_linear_workspace_size(M, N, K) bytes, 16-byte
- *     aligned; may be NULL when that size is 0 (it is up to 8 rows).
+ *   workspace: at least fp8_linear_workspace_size(M, N, K, scale_mode) bytes,
+ *     16-byte aligned; may be NULL when that size is 0 (a few rows, small
+ *     products).
  * Up to FP8_LINEAR_FP32_ROWS rows the products are summed with fp32
  * faithfulness; above, with the accuracy of the GEMMs of fp8blk.h, which take
  * the multiples of 128 rows of large products.
@@ -51,8 +52,8 @@ int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t *x, int64_t ld_x,
                const uint8_t *qw, const float *sw, void *y, int out_dtype, int scale_mode,
                void *workspace, size_t ws_bytes, hipStream_t stream);
 
-/* Workspace bytes of fp8_linear ((size_t)-1 for an invalid shape). */
-size_t fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+/* Workspace bytes of fp8_linear ((size_t)-1 for an invalid shape or mode). */
+size_t fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int scale_mode);
 
 /*
  * The router's choice: for each token the k experts with the largest logits,

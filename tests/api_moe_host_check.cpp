@@ -87,8 +87,8 @@ static void linear_checks() {
     for (int64_t M : {1, 8, 9, 16, 48, 49, 64, 65, 127, 128, 129, 255, 256, 300, 333, 1024, 1100, 4096, 4133, 40000}) {
       for (int mode : {0, 1}) {
         for (int odt : {0, 1, 2}) {
-          const int64_t K = 384, ld = 400;
-          const size_t need = fp8_linear_workspace_size(M, N, K), size = odt ? 4 : 2;
+          const int64_t K = 1408, ld = 1432;
+          const size_t need = fp8_linear_workspace_size(M, N, K, mode), size = odt ? 4 : 2;
           g_quant.clear();
           g_gemm.clear();
           g_rows.clear();
@@ -117,7 +117,7 @@ static void linear_checks() {
                       (char*)r.out.y == y + (size_t)(done * N) * size && r.out.f32 == (odt != 0) &&
                       r.out.accumulate == (odt == 2) && r.f == (mode == 1),
                   "M %lld N %lld: the few rows' operands", (long long)M, (long long)N);
-            if (r.M > fp8blk::raw_rows(mode == 1)) {
+            if (!fp8blk::rows_raw(r.M, N, K, mode == 1)) {
               const size_t from = (const char*)r.ws - ws;
               CHECK(from >= used && from % 16 == 0, "the few rows' workspace overlaps the GEMM's");
               used = from + fp8blk::rows_scales_at(r.M, K) + (size_t)(r.M * (K / 128)) * 4;

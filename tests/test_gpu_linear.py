@@ -38,7 +38,10 @@ M_ALL = [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 96, 100, 127, 128
 SHAPES = [(1, 128, 128), (5, 128, 1152), (3, 1152, 128), (16, 256, 2048), (1, 2048, 6144), (40, 384, 768),
           (7, 8192, 256), (20, 12288, 128), (33, 16384, 256), (64, 640, 384), (130, 8192, 128),
           (700, 8192, 128), (475, 8192, 256), (1100, 4096, 128), (2048, 2048, 128),
-          (1500, 8192, 512), (1200, 8192, 512), (2300, 8192, 128), (513, 3328, 640), (128, 25600, 128)]
+          (1500, 8192, 512), (1200, 8192, 512), (2300, 8192, 128), (513, 3328, 640), (128, 25600, 128),
+          (9, 128, 2176), (77, 256, 2304), (65, 512, 13312), (200, 640, 8192), (333, 1152, 4224), (129, 2176, 5120),
+          (1027, 384, 7680), (9, 65536, 256), (120, 24576, 384), (1600, 2048, 128), (1500, 1664, 256),
+          (64, 2048, 6400), (200, 4096, 1152), (40, 12288, 128), (1230, 8192, 1024), (4, 6144, 256)]
 
 
 @pytest.mark.parametrize("M,N,K,mode", [(m, 256, 384, POW2) for m in M_ALL] +
@@ -71,22 +74,21 @@ def test_whole_numbers_are_exact():
 
 
 @pytest.mark.parametrize("mode", [POW2, FP32])
-@pytest.mark.parametrize("M", [3, 40, 100])
-def test_quantizes_as_the_quantizer(M, mode):
+@pytest.mark.parametrize("M,N,K", [(3, 128, 512), (40, 128, 512), (100, 128, 512), (400, 4096, 512), (100, 128, 2176)])
+def test_quantizes_as_the_quantizer(M, N, K, mode):
     """Groups of zeros, subnormals, huge values and outliers: with W = 1 at
     one place of each block row the output is the quantizer's code times its
     scale (times W's), which the fp32 sum leaves alone."""
     import torch
-    K = 512
     x = synth.normal_bf16((M, K), 1.0, 63, M)
     x[0, :128] = 0                               # a group of +0
     x[1, 128:256] = 0x8000                       # -0
     x[2, :128] = synth.rng_for(64).integers(0, 0x80, 128).astype(np.uint16)       # subnormals
     x[M - 1, 256:384] = 0x7F7F                   # the largest finite
     x[M - 1, 300] = 1
-    W = np.zeros((128, K), np.float32)
-    at = synth.rng_for(65).integers(0, K, 128)
-    W[np.arange(128), at] = 1.0
+    W = np.zeros((N, K), np.float32)
+    at = synth.rng_for(65).integers(0, K, N)
+    W[np.arange(N), at] = 1.0
     qw, _, sw = oracle.quantize_block(oracle.bf16_rne(W), transpose=False, mode=mode)
     y = host(fb.fp8_linear(dev_bf16(x), dev(qw), dev(sw), out_dtype=torch.float32, scale_mode=mode)).astype(np.float64)
     # the largest bf16, (2 - 2^-7) 2^127, rounds to the code 256 at the scale 2^120: 2^128, which fp32 holds as infinity

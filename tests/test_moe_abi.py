@@ -71,22 +71,28 @@ def test_linear_errors(lib):
         assert call(**kw) == EDIM, kw
     for kw in ({"x": P[0] + 8}, {"qw": P[1] + 8}, {"y": P[3] + 4}, {"sw": P[2] + 2}, {"ld": 388}):
         assert call(**kw) == EALIGN, kw
-    need = lib.fp8_linear_workspace_size(300, 256, 384)
-    assert need >= 300 * 384 + 300 * 3 * 4
-    assert call(M=300) == EWS and call(M=300, ws=P[4], wsb=need - 1) == EWS
-    assert call(M=300, ws=P[4] + 8, wsb=need) == EALIGN
-    assert call(M=300, ws=P[4], wsb=need) in NOGPU
+    for mode in (0, 1):
+        need = lib.fp8_linear_workspace_size(300, 4096, 2048, mode)
+        assert need >= 300 * 2048 + 300 * 16 * 4
+        big = {"M": 300, "N": 4096, "K": 2048, "ld": 2048, "mode": mode}
+        assert call(**big) == EWS and call(**big, ws=P[4], wsb=need - 1) == EWS
+        assert call(**big, ws=P[4] + 8, wsb=need) == EALIGN
+        assert call(**big, ws=P[4], wsb=need) in NOGPU
 
 
 def test_linear_workspace(lib):
     q = lib.fp8_linear_workspace_size
-    assert q(1, 128, 128) == 0 and q(8, 12288, 2048) == 0
+    assert q(1, 128, 128, 0) == 0 and q(8, 12288, 2048, 1) == 0 and q(300, 256, 384, 0) == 0
+    assert q(40, 12288, 2048, 0) == 0 and q(40, 12288, 2048, 1) > 0
+    assert q(1, 128, 128, 2) == BAD and q(1, 128, 128, -1) == BAD
     for bad in ((0, 128, 128), (1, 100, 128), (1, 128, 100), (1 << 27, 128, 128), (1, 128, 128 << 18),
                 (1 << 62, 128, 128)):
-        assert q(*bad) == BAD, bad
+        assert q(*bad, 0) == BAD, bad
     # codes and scales of every row that is quantized first, whichever kernel takes it
-    for M, N, K in ((49, 128, 128), (127, 256, 640), (333, 2048, 2048), (4133, 4096, 2048), (1100, 4096, 128)):
-        assert q(M, N, K) >= (M - M % 128 if M % 128 <= 8 else M) * (K + K // 128 * 4)
+    for M, N, K, few in ((64, 12288, 2048, 0), (127, 4096, 4096, 0), (333, 2048, 2048, 0), (4133, 4096, 2048, 37),
+                         (1100, 8192, 2048, 76)):
+        for mode in (0, 1):
+            assert q(M, N, K, mode) >= (M - few) * (K + K // 128 * 4)
 
 
 def test_route_errors(lib):
@@ -181,7 +187,7 @@ def test_header_is_c(tmp_path):
                    "return 4;\n"
                    "  if (fp8_moe_layer(1, 128, 128, 4, 2, 1, 0, 128, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) != "
                    "FP8BLK_ERR_NULL) return 5;\n"
-                   "  if (fp8_linear_workspace_size(0, 1, 1) != (size_t)-1) return 6;\n"
+                   "  if (fp8_linear_workspace_size(0, 1, 1, 0) != (size_t)-1) return 6;\n"
                    "  if (fp8_moe_workspace_size(FP8MOE_MAX_TOKENS + 1, 128, 128, 4, 2) != (size_t)-1) return 7;\n"
                    '  puts("ok");\n  return 0;\n}\n')
     libdir = os.path.dirname(fb.LIB_PATH)
