@@ -20,14 +20,15 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 static_assert(kExactRows == FP8_LINEAR_FP32_ROWS, "the header's promise");
 
 // The rows that the GEMMs of fp8blk.h take: none where their 256x256 tiles
-// would leave many CUs idle, else the multiples of 128.  At K = 2048 the GEMM
-// takes 26 us for anything up to 256 tiles (2048 x 4096: 26.7), after 3.5 for
-// its quantizer, and the rows beyond about 7 more; the kernels for fewer rows
-// take 3.7 us per million outputs, after 2.2 (2048 x 4096: 30.8).  Where K / 128
-// is not a multiple of 4 the GEMM is the general one and slower (1617 x 7680 x
-// 384 26.5 us, the other 18.5).
+// would leave many CUs idle, else the multiples of 128.  us of the GPU, with the
+// GEMM and without, K 2048: 1536 x 4096 31.2 and 29.9, 2048 x 4096 31.2 and
+// 33.6; where rows beyond a multiple of 128 need launches of their own, 2000 x
+// 4096 39.2 and 34.5, 2500 x 4096 39.6 and 41.1.  Where K / 128 is not a
+// multiple of 4 the GEMM is the general one and slower: K 4224, 2048 x 12288 178
+// and 154, 4000 x 9216 297 and 233, 4096 x 7680 232 and 240; K 640, 70 and 46
+// for 3000 x 9216.
 int64_t gemm_rows(int64_t M, int64_t N, int64_t K) {
-  const int64_t most = (K / kGroup % 4 ? 14000000 : 7500000) + (M % kGroup ? 2000000 : 0);
+  const int64_t most = (K / kGroup % 4 ? 40000000 : 7500000) + (M % kGroup ? 2000000 : 0);
   return M <= FP8_LINEAR_FP32_ROWS || M * N <= most ? 0 : M / kGroup * kGroup;
 }
 // Their codes and scales in the workspace, in front of the other rows'.

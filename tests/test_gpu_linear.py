@@ -41,6 +41,7 @@ SHAPES = [(1, 128, 128), (5, 128, 1152), (3, 1152, 128), (16, 256, 2048), (1, 20
           (1500, 8192, 512), (1200, 8192, 512), (2300, 8192, 128), (513, 3328, 640), (128, 25600, 128),
           (9, 128, 2176), (77, 256, 2304), (65, 512, 13312), (200, 640, 8192), (333, 1152, 4224), (129, 2176, 5120),
           (1027, 384, 7680), (9, 65536, 256), (120, 24576, 384), (1600, 2048, 128), (1500, 1664, 256),
+          (2100, 4096, 640), (3000, 3968, 128),
           (64, 2048, 6400), (200, 4096, 1152), (40, 12288, 128), (1230, 8192, 1024), (4, 6144, 256)]
 
 
