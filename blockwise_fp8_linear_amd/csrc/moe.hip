@@ -181,6 +181,16 @@ __device__ __forceinline__ void store4(const RowsOut& out, int64_t at, const v4f
         make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
 }
 
+// Whether the layer's own choice for a token, whose first id is `first`, found
+// no expert.  That is where every logit is NaN or -infinity, so x[t] or wr is
+// not finite: the result is NaN, where the zeros of a token that the
+// caller gives no expert (a padded one) would hide it.
+__device__ __forceinline__ bool none_chosen(const MoeArgs& a, int first) { return a.wr && first < 0; }
+__device__ __forceinline__ v4f none() {
+  const float nan = __uint_as_float(0x7FC00000u);
+  return v4f{nan, nan, nan, nan};
+}
+
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
 // ---------------------------------------------------------------------------
@@ -418,6 +428,7 @@ __global__ __launch_bounds__(64 * W) void down_few_kernel(MoeArgs a, const uint8
   if (wave == 0 && r < a.T) {
     v4f v = red[lane];
     for (int w = 1; w < W; ++w) v += red[w * 64 + lane];
+    if (none_chosen(a, f.ids[r * a.k])) v = none();
     const int64_t at = (int64_t)r * a.H + n0 + 4 * c;
     if (gridDim.y > 1)
       *reinterpret_cast<v4f*>(partial + (int64_t)blockIdx.y * a.T * a.H + at) = v;
@@ -562,7 +573,7 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, const float* __
   const int u = blockIdx.x * 256 + threadIdx.x, per = a.H / 4;
   const int t = u / per, n = (u - t * per) * 4;
   if (t >= a.T) return;
-  v4f v{};
+  v4f v = none_chosen(a, a.ids[t * a.k]) ? none() : v4f{};
   for (int j0 = 0; j0 < a.k; j0 += 4) {  // the terms of four choices are loaded together
     v4f term[4];
 #pragma unroll
