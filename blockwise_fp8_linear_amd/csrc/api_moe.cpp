@@ -5,6 +5,7 @@
 
 #include "fp8blk_host.h"
 #include "fp8blk_launch.h"
+#include "fp8blk_plan.h"
 #include "fp8moe_launch.h"
 
 using namespace fp8blk;
@@ -19,16 +20,24 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 static_assert(kExactRows == FP8_LINEAR_FP32_ROWS, "the header's promise");
 
-// The rows that the GEMMs of fp8blk.h take: none where their 256x256 tiles
-// would leave many CUs idle, else the multiples of 128.  us of the GPU, with the
-// GEMM and without, K 2048: 1536 x 4096 31.2 and 29.9, 2048 x 4096 31.2 and
-// 33.6; where rows beyond a multiple of 128 need launches of their own, 2000 x
-// 4096 39.2 and 34.5, 2500 x 4096 39.6 and 41.1.  Where K / 128 is not a
-// multiple of 4 the GEMM is the general one and slower: K 4224, 2048 x 12288 178
-// and 154, 4000 x 9216 297 and 233, 4096 x 7680 232 and 240; K 640, 70 and 46
-// for 3000 x 9216.
-int64_t gemm_rows(int64_t M, int64_t N, int64_t K) {
-  const int64_t most = (K / kGroup % 4 ? 40000000 : 7500000) + (M % kGroup ? 2000000 : 0);
+// The rows that the GEMMs of fp8blk.h take: none where the kernels for any
+// number of rows are faster, else the multiples of 128.  us of the GPU, with the
+// GEMM and without:
+//   the block-scaled GEMM, whose 256x256 tiles leave many CUs idle below.  K
+//   2048, 1536 x 4096 33.3 and 31.9, 2048 x 4096 32.9 and 35.5; where rows
+//   beyond a multiple of 128 need launches of their own, 2000 x 4096 41.4 and
+//   36.7, 2500 x 4096 41.4 and 42.9;
+//   the general one (amax / 448 scales, and reductions that the other does not
+//   take).  amax / 448, K 2048, 768 x 12288 62 and 43, 3000 x 9216 125 and 94,
+//   4096 x 7680 123 and 121, 4000 x 10240 161 and 140, 8192 x 8192 235 and 325;
+//   K 8192, 768 x 12288 179 and 131, 3000 x 9216 396 and 342, 4096 x 7680 393
+//   and 465, 4000 x 10240 504 and 516, 4096 x 14336 667 and 861.  Power-of-two
+//   scales, K 640, 3000 x 9216 72 and 48, 4000 x 10240 89 and 69, 8192 x 8192
+//   122 and 138; K 4224, 3000 x 9216 244 and 174, 4096 x 7680 237 and 213, 4000
+//   x 10240 307 and 262, 8192 x 8192 461 and 622.
+int64_t gemm_rows(int64_t M, int64_t N, int64_t K, bool fp32_scale) {
+  const bool block_scaled = !fp32_scale && K / kGroup % 4 == 0 && K / kGroup <= kMxMaxKb;
+  const int64_t most = (block_scaled ? 7500000 : 40000000) + (M % kGroup ? 2000000 : 0);
   return M <= FP8_LINEAR_FP32_ROWS || M * N <= most ? 0 : M / kGroup * kGroup;
 }
 // Their codes and scales in the workspace, in front of the other rows'.
@@ -37,7 +46,7 @@ size_t gemm_bytes(int64_t rows, int64_t K) {
   return rows ? codes_bytes(rows, K) + up256((size_t)(rows * (K / kGroup)) * sizeof(float)) : 0;
 }
 size_t linear_bytes(int64_t M, int64_t N, int64_t K, bool fp32_scale) {
-  const int64_t main = gemm_rows(M, N, K);
+  const int64_t main = gemm_rows(M, N, K, fp32_scale);
   return gemm_bytes(main, K) + rows_workspace_bytes(M - main, N, K, fp32_scale);
 }
 
@@ -145,7 +154,7 @@ int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x,
   if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8BLK_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
   if (int rc = check_device()) return rc;
-  const int64_t main = gemm_rows(M, N, K);
+  const int64_t main = gemm_rows(M, N, K, fp32_scale);
   if (main > 0) {
     uint8_t* q = static_cast<uint8_t*>(workspace);
     float* s = reinterpret_cast<float*>(q + codes_bytes(main, K));
