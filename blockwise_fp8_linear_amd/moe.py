@@ -156,10 +156,12 @@ def _scratch(need, workspace, like, index, stream):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _topk(k):
-    """Refuse what a C int would not hold; the call refuses the rest."""
+def _topk(k, E):
+    """Refuse what a C int would not hold.  Returns whether the call will take k
+    choices of E: if not, it says why, and no output is made for it."""
     if not -2**31 <= k < 2**31:
         raise ValueError(f"topk: {k} is not between 1 and {FP8MOE_MAX_TOPK}")
+    return 1 <= k <= min(E, FP8MOE_MAX_TOPK)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -223,9 +225,10 @@ def fp8_moe_route(logits, topk, renormalize=True, ids=None, weights=None, stream
     whose logit is -inf or NaN are masked out; where fewer than topk are left
     the rest of the row is id -1, weight 0."""
     index, T, E, ld = _matrix(logits, _LOGITS, "logits")
-    _topk(topk)
-    ids, pids = _result(ids, logits, (T, topk), torch.int32, "ids", index, stream)
-    weights, pw = _result(weights, logits, (T, topk), torch.float32, "weights", index, stream)
+    pids = pw = None
+    if _topk(topk, E):
+        ids, pids = _result(ids, logits, (T, topk), torch.int32, "ids", index, stream)
+        weights, pw = _result(weights, logits, (T, topk), torch.float32, "weights", index, stream)
     rc = _functions().fp8_moe_route(T, E, topk, logits.data_ptr(),
                                     FP8MOE_FP32 if logits.dtype is torch.float32 else FP8MOE_BF16, ld,
                                     1 if renormalize else 0, pids, pw, _stream(stream, index))
@@ -242,7 +245,7 @@ def fp8_moe_route_backward(logits, ids, dweights, renormalize=True, dlogits=None
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids: expected a 2-dim tensor")
     k = ids.shape[1]
-    _topk(k)
+    _topk(k, E)
     pids = _operand(ids, torch.int32, (T, k), "ids", index)
     pg = _operand(dweights, torch.float32, (T, k), "dweights", index)
     dtype = logits.dtype
@@ -296,7 +299,7 @@ def fp8_moe_experts(x, ids, weights, qw1, sw1, qw2, sw2, out_dtype=None, out=Non
     pw = _operand(weights, torch.float32, (T, k), "weights", index)
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     odt = _fb._odt(out_dtype)
-    _topk(k)
+    _topk(k, E)
     lib = _functions()
     keep, ws, size = _scratch(_moe_need(T, H, I, E, k), workspace, x, index, stream)
     y, py = _result(out, x, (T, H), out_dtype, "out", index, stream)
@@ -321,7 +324,7 @@ def fp8_moe_layer(x, wr, qw1, sw1, qw2, sw2, topk, renormalize=True, out_dtype=N
     pw = None if weights is None else _operand(weights, torch.float32, (T, topk), "weights", index)
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     odt = _fb._odt(out_dtype)
-    _topk(topk)
+    _topk(topk, E)
     lib = _functions()
     keep, ws, size = _scratch(_moe_need(T, H, I, E, topk), workspace, x, index, stream)
     y, py = _result(out, x, (T, H), out_dtype, "out", index, stream)
