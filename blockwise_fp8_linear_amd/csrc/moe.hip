@@ -200,12 +200,6 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // 64 experts of 1024 are 512 workgroups of gate/up, where the wide kernel below
 // has 64 (20 and 27 us for both products).
 // ---------------------------------------------------------------------------
-constexpr int kFew = 16;
-constexpr int kCus = 256;
-// About the most workgroups of gate/up; beyond, each takes several columns, so
-// that its start counts less (4 tokens, 18 experts of 1408 x 256: 44 us without,
-// 35 with; at 768 as well, but 8 tokens, 51 experts of 768 x 2048 60 and 62).
-constexpr int kFewGrid = 2304;
 constexpr int kParts = 16;  // workgroups that share a column of y, at most
 
 // The choice of the whole call in LDS, and the experts it reaches, in the order
@@ -456,7 +450,7 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(MoeArgs a, const float* 
 //   40 tokens, 121 of 128 experts of 768 reached: gate/up 69 us (5.5 TB/s),
 //   down 35 (5.4); 256 tokens, 64 experts of 1024: 59 (4.5) and 35 (3.8).
 // ---------------------------------------------------------------------------
-// Dynamic LDS: the two slots for the most tiles, then the list of rows.
+// Dynamic LDS: the slots for the most tiles, then the list of rows.
 constexpr int kMostRows = 8192;  // T k
 template <int RT, int TMAX, int SLOTS>
 constexpr int kRing = rows_ring_bytes<RT, TMAX, SLOTS>();
@@ -626,37 +620,12 @@ hipError_t moe_few(const MoeArgs& a, const MoeBuffers& b, double reached, hipStr
   const auto k = b.logits ? &gate_up_few_kernel<W, XL, D, true, S> : &gate_up_few_kernel<W, XL, D, false, S>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(k), lds, &raised[b.logits != nullptr])) return e;
   const int most = a.T * a.k < a.E ? a.T * a.k : a.E;  // experts reached
-  int across = a.I / 16;
-  if (across * most > kFewGrid) across = (kFewGrid + most - 1) / most;
-  hipLaunchKernelGGL(k, dim3(across, most), dim3(64 * W), lds, stream, a, b.logits, reinterpret_cast<uint16_t*>(b.h));
+  hipLaunchKernelGGL(k, dim3(few_columns(a.T, a.I, a.E, a.k), most), dim3(64 * W), lds, stream, a, b.logits,
+                     reinterpret_cast<uint16_t*>(b.h));
   if (hipError_t e = hipGetLastError()) return e;
   return down_few<XL, true, S>(a, b, reached, stream);
 }
 
-// How a wide kernel's workgroups take the rows of an expert: `tiles` of 16 at a
-// time, `parts` workgroups in turn.
-struct RowSplit {
-  int tiles, parts;
-};
-// `columns`: workgroups of an expert's columns.  Tiles for about twice as many
-// rows as an expert has on average, since some have more (64 experts, k 8; one,
-// two, four tiles at most: 64 tokens 90, 97, - us; 100 tokens 119, 107, 107; 200
-// tokens -, 115, 104).  Where the columns leave CUs idle, fewer tiles in more
-// workgroups, which read the weights again, from a cache (256 tokens, 4 experts
-// of 512 x 1024: 80 us without, 26 with; 512 tokens, 64 of 256 x 2048 89 and 75).
-RowSplit row_split(const MoeArgs& a, int columns) {
-  const int mean = a.T * a.k / a.E, rows = 2 * mean < a.T ? 2 * mean : a.T;
-  const int most = mean <= 8 ? 1 : mean <= 20 ? 2 : 4, fit = kCus / (columns * a.E);
-  for (int tiles = 1;; tiles *= 2) {
-    const int parts = (rows + 16 * tiles - 1) / (16 * tiles);
-    if (parts <= fit) return RowSplit{tiles, parts < 1 ? 1 : parts};
-    if (tiles == most) return RowSplit{tiles, fit < 1 ? 1 : fit};
-  }
-}
-
-// Slots of the ring: as many as fit while each CU has one workgroup (17 tokens,
-// 8 experts of 6144: 86 us, with two slots 106); beyond, two (256 tokens, 64
-// experts of 1024, three slots of four tiles: 127 us, two 120).
 template <int TT, int SLOTS, class S>
 hipError_t gate_up_launch(const MoeArgs& a, const MoeBuffers& b, int parts, hipStream_t stream) {
   static std::atomic<uint64_t> raised{0};
@@ -668,9 +637,9 @@ hipError_t gate_up_launch(const MoeArgs& a, const MoeBuffers& b, int parts, hipS
 }
 
 template <int TT, class S>
-hipError_t gate_up_wide(const MoeArgs& a, const MoeBuffers& b, int parts, hipStream_t stream) {
-  if (a.I / 128 * (int64_t)a.E * parts > kCus) return gate_up_launch<TT, 2, S>(a, b, parts, stream);
-  return gate_up_launch<TT, TT == 1 ? 4 : 3, S>(a, b, parts, stream);
+hipError_t gate_up_wide(const MoeArgs& a, const MoeBuffers& b, const WidePlan& p, hipStream_t stream) {
+  return p.slots == 2 ? gate_up_launch<TT, 2, S>(a, b, p.parts, stream)
+                      : gate_up_launch<TT, gate_up_slots(TT), S>(a, b, p.parts, stream);
 }
 
 template <int RT, int TT, int SLOTS>
@@ -684,23 +653,23 @@ hipError_t down_launch(const MoeArgs& a, const MoeBuffers& b, int parts, hipStre
   return hipGetLastError();
 }
 
-template <int RT, int TT>
-hipError_t down_wide(const MoeArgs& a, const MoeBuffers& b, int parts, hipStream_t stream) {
-  const int columns = (a.H + 128 * RT - 1) / (128 * RT);
-  if (columns * (int64_t)a.E * parts > kCus) return down_launch<RT, TT, 2>(a, b, parts, stream);
-  return down_launch<RT, TT, RT == 1 ? 4 : 3>(a, b, parts, stream);
+template <int TT>
+hipError_t down_wide(const MoeArgs& a, const MoeBuffers& b, const WidePlan& p, hipStream_t stream) {
+  constexpr int RT = down_columns(TT);
+  return p.slots == 2 ? down_launch<RT, TT, 2>(a, b, p.parts, stream)
+                      : down_launch<RT, TT, down_slots(TT)>(a, b, p.parts, stream);
 }
 
 template <class S>
 hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
-  const RowSplit g = row_split(a, a.I / 128), d = row_split(a, a.H / 128);
-  if (hipError_t e = g.tiles == 1   ? gate_up_wide<1, S>(a, b, g.parts, stream)
-                     : g.tiles == 2 ? gate_up_wide<2, S>(a, b, g.parts, stream)
-                                    : gate_up_wide<4, S>(a, b, g.parts, stream))
+  const WidePlan g = gate_up_plan(a.T, a.I, a.E, a.k), d = down_plan(a.T, a.H, a.E, a.k);
+  if (hipError_t e = g.tiles == 1   ? gate_up_wide<1, S>(a, b, g, stream)
+                     : g.tiles == 2 ? gate_up_wide<2, S>(a, b, g, stream)
+                                    : gate_up_wide<4, S>(a, b, g, stream))
     return e;
-  if (hipError_t e = d.tiles == 1   ? down_wide<2, 1>(a, b, d.parts, stream)
-                     : d.tiles == 2 ? down_wide<1, 2>(a, b, d.parts, stream)
-                                    : down_wide<1, 4>(a, b, d.parts, stream))
+  if (hipError_t e = d.tiles == 1   ? down_wide<1>(a, b, d, stream)
+                     : d.tiles == 2 ? down_wide<2>(a, b, d, stream)
+                                    : down_wide<4>(a, b, d, stream))
     return e;
   hipLaunchKernelGGL(combine_kernel, dim3((a.T * (a.H / 4) + 255) / 256), dim3(256), 0, stream, a, b.partial);
   return hipGetLastError();
@@ -708,17 +677,8 @@ hipError_t moe_wide(const MoeArgs& a, const MoeBuffers& b, hipStream_t stream) {
 
 template <class S>
 hipError_t moe(const MoeArgs& a, MoeBuffers b, hipStream_t stream) {
-  // how many experts the tokens reach, if each is as likely as the next; with
-  // fewer than 64 workgroups the wide gate/up kernel leaves too many CUs idle
-  // (14 tokens, 9 experts of 1664 x 256, 88 workgroups: narrow 43 us, wide 24).
-  // Up to 8 tokens the narrow one is as fast at any number (8 tokens, 128 experts
-  // of 768: 60 us, wide 67; 16 tokens, 64 experts of 1024: 112 and 93), but it
-  // quantizes x again for each 16 columns, which amax / 448 scales make dearer
-  // (8 tokens 73 us, wide 64)
-  double missed = 1.0;
-  for (int t = 0; t < a.T; ++t) missed *= 1.0 - (double)a.k / a.E;
-  const double reached = a.E * (1.0 - missed);
-  const bool few = a.T <= (a.fp32_scale ? 4 : 8) || (a.T <= kFew && reached * (a.I / 128) < 64);
+  const double reached = experts_reached(a.T, a.E, a.k);
+  const bool few = few_plan(a.T, a.I, a.E, a.k, a.fp32_scale);
   // the choice: with its logits where wr is small, else from the logits' own launch, by the narrow gate/up itself or
   // with x's codes
   if (a.wr && a.E * (int64_t)a.H <= kTokenLogits) {
@@ -743,7 +703,7 @@ hipError_t moe(const MoeArgs& a, MoeBuffers b, hipStream_t stream) {
     return a.T <= 8 ? moe_few<2, S>(a, b, reached, stream) : moe_few<4, S>(a, b, reached, stream);
   }
   if (a.T <= kFew) {
-    if (hipError_t e = gate_up_wide<1, S>(a, b, 1, stream)) return e;
+    if (hipError_t e = gate_up_wide<1, S>(a, b, gate_up_plan(a.T, a.I, a.E, a.k), stream)) return e;
     return a.T <= 8 ? down_few<1, false, S>(a, b, reached, stream) : down_few<2, false, S>(a, b, reached, stream);
   }
   return moe_wide<S>(a, b, stream);

@@ -120,7 +120,6 @@ hipError_t launch(int64_t M, int64_t N, int64_t K, const void* x, int64_t row_by
 // multiply-adds) and by one block's latency.  (Columns x rows) 128 x 32, 128 x
 // 128, 256 x 64 and 256 x 128 measured slower: 1024 x 4096 x 2048 16.9 us, and
 // 23.1, 18.6, 20.2, 28.7.
-constexpr int kWideTiles = 4;
 template <int SLOTS>
 __global__ __launch_bounds__(512) void linear_wide_kernel(int64_t M, int64_t N, int64_t K,
                                                           const uint8_t* __restrict__ q, const float* __restrict__ xs,
@@ -170,9 +169,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t M, int nkb, 
 }
 
 // Tiles are chosen so that a launch has about one workgroup of eight waves per
-// CU: a smaller tile loads the tokens more often, a larger one leaves CUs
-// idle.  Times below are us as a graph node at K = 2048 (an empty node takes
-// 2.1), power-of-two scales.
+// CU.  Times below are us as a graph node at K = 2048 (an empty node takes 2.1),
+// power-of-two scales.
 
 // rows_raw(): one launch that quantizes as it multiplies.  16 tokens per
 // workgroup (more rows per tile only pay at large N: 32 x 12288 9.7 with two
@@ -207,31 +205,25 @@ hipError_t launch_wide(int64_t M, int64_t N, int64_t K, const uint8_t* q, const 
   return hipGetLastError();
 }
 
-// More rows: x quantized once (2.2 us), then tiles of codes.  The smallest of
-// (tiles of columns, of tokens) (1, 1), (2, 1), (2, 2), (4, 2), (4, 4) that
-// has at most 256 workgroups: 24 x 4096 (2, 1) 4.1; 64 x 4096 (2, 2) 4.9 and
-// (4, 1) 5.1; 128 x 4096 (4, 2) 6.0 and (2, 2) 6.6; 256 x 4096 (4, 4) 8.2 and
-// (4, 2) 9.9.  Where all have more, smaller workgroups of (3, 2): 64 x 12288
-// 10.4 and (4, 4) 11.4; 96 x 12288 12.0 and (4, 2) 13.3.  Above kExactRows
-// rows, and with 200 workgroups of it, the wide kernel: 512 x 4096 12.8 and
-// 16.6, 1467 x 2560 (K 6400) 44 and 73; with fewer, 333 x 2048 11.4 and 8.3.
-// Its slots: four while each CU has one workgroup, 1000 x 2048 (K 6400) 34.0 and
-// with two 37.4; beyond, two, so that two fit (1467 x 2560: 45.0, three 48.6).
+// More rows: x quantized once (2.2 us), then the kernel of codes_tile().
 hipError_t launch_codes(int64_t M, int64_t N, int64_t K, const uint8_t* q, const float* s, const uint8_t* qw,
                         const float* sw, RowsOut out, hipStream_t stream) {
-  const int64_t tiles = N / 16, m1 = (M + 15) / 16, m2 = (M + 31) / 32, m4 = (M + 63) / 64;
-  const int64_t wide = tiles / 8 * m4;
-  if (M > kExactRows && wide >= 200)
-    return wide <= 256 ? launch_wide<4>(M, N, K, q, s, qw, sw, out, stream)
-                       : launch_wide<2>(M, N, K, q, s, qw, sw, out, stream);
-#define FP8_CODES(W, RT, TT) launch<W, RT, TT, 2, 1, false, Pow2Scale>(M, N, K, q, K, s, qw, sw, out, stream)
-  if (tiles * m1 <= 256) return FP8_CODES(16, 1, 1);
-  if (tiles / 2 * m1 <= 256) return FP8_CODES(8, 2, 1);
-  if (tiles / 2 * m2 <= 256) return FP8_CODES(8, 2, 2);
-  if (tiles / 4 * m2 <= 256) return FP8_CODES(8, 4, 2);
-  if (tiles / 4 * m4 <= 256 && M > 64) return FP8_CODES(8, 4, 4);
-  return tiles % 3 == 0 ? FP8_CODES(4, 3, 2) : FP8_CODES(4, 4, 2);
+  const RowsTile t = codes_tile(M, N);
+  if (t.slots)
+    return t.slots == 4 ? launch_wide<4>(M, N, K, q, s, qw, sw, out, stream)
+                        : launch_wide<2>(M, N, K, q, s, qw, sw, out, stream);
+#define FP8_CODES(W, RT, TT)                             \
+  if (t.waves == W && t.columns == RT && t.tokens == TT) \
+  return launch<W, RT, TT, 2, 1, false, Pow2Scale>(M, N, K, q, K, s, qw, sw, out, stream)
+  FP8_CODES(16, 1, 1);
+  FP8_CODES(8, 2, 1);
+  FP8_CODES(8, 2, 2);
+  FP8_CODES(8, 4, 2);
+  FP8_CODES(8, 4, 4);
+  FP8_CODES(4, 3, 2);
+  FP8_CODES(4, 4, 2);
 #undef FP8_CODES
+  return hipErrorInvalidValue;
 }
 
 template <class S>
