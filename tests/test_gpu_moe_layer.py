@@ -66,3 +66,42 @@ def test_layer_shows_a_token_that_is_not_finite(T, H, I, E, k, mode):
     y, ids, _ = _layer(z, wr, exps, k, scale_mode=mode)
     assert host(ids[1]).tolist() == list(range(k)) and bool((y[1] == 0).all())
     assert bool(torch.isfinite(clean).all())
+
+
+# routers of every size class: inside the token's own launch (E H <= 64 Ki; 2 to 8 rounds of 64 experts), in the narrow
+# gate/up with 4, 8 and 16 tokens' rows, and in the wide kernels' token launch
+ROUTERS = [(5, 128, 128, 129, 4), (30, 128, 128, 257, 3), (3, 128, 128, 512, 16), (40, 128, 128, 512, 2),
+           (1, 128, 128, 1024, 16), (3, 128, 128, 1024, 5), (6, 512, 128, 200, 5), (12, 512, 128, 200, 3),
+           (12, 128, 128, 1024, 2), (20, 128, 128, 1024, 16), (17, 640, 128, 256, 7)]
+
+
+@pytest.mark.parametrize("T,H,I,E,k", ROUTERS)
+@pytest.mark.parametrize("mode", [POW2, FP32])
+def test_layer_chooses_and_ties(T, H, I, E, k, mode):
+    """Each expert of the first half stands again in the second, with the same
+    logit: the lower index comes first.  The choice is held to 64-bit logits (an
+    fp32 sum may exchange what lies closer than its error), the weights to the
+    softmax of the choice, the result to the experts' own call."""
+    import torch
+    x, _, _, q1, s1, q2, s2 = _case(T, H, I, E, 1, 800 + T, mode)
+    wr = synth.normal_bf16((E, H), 0.3, 94, T + E)
+    half = E // 2
+    wr[half:2 * half] = wr[:half]
+    exps, renorm = tuple(dev(a) for a in (q1, s1, q2, s2)), T % 2 == 0
+    y, ids, w = _layer(dev_bf16(x), dev_bf16(wr), exps, k, renormalize=renorm, scale_mode=mode)
+    lg = moe_ref.f64(x) @ moe_ref.f64(wr).T
+    err = (H + 16) * 2 * moe_ref.U * (np.abs(moe_ref.f64(x)) @ np.abs(moe_ref.f64(wr)).T).max()
+    got, gw = host(ids), host(w).astype(np.float64)
+    for t in range(T):
+        row, chosen = lg[t], list(got[t])
+        assert len(set(chosen)) == k and 0 <= min(chosen) and max(chosen) < E
+        assert np.all(np.abs(row[chosen] - np.sort(row)[::-1][:k]) <= 2 * err)
+        for at, e in enumerate(chosen):
+            if half <= e < 2 * half:
+                assert e - half in chosen[:at], (t, chosen)
+        p = moe_ref._softmax(row, chosen if renorm else list(range(E)))
+        rw = np.array([p[j] for j in chosen])
+        assert np.all(np.abs(gw[t] - rw) <= (2 * err + moe_ref.route_tolerance(np.ptp(row), E)) * 1.01 * rw)
+    assert torch.equal(y, fb.fp8_moe_experts(dev_bf16(x), ids, w, *exps, out_dtype=torch.float32, scale_mode=mode))
+    b = fb.fp8_moe_layer(dev_bf16(x), dev_bf16(wr), *exps, k, renormalize=renorm, scale_mode=mode)
+    assert torch.equal(b, y.bfloat16())
