@@ -28,16 +28,18 @@ static_assert(kExactRows == FP8_LINEAR_FP32_ROWS, "the header's promise");
 //   beyond a multiple of 128 need launches of their own, 2000 x 4096 41.4 and
 //   36.7, 2500 x 4096 41.4 and 42.9;
 //   the general one (amax / 448 scales, and reductions that the other does not
-//   take).  amax / 448, K 2048, 768 x 12288 62 and 43, 3000 x 9216 125 and 94,
-//   4096 x 7680 123 and 121, 4000 x 10240 161 and 140, 8192 x 8192 235 and 325;
-//   K 8192, 768 x 12288 179 and 131, 3000 x 9216 396 and 342, 4096 x 7680 393
-//   and 465, 4000 x 10240 504 and 516, 4096 x 14336 667 and 861.  Power-of-two
-//   scales, K 640, 3000 x 9216 72 and 48, 4000 x 10240 89 and 69, 8192 x 8192
-//   122 and 138; K 4224, 3000 x 9216 244 and 174, 4096 x 7680 237 and 213, 4000
-//   x 10240 307 and 262, 8192 x 8192 461 and 622.
+//   take), from memory rather than a cache: four sets of operands in turn.
+//   amax / 448, K 2048, 768 x 12288 61 and 42, 3000 x 9216 130 and 99, 4096 x
+//   7680 129 and 124, 4000 x 10240 161 and 142, (two sets) 8192 x 8192 235 and
+//   325.  Power-of-two scales, K 640, 3000 x 9216 71 and 47, 4000 x 10240 85 and
+//   64; K 4224, 3000 x 9216 250 and 193, 4000 x 7680 251 and 242, 4000 x 9216
+//   307 and 257, 4000 x 10240 316 and 282, but 4096 x 7680 240 and 252.  Long
+//   reductions turn earlier: amax / 448, K 8192, 3000 x 9216 413 and 367, 4096 x
+//   6144 313 and 316, 4000 x 7680 414 and 455, 4096 x 8192 405 and 419, 4096 x
+//   7680 399 and 474.
 int64_t gemm_rows(int64_t M, int64_t N, int64_t K, bool fp32_scale) {
   const bool block_scaled = !fp32_scale && K / kGroup % 4 == 0 && K / kGroup <= kMxMaxKb;
-  const int64_t most = (block_scaled ? 7500000 : 40000000) + (M % kGroup ? 2000000 : 0);
+  const int64_t most = (block_scaled ? 7500000 : K <= 6144 ? 40000000 : 28000000) + (M % kGroup ? 2000000 : 0);
   return M <= FP8_LINEAR_FP32_ROWS || M * N <= most ? 0 : M / kGroup * kGroup;
 }
 // Their codes and scales in the workspace, in front of the other rows'.
