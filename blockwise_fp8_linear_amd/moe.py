@@ -4,7 +4,10 @@ mixture-of-experts layer for a few tokens.
 
 The manner is the package's: the C entry points' names, torch tensors on the
 current device, checks of dtype, layout and shape before any C call,
-RuntimeError on a non-zero status.  These calls stand in decoding loops, where
+RuntimeError on a non-zero status.  The calls record nothing for autograd,
+whatever `requires_grad` says, and return tensors without a gradient:
+fp8_moe_route_backward and the package's Dgrad and Wgrad are called by the
+user's own autograd function.  These calls stand in decoding loops, where
 their own cost is what a caller waits for, so the checks of an operand are one
 function and the stream is taken as a raw handle.
 """
@@ -223,7 +226,8 @@ def fp8_moe_route(logits, topk, renormalize=True, ids=None, weights=None, stream
     the largest logits, largest first, equal ones by lower index, and their
     softmax weights -- over the chosen ones (renormalize) or over all.  Experts
     whose logit is -inf or NaN are masked out; where fewer than topk are left
-    the rest of the row is id -1, weight 0."""
+    the rest of the row is id -1, weight 0.  Nothing is recorded for autograd:
+    fp8_moe_route_backward gives the gradient."""
     index, T, E, ld = _matrix(logits, _LOGITS, "logits")
     pids = pw = None
     if _topk(topk, E):

@@ -36,17 +36,21 @@ enum fp8moe_dtype { FP8MOE_BF16 = 0, FP8MOE_FP32 = 1 };
  * Y = X W^T for any number of tokens, from bf16 activations: what
  * fp8_quantize_rowgroup of X followed by Fprop computes (the same codes and
  * scales, fp32 accumulation), without the multiple-of-128 limit on M.
- *   x   [M][K] bf16, row stride ld_x (>= K, multiple of 8), M >= 1
+ *   x   [M][K] bf16, row stride ld_x (>= K, multiple of 8, at most 2^26), M >= 1
  *   qw  [N][K] codes + sw [N/128][K/128] (from fp8_quantize_block of W)
  *   y   [M][N] dense, bf16 or fp32 (FP8BLK_OUT_FP32_ACCUM adds to it)
  *   scale_mode: the rule that made sw, and the rule x is quantized by.
- *   N, K positive multiples of 128; x, qw, y 16-byte aligned.
+ *   N, K positive multiples of 128; x, qw, y 16-byte aligned.  M < 2^27, N <
+ *   2^27, K < 2^25; M N, M K, N K and M ld_x at most 2^40, M K / 128 < 2^31.
  *   workspace: at least fp8_linear_workspace_size(M, N, K, scale_mode) bytes,
  *     16-byte aligned; may be NULL when that size is 0 (a few rows, small
  *     products).
  * Up to FP8_LINEAR_FP32_ROWS rows the products are summed with fp32
- * faithfulness; above, with the accuracy of the GEMMs of fp8blk.h, which take
- * the multiples of 128 rows of large products.
+ * faithfulness; above, with at least the accuracy of the GEMMs of fp8blk.h (on
+ * the fp8 matrix instruction, 1.5e-5 to 4.5e-5 of the result's norm), which take
+ * the multiples of 128 rows of large products.  Which kernel sums a row, and in
+ * which order, is decided by M, N, K and scale_mode alone: equal calls give equal
+ * bits, but a row may differ in its last bits between calls of different M.
  */
 int fp8_linear(int64_t M, int64_t N, int64_t K, const uint16_t *x, int64_t ld_x,
                const uint8_t *qw, const float *sw, void *y, int out_dtype, int scale_mode,
@@ -66,7 +70,8 @@ size_t fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int scale_mode
  * chosen and takes no part in the softmax.  Where fewer than k are left, the
  * rest of the row is id -1 with weight 0.  A logit of +infinity outweighs
  * every finite one; several of them share evenly.
- *   T >= 1, 1 <= E <= FP8MOE_MAX_EXPERTS, 1 <= k <= min(E, FP8MOE_MAX_TOPK).
+ *   1 <= T < 2^31, T ld at most 2^40, 1 <= E <= FP8MOE_MAX_EXPERTS, 1 <= k <=
+ *   min(E, FP8MOE_MAX_TOPK).
  */
 int fp8_moe_route(int64_t T, int64_t E, int k, const void *logits, int dtype, int64_t ld,
                   int renormalize, int32_t *ids, float *weights, hipStream_t stream);
@@ -94,16 +99,19 @@ int fp8_moe_route_backward(int64_t T, int64_t E, int k, const void *logits, int 
  *   with no expert (a padded one: ids -1) gets zeros.
  * Every product is the linear layer above: x[t] is quantized in groups of
  * 128 by scale_mode's rule; h is rounded to bf16 once and quantized by the
- * same rule; products, silu and the weighted sum are fp32.
- *   x   [T][H] bf16, row stride ld_x (>= H, multiple of 8)
+ * same rule; products, silu and the weighted sum are fp32.  Equal calls give
+ * equal bits; in which order a token's terms are added may depend on the other
+ * tokens of the call (on their number and on the experts that they reach).
+ *   x   [T][H] bf16, row stride ld_x (>= H, multiple of 8, at most 2^26)
  *   ids [T][k] int32, weights [T][k] fp32, dense
  *   qw1 [E][2 I][H] codes, sw1 [E][2 I / 128][H / 128]: for each expert the
  *       I rows of G, then the I rows of U
  *   qw2 [E][H][I] codes, sw2 [E][H / 128][I / 128]: Wd
  *       (each as fp8_quantize_block quantizes the stacked matrix)
  *   y   [T][H] dense, bf16 or fp32 (no accumulation)
- *   1 <= T <= FP8MOE_MAX_TOKENS; H, I positive multiples of 128; E and k as
- *   for fp8_moe_route; codes, x and y 16-byte aligned, the rest 4-byte.
+ *   1 <= T <= FP8MOE_MAX_TOKENS; H, I positive multiples of 128, at most 2^20,
+ *   H I at most 2^29 and T k I < 2^31; E and k as for fp8_moe_route; codes, x
+ *   and y 16-byte aligned, the rest 4-byte.
  *   workspace: at least fp8_moe_workspace_size(T, H, I, E, k) bytes, 16-byte
  *     aligned.
  */
