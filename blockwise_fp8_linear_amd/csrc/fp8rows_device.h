@@ -16,7 +16,7 @@
 // The products run on the bf16 matrix instructions, not the fp8 ones: an E4M3
 // value is a bf16 value exactly, a product of two is exact in fp32, and the
 // bf16 instructions keep the sum to fp32 rounding (the fp8 ones were measured
-// at 1.5e-5 of the result's norm).  The extra conversions (16 per 2 KiB of
+// at 1.5e-5 to 4.5e-5 of the result's norm).  The extra conversions (16 per 2 KiB of
 // weights and wave) stay far below the time to read the weights.
 #pragma once
 
@@ -69,8 +69,10 @@ __device__ __forceinline__ v4f block_product(const BfFrag& a, const BfFrag& b) {
 }
 
 // The same on the fp8 matrix instruction, straight from the codes: a quarter of
-// the instructions and no conversions, for where the fp8 GEMMs' accuracy does
-// (1.5e-5 of the result's norm; each operand's own scale is 2^0).
+// the instructions and no conversions, for where the fp8 GEMMs' accuracy does:
+// the instruction adds a block's 128 products with fewer bits than fp32 has
+// (1.5e-5 to 4.5e-5 of the result's norm, the more the wider the codes' range;
+// the blocks are then added in fp32).  Each operand's own scale is 2^0.
 __device__ __forceinline__ v4f block_product_fp8(const CodeFrag& a, const CodeFrag& b) {
   typedef int v8i_t __attribute__((ext_vector_type(8)));
   const auto join = [](const CodeFrag& q) {
