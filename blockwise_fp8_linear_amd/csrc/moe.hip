@@ -182,9 +182,9 @@ __device__ __forceinline__ void store4(const RowsOut& out, int64_t at, const v4f
 }
 
 // Whether the layer's own choice for a token, whose first id is `first`, found
-// no expert.  That is where every logit is NaN or -infinity, so x[t] or wr is
-// not finite: the result is NaN, where the zeros of a token that the
-// caller gives no expert (a padded one) would hide it.
+// no expert.  That is where every logit is NaN or -infinity, so x[t], wr or
+// their product is not finite: the result is NaN, where the zeros of a token
+// that the caller gives no expert (a padded one) would hide it.
 __device__ __forceinline__ bool none_chosen(const MoeArgs& a, int first) { return a.wr && first < 0; }
 __device__ __forceinline__ v4f none() {
   const float nan = __uint_as_float(0x7FC00000u);

@@ -319,8 +319,8 @@ def fp8_moe_layer(x, wr, qw1, sw1, qw2, sw2, topk, renormalize=True, out_dtype=N
     """A whole mixture-of-experts layer for a few tokens: router logits x wr^T
     (wr bf16 [E,H]), fp8_moe_route's choice of topk experts, fp8_moe_experts of
     it.  `ids` (int32) and `weights` (fp32) [T,topk], where given, get the
-    choice.  A token whose logits are all NaN or -inf (its row of x is not
-    finite) gets ids -1, weights 0 and a row of NaN."""
+    choice.  A token whose logits are all NaN or -inf (its row of x, wr or their
+    product is not finite) gets ids -1, weights 0 and a row of NaN."""
     index, T, H, ld = _matrix(x, (torch.bfloat16,), "x")
     E, I, pq1, ps1, pq2, ps2 = _experts(qw1, sw1, qw2, sw2, H, index)
     pwr = _operand(wr, torch.bfloat16, (E, H), "wr", index)

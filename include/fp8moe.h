@@ -128,8 +128,8 @@ int fp8_moe_experts(int64_t T, int64_t H, int64_t I, int64_t E, int k,
  *   wr  [E][H] bf16 router weights, dense, 16-byte aligned
  *   ids, weights [T][k]: where the choice is written; both may be NULL.
  *   A token none of whose logits can be chosen (all NaN or -infinity: x[t] or
- *   wr is not finite) has ids -1 and weights 0, and its row of y is NaN: unlike
- *   a caller's -1 it is no padding.
+ *   wr is not finite, or their product overflows) has ids -1 and weights 0, and
+ *   its row of y is NaN: unlike a caller's -1 it is no padding.
  *   everything else as for fp8_moe_route and fp8_moe_experts.
  */
 int fp8_moe_layer(int64_t T, int64_t H, int64_t I, int64_t E, int k, int renormalize,
