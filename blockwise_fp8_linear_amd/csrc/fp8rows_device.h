@@ -21,8 +21,32 @@
 #pragma once
 
 #include "fp8blk_device.h"
+#include "fp8moe_launch.h"
 
 namespace fp8blk {
+
+// Four neighbouring elements of the result; ACCUM: a call may ask to add them.
+template <bool ACCUM>
+__device__ __forceinline__ void store_rows(const RowsOut& out, int64_t at, const v4f& v) {
+  if (out.f32) {
+    v4f* y = reinterpret_cast<v4f*>(static_cast<float*>(out.y) + at);
+    *y = ACCUM && out.accumulate ? *y + v : v;
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out.y) + at) =
+        make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+  }
+}
+
+// A group of 128 bf16 values on 16 neighbouring lanes, 8 each: this lane's codes
+// and the group's scale, as the row-group quantizer gives them (amax over the
+// group, scale rule S, round to nearest even).
+template <class S>
+__device__ __forceinline__ uint2 quantize8(const u32x4& v, float* scale) {
+  const uint32_t m = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
+  const S sc(row16_max(max(m & 0xFFFFu, m >> 16)));
+  *scale = sc.s;
+  return make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
+}
 
 typedef __bf16 v8bf_t __attribute__((ext_vector_type(8)));
 
@@ -125,20 +149,16 @@ __device__ __forceinline__ CodeFrag read_codes(const uint8_t* tile, uint32_t r, 
 
 // Rows that are still bf16 come through registers, 4 to a load: lane p has the
 // chunk p % 16 (8 values) of row 4 load + p / 16, sixteen neighbouring lanes a
-// whole group.  They are quantized on the way into the tile of codes -- the
-// same codes and scale that the row-group quantizer gives: amax over the group,
-// scale rule S, round to nearest even -- and each row's scale goes to
-// scale[row].
+// whole group.  They are quantized on the way into the tile of codes, and each
+// row's scale goes to scale[row].
 __device__ __forceinline__ uint32_t raw_row(uint32_t p, int load) { return load * 4 + (p >> 4); }
 
 template <class S>
 __device__ __forceinline__ void quantize_into(uint8_t* tile, float* scale, const u32x4& v, uint32_t p, int load) {
   const uint32_t row = raw_row(p, load), l16 = p & 15;
-  const uint32_t m = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
-  const S sc(row16_max(max(m & 0xFFFFu, m >> 16)));
-  *reinterpret_cast<uint2*>(tile + row * 128 + (((l16 >> 1) ^ (row & 7)) << 4) + (l16 & 1) * 8) =
-      make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
-  if (l16 == 0) scale[row] = sc.s;
+  float s;
+  *reinterpret_cast<uint2*>(tile + row * 128 + (((l16 >> 1) ^ (row & 7)) << 4) + (l16 & 1) * 8) = quantize8<S>(v, &s);
+  if (l16 == 0) scale[row] = s;
 }
 
 // The wave's direct loads have landed / its LDS reads have returned.  (Written

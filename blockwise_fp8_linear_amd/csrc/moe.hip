@@ -117,12 +117,9 @@ __global__ __launch_bounds__(kTokenThreads<WR>) void token_kernel(MoeArgs a, con
   if (qx) {
     for (int g = threadIdx.x >> 4; g < a.H / 128; g += kTokenThreads<WR> / 16) {
       const u32x4 v = *reinterpret_cast<const u32x4*>(x + g * 128 + l16 * 8);
-      uint32_t m = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
-      m = row16_max(max(m & 0xFFFFu, m >> 16));
-      const S sc(m);
-      *reinterpret_cast<uint2*>(qx + (int64_t)t * a.H + g * 128 + l16 * 8) =
-          make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
-      if (l16 == 0) sx[(int64_t)g * a.T + t] = sc.s;
+      float scale;
+      *reinterpret_cast<uint2*>(qx + (int64_t)t * a.H + g * 128 + l16 * 8) = quantize8<S>(v, &scale);
+      if (l16 == 0) sx[(int64_t)g * a.T + t] = scale;
     }
   }
   if constexpr (WR) __syncthreads();
@@ -170,15 +167,6 @@ __device__ __forceinline__ int rows_of_expert(const int32_t* __restrict__ ids, i
     __syncthreads();
   }
   return found;
-}
-
-// Four neighbouring elements of the result.
-__device__ __forceinline__ void store4(const RowsOut& out, int64_t at, const v4f& v) {
-  if (out.f32)
-    *reinterpret_cast<v4f*>(static_cast<float*>(out.y) + at) = v;
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out.y) + at) =
-        make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
 }
 
 // Whether the layer's own choice for a token, whose first id is `first`, found
@@ -427,7 +415,7 @@ __global__ __launch_bounds__(64 * W) void down_few_kernel(MoeArgs a, const uint8
     if (gridDim.y > 1)
       *reinterpret_cast<v4f*>(partial + (int64_t)blockIdx.y * a.T * a.H + at) = v;
     else
-      store4(a.out, at, v);
+      store_rows<false>(a.out, at, v);
   }
 }
 
@@ -437,7 +425,7 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(MoeArgs a, const float* 
   if (at >= size) return;
   v4f v{};
   for (int p = 0; p < parts; ++p) v += *reinterpret_cast<const v4f*>(partial + p * size + at);
-  store4(a.out, at, v);
+  store_rows<false>(a.out, at, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -579,7 +567,7 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, const float* __
 #pragma unroll
     for (int j = 0; j < 4; ++j) v += term[j];
   }
-  store4(a.out, (int64_t)t * a.H + n, v);
+  store_rows<false>(a.out, (int64_t)t * a.H + n, v);
 }
 
 // The launches of up to kFew tokens, and of more.

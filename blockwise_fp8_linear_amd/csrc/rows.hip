@@ -10,17 +10,6 @@ namespace fp8blk {
 
 namespace {
 
-// Four neighbouring elements of y.
-__device__ __forceinline__ void store_rows(const RowsOut& out, int64_t at, const v4f& v) {
-  if (out.f32) {
-    v4f* y = reinterpret_cast<v4f*>(static_cast<float*>(out.y) + at);
-    *y = out.accumulate ? *y + v : v;
-  } else {
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out.y) + at) =
-        make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
-  }
-}
-
 // The tile that a workgroup of a launch of columns x rows tiles takes.
 // Consecutive workgroups go to the eight XCDs in turn, each with an L2 of its
 // own: here every XCD gets a contiguous range of tiles in the order in which
@@ -95,7 +84,7 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(int64_t M, int64_t 
     const int tile = u >> 6, l = u & 63;
     const int64_t m = m0 + (tile % TT) * 16 + (l & 15), n = n0 + (tile / TT) * 16 + 4 * (l >> 4);
     if (m >= M) continue;
-    store_rows(out, m * N + n, v);
+    store_rows<true>(out, m * N + n, v);
   }
 }
 
@@ -144,7 +133,7 @@ __global__ __launch_bounds__(512) void linear_wide_kernel(int64_t M, int64_t N, 
       lds, wp, sp, K, q + m0 * K, xoff, xs + m0, M, [&](int i) { return min(i, rows - 1); }, nkb, acc);
 #pragma unroll
   for (int tt = 0; tt < TT; ++tt)
-    if (tt * 16 + r < rows) store_rows(out, (m0 + tt * 16 + r) * N + n0 + 4 * c, acc[0][tt]);
+    if (tt * 16 + r < rows) store_rows<true>(out, (m0 + tt * 16 + r) * N + n0 + 4 * c, acc[0][tt]);
 }
 
 // ---------------------------------------------------------------------------
@@ -163,11 +152,9 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t M, int nkb, 
     const int64_t m = u / nkb;
     const int g = (int)(u - m * nkb);
     const u32x4 v = *reinterpret_cast<const u32x4*>(x + m * ld_x + g * 128 + l16 * 8);
-    uint32_t a = pk_max_u16(pk_max_u16(abs2(v[0]), abs2(v[1])), pk_max_u16(abs2(v[2]), abs2(v[3])));
-    a = row16_max(max(a & 0xFFFFu, a >> 16));
-    const S sc(a);
-    *reinterpret_cast<uint2*>(q + u * 128 + l16 * 8) = make_uint2(quant4(v[0], v[1], sc), quant4(v[2], v[3], sc));
-    if (l16 == 0) s[g * M + m] = sc.s;
+    float scale;
+    *reinterpret_cast<uint2*>(q + u * 128 + l16 * 8) = quantize8<S>(v, &scale);
+    if (l16 == 0) s[g * M + m] = scale;
   }
 }
 
