@@ -1,0 +1,157 @@
+// A 128 x 128 tile of bf16 values held in the registers of a 256-thread
+// workgroup, quantized in row groups, in column groups (written transposed), or
+// both: the core of the one-pass quantizer (quant.hip) and of the kernels that
+// make such a tile on the way (sorted.hip, gated.hip).
+//
+// Thread t owns rows 8 * (t / 16) .. +7 and columns 8 * (t % 16) .. +7; v[i]
+// holds row i's eight values, two per word.  Row groups: the 16 lanes of a DPP
+// row share the rows, so the row amax is a DPP reduction and each lane stores 8
+// codes per row.  Column groups: a packed per-column max over the thread's rows,
+// then over the 16 row blocks (wave shuffles, then LDS across the 4 waves); the
+// thread's 8x8 codes are formed column by column (each pair of rows gathered
+// into one word by a byte permute, then converted) and staged in LDS, from where
+// whole 128-byte lines of the transposed output are stored.
+#pragma once
+
+#include "fp8blk_device.h"
+
+namespace fp8blk {
+
+constexpr int kTileThreads = 256;
+
+// What the column groups of one tile need of LDS.
+struct TileLds {
+  uint32_t red[kTileThreads / 64][16][4];
+  __attribute__((aligned(16))) uint2 tq[128][16];  // column codes: [column][8-row block]
+};
+
+// Row groups.  q: the tile's first row and the thread's first column; s: the
+// tile's first row and its group; G: groups per row of s.
+template <class S>
+__device__ __forceinline__ void tile_row_groups(const u32x4 (&v)[8], uint8_t* __restrict__ q, int64_t ld_q,
+                                                float* __restrict__ s, uint32_t G, uint32_t rb, uint32_t cb) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t m = pk_max_u16(pk_max_u16(abs2(v[i].x), abs2(v[i].y)), pk_max_u16(abs2(v[i].z), abs2(v[i].w)));
+    m = max(m & 0xFFFFu, m >> 16);
+    m = row16_max(m);
+    const S sc(m);
+    uint2 o;
+    o.x = quant4(v[i].x, v[i].y, sc);
+    o.y = quant4(v[i].z, v[i].w, sc);
+    uint2* const qp = reinterpret_cast<uint2*>(q + (int64_t)(rb * 8 + i) * ld_q);
+    *qp = o;
+    if (cb == 0) s[(int64_t)(rb * 8 + i) * G] = sc.s;
+  }
+}
+
+// Column groups.  qT: the tile's first column (a row of qT) and first row; sT:
+// the tile's first column and its row group; G: row groups per column of sT.
+// Passes two barriers; the LDS may be used again after another one.
+template <class S>
+__device__ __forceinline__ void tile_col_groups(const u32x4 (&v)[8], TileLds& lds, uint8_t* __restrict__ qT,
+                                                int64_t ld_qT, float* __restrict__ sT, uint32_t G, uint32_t rb,
+                                                uint32_t cb) {
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  // packed (two columns per word) max over the 128 rows
+  uint32_t cm[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    cm[0] = pk_max_u16(cm[0], abs2(v[i].x));
+    cm[1] = pk_max_u16(cm[1], abs2(v[i].y));
+    cm[2] = pk_max_u16(cm[2], abs2(v[i].z));
+    cm[3] = pk_max_u16(cm[3], abs2(v[i].w));
+  }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {  // the wave's 4 row blocks of this column block: lanes cb, cb+16, +32, +48
+    cm[w] = pk_max_u16(cm[w], (uint32_t)__shfl_xor((int)cm[w], 16, 64));
+    cm[w] = pk_max_u16(cm[w], (uint32_t)__shfl_xor((int)cm[w], 32, 64));
+  }
+  if (lane < 16) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) lds.red[wave][cb][w] = cm[w];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    cm[w] = pk_max_u16(pk_max_u16(lds.red[0][cb][w], lds.red[1][cb][w]),
+                       pk_max_u16(lds.red[2][cb][w], lds.red[3][cb][w]));
+  // column j's amax is half j % 2 of cm[j / 2]
+  const S inv[8] = {S(cm[0] & 0xFFFFu), S(cm[0] >> 16), S(cm[1] & 0xFFFFu), S(cm[1] >> 16),
+                    S(cm[2] & 0xFFFFu), S(cm[2] >> 16), S(cm[3] & 0xFFFFu), S(cm[3] >> 16)};
+  // The thread's 8x8 codes, one column at a time (rows 0..3 and 4..7 of
+  // column j, each with the column's scale: word j / 2 of each row, half
+  // j % 2), go through LDS as tq[column][row block], the 8-byte unit
+  // XOR-swizzled by the column block cb, and leave as whole 128-byte lines of
+  // qT: 8 lanes per column, 16 bytes (two row blocks) each.
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int m = j >> 1;
+    uint32_t a, b;
+    if (j & 1) {
+      a = quant4_col<1>(v[0][m], v[1][m], v[2][m], v[3][m], inv[j]);
+      b = quant4_col<1>(v[4][m], v[5][m], v[6][m], v[7][m], inv[j]);
+    } else {
+      a = quant4_col<0>(v[0][m], v[1][m], v[2][m], v[3][m], inv[j]);
+      b = quant4_col<0>(v[4][m], v[5][m], v[6][m], v[7][m], inv[j]);
+    }
+    lds.tq[cb * 8 + j][rb ^ cb] = make_uint2(a, b);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t c = k * 32 + (t >> 3), p = t & 7;
+    const uint32_t pu = (2 * p) ^ (c >> 3);  // physical unit of row block 2p
+    u32x4 w = *reinterpret_cast<const u32x4*>(&lds.tq[c][pu & ~1u]);
+    if (pu & 1) w = u32x4{w[2], w[3], w[0], w[1]};  // the pair is stored swapped
+    u32x4* const qTp = reinterpret_cast<u32x4*>(qT + (int64_t)c * ld_qT + 16 * p);
+    *qTp = w;
+  }
+  if (rb == 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sT[(int64_t)(cb * 8 + j) * G] = inv[j].s;
+  }
+}
+
+// Tile order of the one-pass quantizers.  A tile's scales are 128 four-byte
+// values strided through s (one per row) and 128 through sT (one per
+// column); the 8 tiles side by side along a row band fill one 32-byte
+// sector of s, the 8 above one another one of sT.  Where the shape allows
+// (tile_blocked: a multiple of 16 row tiles and of 8 column tiles, whole
+// multiples of 8 blocks), the tiles go in blocks of 8 column tiles x 16 row
+// tiles, block k to the workgroups k, k + 8, ... mod 8, i.e. to one XCD
+// (workgroups are dealt to the 8 XCDs in turn), walked down each column of
+// the block: every sector of s and sT is then written by one XCD, whose L2
+// merges the pieces before writing the sector back.  Measured on the
+// activation shapes: written bytes at the algorithmic count (+11% in row-band
+// order, from partial sectors written back from several L2s), and 0-8%
+// faster.  Other shapes walk row band by row band.  The codes leave with
+// plain stores: non-temporal ones were faster for the quantizer timed alone
+// (launch after launch) but slower in a training step, where the GEMMs read
+// the codes right after (they no longer found them in the caches) and the
+// quantizer itself ran slower too.
+constexpr uint32_t kTileBlockCols = 8, kTileBlockRows = 16;
+
+__host__ __device__ __forceinline__ bool tile_blocked(uint32_t row_tiles, uint32_t col_tiles) {
+  return row_tiles % kTileBlockRows == 0 && col_tiles % kTileBlockCols == 0 &&
+         (row_tiles / kTileBlockRows) * (col_tiles / kTileBlockCols) % 8 == 0;
+}
+
+// Workgroup bid's tile.
+__device__ __forceinline__ void tile_of(uint32_t bid, uint32_t col_tiles, bool blocked, uint32_t& rt, uint32_t& ct) {
+  if (blocked) {
+    constexpr uint32_t kPerBlock = kTileBlockCols * kTileBlockRows;
+    const uint32_t xcd = bid % 8, j = bid / 8;
+    const uint32_t blk = xcd + 8 * (j / kPerBlock), w = j % kPerBlock;
+    const uint32_t col_blocks = col_tiles / kTileBlockCols;
+    rt = (blk / col_blocks) * kTileBlockRows + w % kTileBlockRows;
+    ct = (blk % col_blocks) * kTileBlockCols + w / kTileBlockRows;
+  } else {
+    // consecutive workgroups walk along the rows, so that the ones in flight
+    // together read whole rows
+    rt = bid / col_tiles;
+    ct = bid - rt * col_tiles;
+  }
+}
+
+}  // namespace fp8blk

@@ -17,6 +17,7 @@
 // DPP; the scale exponent comes from the amax bits with integer ops.
 #include "fp8blk_device.h"
 #include "fp8blk_launch.h"
+#include "fp8tile_device.h"
 
 namespace fp8blk {
 
@@ -242,64 +243,18 @@ __global__ __launch_bounds__(kBlkThreads) void quant_block_batch_kernel(BlockJob
 // fourth paragraph); producing both orientations from one read of the bf16
 // tensor saves a whole second read.  Results are identical to
 // quant_rowgroup_kernel + quant_colgroup_kernel.
-// A workgroup takes a 128 x 128 tile; thread t owns rows 8*(t/16) .. +7 and
-// columns 8*(t%16) .. +7 (one 16-byte load per row; 16 lanes = a 256-byte
-// row).  Row groups: the 16 lanes of a DPP row share the rows, so the row
-// amax is a DPP reduction and each lane stores 8 codes per row.  Column
-// groups: a packed per-column max over the thread's rows, then over the 16
-// row blocks (wave shuffles, then LDS across the 4 waves); the thread's 8x8
-// codes are formed column by column (each pair of rows gathered into one
-// word by a byte permute, then converted) and staged in LDS, from where
-// whole 128-byte lines of the transposed output are stored.
+// A workgroup takes a 128 x 128 tile, one 16-byte load per row and thread (16
+// lanes = a 256-byte row); see fp8tile_device.h.
 // ---------------------------------------------------------------------------
-constexpr int kDualThreads = 256;
-
-// Tile order of the one-pass quantizer.  A tile's scales are 128 four-byte
-// values strided through s (one per row) and 128 through sT (one per
-// column); the 8 tiles side by side along a row band fill one 32-byte
-// sector of s, the 8 above one another one of sT.  Where the shape allows
-// (kDualBlocked: a multiple of 16 row tiles and of 8 column tiles, whole
-// multiples of 8 blocks), the tiles go in blocks of 8 column tiles x 16 row
-// tiles, block k to the workgroups k, k + 8, ... mod 8, i.e. to one XCD
-// (workgroups are dealt to the 8 XCDs in turn), walked down each column of
-// the block: every sector of s and sT is then written by one XCD, whose L2
-// merges the pieces before writing the sector back.  Measured on the
-// activation shapes: written bytes at the algorithmic count (+11% in row-band
-// order, from partial sectors written back from several L2s), and 0-8%
-// faster.  Other shapes walk row band by row band.  The codes leave with
-// plain stores: non-temporal ones were faster for the quantizer timed alone
-// (launch after launch) but slower in a training step, where the GEMMs read
-// the codes right after (they no longer found them in the caches) and the
-// quantizer itself ran slower too.
-constexpr uint32_t kDualBlockCols = 8, kDualBlockRows = 16;
-
-__host__ __device__ __forceinline__ bool dual_blocked(uint32_t row_tiles, uint32_t col_tiles) {
-  return row_tiles % kDualBlockRows == 0 && col_tiles % kDualBlockCols == 0 &&
-         (row_tiles / kDualBlockRows) * (col_tiles / kDualBlockCols) % 8 == 0;
-}
-
 template <class S>
-__global__ __launch_bounds__(kDualThreads) void quant_dual_kernel(
+__global__ __launch_bounds__(kTileThreads) void quant_dual_kernel(
     const uint16_t* __restrict__ x, int64_t ld_x, uint8_t* __restrict__ q, int64_t ld_q, float* __restrict__ s,
     uint8_t* __restrict__ qT, int64_t ld_qT, float* __restrict__ sT, uint32_t row_tiles, uint32_t col_tiles,
     uint32_t blocked) {
-  __shared__ uint32_t red[kDualThreads / 64][16][4];
-  __shared__ __attribute__((aligned(16))) uint2 tq[128][16];  // column codes: [column][8-row block]
-  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  __shared__ TileLds lds;
+  const uint32_t t = threadIdx.x;
   uint32_t rt, ct;
-  if (blocked) {
-    constexpr uint32_t kPerBlock = kDualBlockCols * kDualBlockRows;
-    const uint32_t xcd = blockIdx.x % 8, j = blockIdx.x / 8;
-    const uint32_t blk = xcd + 8 * (j / kPerBlock), w = j % kPerBlock;
-    const uint32_t col_blocks = col_tiles / kDualBlockCols;
-    rt = (blk / col_blocks) * kDualBlockRows + w % kDualBlockRows;
-    ct = (blk % col_blocks) * kDualBlockCols + w / kDualBlockRows;
-  } else {
-    // consecutive workgroups walk along the rows, so that the ones in flight
-    // together read whole rows of x
-    rt = blockIdx.x / col_tiles;
-    ct = blockIdx.x - rt * col_tiles;
-  }
+  tile_of(blockIdx.x, col_tiles, blocked, rt, ct);
   const int64_t m0 = (int64_t)rt * 128, c0 = (int64_t)ct * 128;
   const uint32_t rb = t >> 4, cb = t & 15;
   const int64_t r0 = m0 + rb * 8;
@@ -308,81 +263,8 @@ __global__ __launch_bounds__(kDualThreads) void quant_dual_kernel(
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + (r0 + i) * ld_x + c0 + cb * 8));
-
-  // ---- row groups (this tile's 128 columns are exactly one group per row)
-  const uint32_t G = col_tiles;  // groups per row
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t m = pk_max_u16(pk_max_u16(abs2(v[i].x), abs2(v[i].y)), pk_max_u16(abs2(v[i].z), abs2(v[i].w)));
-    m = max(m & 0xFFFFu, m >> 16);
-    m = row16_max(m);
-    const S sc(m);
-    uint2 o;
-    o.x = quant4(v[i].x, v[i].y, sc);
-    o.y = quant4(v[i].z, v[i].w, sc);
-    uint2* const qp = reinterpret_cast<uint2*>(q + (r0 + i) * ld_q + c0 + cb * 8);
-    *qp = o;
-    if (cb == 0) s[(r0 + i) * G + ct] = sc.s;
-  }
-
-  // ---- column groups: packed (two columns per word) max over the 128 rows
-  uint32_t cm[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    cm[0] = pk_max_u16(cm[0], abs2(v[i].x));
-    cm[1] = pk_max_u16(cm[1], abs2(v[i].y));
-    cm[2] = pk_max_u16(cm[2], abs2(v[i].z));
-    cm[3] = pk_max_u16(cm[3], abs2(v[i].w));
-  }
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {  // the wave's 4 row blocks of this column block: lanes cb, cb+16, +32, +48
-    cm[w] = pk_max_u16(cm[w], (uint32_t)__shfl_xor((int)cm[w], 16, 64));
-    cm[w] = pk_max_u16(cm[w], (uint32_t)__shfl_xor((int)cm[w], 32, 64));
-  }
-  if (lane < 16) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) red[wave][cb][w] = cm[w];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 4; ++w)
-    cm[w] = pk_max_u16(pk_max_u16(red[0][cb][w], red[1][cb][w]), pk_max_u16(red[2][cb][w], red[3][cb][w]));
-  // column j's amax is half j % 2 of cm[j / 2]
-  const S inv[8] = {S(cm[0] & 0xFFFFu), S(cm[0] >> 16), S(cm[1] & 0xFFFFu), S(cm[1] >> 16),
-                    S(cm[2] & 0xFFFFu), S(cm[2] >> 16), S(cm[3] & 0xFFFFu), S(cm[3] >> 16)};
-  // The thread's 8x8 codes, one column at a time (rows 0..3 and 4..7 of
-  // column j, each with the column's scale: word j / 2 of each row, half
-  // j % 2), go through LDS as tq[column][row block], the 8-byte unit
-  // XOR-swizzled by the column block cb, and leave as whole 128-byte lines of
-  // qT: 8 lanes per column, 16 bytes (two row blocks) each.
-  const int64_t cc = c0 + cb * 8;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int m = j >> 1;
-    uint32_t a, b;
-    if (j & 1) {
-      a = quant4_col<1>(v[0][m], v[1][m], v[2][m], v[3][m], inv[j]);
-      b = quant4_col<1>(v[4][m], v[5][m], v[6][m], v[7][m], inv[j]);
-    } else {
-      a = quant4_col<0>(v[0][m], v[1][m], v[2][m], v[3][m], inv[j]);
-      b = quant4_col<0>(v[4][m], v[5][m], v[6][m], v[7][m], inv[j]);
-    }
-    tq[cb * 8 + j][rb ^ cb] = make_uint2(a, b);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t c = k * 32 + (t >> 3), p = t & 7;
-    const uint32_t pu = (2 * p) ^ (c >> 3);  // physical unit of row block 2p
-    u32x4 w = *reinterpret_cast<const u32x4*>(&tq[c][pu & ~1u]);
-    if (pu & 1) w = u32x4{w[2], w[3], w[0], w[1]};  // the pair is stored swapped
-    u32x4* const qTp = reinterpret_cast<u32x4*>(qT + (c0 + c) * ld_qT + m0 + 16 * p);
-    *qTp = w;
-  }
-  if (rb == 0) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sT[(cc + j) * row_tiles + rt] = inv[j].s;
-  }
+  tile_row_groups<S>(v, q + m0 * ld_q + c0 + cb * 8, ld_q, s + m0 * col_tiles + ct, col_tiles, rb, cb);
+  tile_col_groups<S>(v, lds, qT + c0 * ld_qT + m0, ld_qT, sT + c0 * row_tiles + rt, row_tiles, rb, cb);
 }
 
 // ------------------------------------------------------------- launchers ---
@@ -448,8 +330,8 @@ hipError_t launch_quant_dual(const uint16_t* x, int64_t rows, int64_t cols, int6
                              float* s, uint8_t* qT, int64_t ld_qT, float* sT, bool fp32_scale, hipStream_t stream) {
   const uint32_t rt = (uint32_t)(rows / 128);
   const uint32_t ct = (uint32_t)(cols / 128);
-  const uint32_t blocked = dual_blocked(rt, ct) ? 1u : 0u;
-  const dim3 grid(rt * ct), block(kDualThreads);
+  const uint32_t blocked = tile_blocked(rt, ct) ? 1u : 0u;
+  const dim3 grid(rt * ct), block(kTileThreads);
   if (fp32_scale)
     hipLaunchKernelGGL(quant_dual_kernel<Fp32Scale>, grid, block, 0, stream, x, ld_x, q, ld_q, s, qT, ld_qT, sT, rt, ct,
                        blocked);
