@@ -469,18 +469,26 @@ def fp8_block_gemm_backward_w_noalloc(qdy, sdy, qw, sw, qdyT, sdyT, qxT, sxT, dx
     return dx, dw
 
 
-# ------------------------------------------- any number of tokens, experts --
-# moe.py binds include/fp8moe.h.  It is loaded on first use: it imports torch,
-# which importing this package does not.
+# ------------------------------ any number of tokens, experts, their training --
+# moe.py binds include/fp8moe.h, train.py include/fp8train.h.  They are loaded on
+# first use: they import torch, which importing this package does not.
 
 _MOE = ("fp8_linear", "fp8_linear_workspace_size", "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_experts",
         "fp8_moe_layer", "fp8_moe_workspace_size", "FP8_LINEAR_FP32_ROWS", "FP8MOE_BF16", "FP8MOE_FP32", "FP8MOE_MAX_EXPERTS",
         "FP8MOE_MAX_TOPK", "FP8MOE_MAX_TOKENS")
+_TRAIN = ("fp8_moe_sorted_rows", "fp8_moe_sort_workspace_size", "fp8_moe_sort", "fp8_moe_gather", "fp8_moe_combine",
+          "fp8_moe_combine_backward", "fp8_moe_gemm_fprop", "fp8_moe_gemm_dgrad", "fp8_moe_gemm_wgrad",
+          "fp8_gated_forward", "fp8_gated_backward", "fp8_requantize_colgroup")
 
 
 def __getattr__(name):
-    if name not in _MOE:
+    if name in _MOE:
+        from . import moe as module
+        names = _MOE
+    elif name in _TRAIN:
+        from . import train as module
+        names = _TRAIN
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import moe
-    globals().update({n: getattr(moe, n) for n in _MOE})
+    globals().update({n: getattr(module, n) for n in names})
     return globals()[name]

@@ -1,0 +1,78 @@
+// Internal launch entry points of the operators declared in include/fp8train.h.
+// Arguments are validated by the C ABI layer (api_train.cpp) before any of these
+// is called.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "fp8blk_launch.h"
+#include "fp8moe_launch.h"
+
+namespace fp8blk {
+
+// The workgroups that a sort's choices are dealt to, each a run of whole rounds
+// of kSortRound; one counts for itself, more leave their counts in the workspace.
+constexpr int64_t kSortRound = 1024, kSortMaxBlocks = 256, kSortAloneRounds = 4;
+struct SortPlan {
+  int64_t blocks, rounds;
+};
+inline SortPlan sort_plan(int64_t n) {
+  const int64_t all = (n + kSortRound - 1) / kSortRound;
+  if (all <= kSortAloneRounds) return {1, all};
+  const int64_t rounds = (all + kSortMaxBlocks - 1) / kSortMaxBlocks;
+  return {(all + rounds - 1) / rounds, rounds};
+}
+
+hipError_t launch_moe_sort(int64_t n, int E, int64_t R, const int32_t* ids, int32_t* rows, int32_t* source,
+                           int32_t* offsets, int32_t* counts, hipStream_t stream);
+
+// Codes in one orientation: where they go (null: not wanted) and their scales.
+struct CodesOut {
+  uint8_t* q;
+  int64_t ld;
+  float* s;
+};
+
+// weights may be null, used may be null (all rows); qT.q null: row groups only.
+struct GatherArgs {
+  int64_t T, H, R;
+  int k;
+  const uint16_t* x;
+  int64_t ld_x;
+  const int32_t* source;
+  const float* weights;
+  const int32_t* used;
+  CodesOut q, qT;
+  bool fp32_scale;
+};
+hipError_t launch_moe_gather(const GatherArgs& a, hipStream_t stream);
+
+hipError_t launch_moe_combine(int64_t T, int64_t H, int64_t R, int k, const uint16_t* z, int64_t ld_z,
+                              const int32_t* rows, const float* weights, RowsOut out, hipStream_t stream);
+hipError_t launch_moe_combine_dweights(int64_t T, int64_t H, int64_t R, int k, const uint16_t* dy, int64_t ld_dy,
+                                       const uint16_t* z, int64_t ld_z, const int32_t* rows, float* dweights,
+                                       hipStream_t stream);
+
+// qc.q may be null.
+hipError_t launch_gated_forward(int64_t M, int64_t I, const uint16_t* gu, int64_t ld_gu, const int32_t* used,
+                                CodesOut q, CodesOut qc, bool fp32_scale, hipStream_t stream);
+hipError_t launch_gated_backward(int64_t M, int64_t I, const uint16_t* dh, int64_t ld_dh, const uint8_t* qc,
+                                 int64_t ld_qc, const float* sc, const int32_t* used, CodesOut q, CodesOut qT,
+                                 CodesOut qhT, bool fp32_scale, hipStream_t stream);
+hipError_t launch_requantize_colgroup(const uint8_t* q, int64_t rows, int64_t cols, int64_t ld_q, const float* s,
+                                      const int32_t* used, CodesOut qT, bool fp32_scale, hipStream_t stream);
+
+// Every expert's contraction: a GemmArgs whose rows (Wgrad: reduction) are cut
+// into the experts' segments; b and sb (Wgrad: out) are expert 0's.
+struct GroupedArgs {
+  GemmArgs g;
+  const int32_t* offsets;  // [E + 1]
+  int64_t E;
+  int64_t b_stride, sb_stride, out_stride;  // from one expert to the next
+};
+hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);   // Fprop, Dgrad
+hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);
+
+}  // namespace fp8blk

@@ -1,0 +1,256 @@
+// The gated unit between two linears with its inputs kept in 8 bits, its
+// gradient from them, and row groups turned into column groups
+// (include/fp8train.h).
+//
+//   sig = 1 / (1 + e^-g),  h = g sig u,
+//   du = dh g sig,  dg = dh u sig (1 + g (1 - sig)).
+//
+// All are bound by memory: per element of h the forward pass moves 4 bytes in
+// and 3 out, the backward pass 4 in and 5 out, the turn 1 in and 1 out.
+#include "fp8blk_device.h"
+#include "fp8tile_device.h"
+#include "fp8train_launch.h"
+#include "fp8used_device.h"
+
+namespace fp8blk {
+
+namespace {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+
+// sigmoid(g).  e^-g is 2^(-g log2 e), off by about |g| 2^-24 of itself: for a
+// large g it vanishes beside 1, and for a very negative one the result, which is
+// then as far off, stays within 2^-17 wherever fp32 can hold it (g > -104), well
+// inside the bf16 rounding (2^-9) that follows.  The division is IEEE's.
+__device__ __forceinline__ float sigmoid(float g) {
+#pragma clang fp contract(off)
+  return 1.0f / (1.0f + exp2f(g * -1.4426950408889634f));
+}
+
+__device__ __forceinline__ float gated(float g, float u) {
+#pragma clang fp contract(off)
+  return g * sigmoid(g) * u;
+}
+
+// Eight bf16 of a group of 128 that 16 lanes hold, quantized.
+template <class S>
+__device__ __forceinline__ S quant_group(u32x4 v, uint2& o) {
+  uint32_t m = pk_max_u16(pk_max_u16(abs2(v.x), abs2(v.y)), pk_max_u16(abs2(v.z), abs2(v.w)));
+  m = row16_max(max(m & 0xFFFFu, m >> 16));
+  const S sc(m);
+  o.x = quant4(v.x, v.y, sc);
+  o.y = quant4(v.z, v.w, sc);
+  return sc;
+}
+
+// ---------------------------------------------------------------------------
+// Forward: 16 lanes to a group of 128 columns of g and of u, and of h.
+// ---------------------------------------------------------------------------
+constexpr int kUnroll = 2;
+constexpr int kGroupsPerWave = 4 * kUnroll;
+
+template <class S, bool KEEP>
+__global__ __launch_bounds__(kThreads) void gated_forward_kernel(int64_t M, uint32_t G, const uint16_t* __restrict__ gu,
+                                                                 int64_t ld_gu, const int32_t* __restrict__ used,
+                                                                 CodesOut q, CodesOut qc) {
+  const uint32_t lane = threadIdx.x & 63, sub = lane >> 4, l16 = lane & 15;
+  const uint32_t total = (uint32_t)used_rows(used, M) * G;
+  const uint32_t g0 = (blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)) * kGroupsPerWave;
+  if (g0 >= total) return;
+  const int64_t I = (int64_t)G * 128;
+  u32x4 g[kUnroll], u[kUnroll];
+  uint32_t row[kUnroll], grp[kUnroll];
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const uint32_t at = g0 + i * 4 + sub, a = at < total ? at : 0;
+    row[i] = a / G;
+    grp[i] = a - row[i] * G;
+    const uint16_t* p = gu + (int64_t)row[i] * ld_gu + grp[i] * 128 + l16 * 8;
+    g[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+    u[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + I));
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    u32x4 h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      h[j] = bf16x2_rne(gated(bf16_lo(g[i][j]), bf16_lo(u[i][j])), gated(bf16_hi(g[i][j]), bf16_hi(u[i][j])));
+    uint2 oh, og, ou;
+    const S sh = quant_group<S>(h, oh);
+    const bool live = g0 + i * 4 + sub < total;
+    const int64_t r = row[i];
+    const int64_t c = grp[i] * 128 + l16 * 8;
+    if (live) {
+      *reinterpret_cast<uint2*>(q.q + r * q.ld + c) = oh;
+      if (l16 == 0) q.s[r * G + grp[i]] = sh.s;
+    }
+    if constexpr (KEEP) {
+      const S sg = quant_group<S>(g[i], og);
+      const S su = quant_group<S>(u[i], ou);
+      if (live) {
+        *reinterpret_cast<uint2*>(qc.q + r * qc.ld + c) = og;
+        *reinterpret_cast<uint2*>(qc.q + r * qc.ld + I + c) = ou;
+        if (l16 == 0) {
+          qc.s[r * 2 * G + grp[i]] = sg.s;
+          qc.s[r * 2 * G + G + grp[i]] = su.s;
+        }
+      }
+    }
+  }
+}
+
+// Four E4M3 codes times their scale, rounded to bf16 (exact for power-of-two
+// scales from 2^-124 on), two to a word.
+__device__ __forceinline__ u32x2 decode4(uint32_t codes, float s) {
+  const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
+  const auto b = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
+  return u32x2{bf16x2_rne(a[0] * s, a[1] * s), bf16x2_rne(b[0] * s, b[1] * s)};
+}
+
+// The thread's 8 x 8 values of a 128 x 128 tile from its codes.  q: the tile's
+// first row, the thread's first column; s: the tile's first row, its group.
+__device__ __forceinline__ void decode_tile(const uint8_t* __restrict__ q, int64_t ld_q, const float* __restrict__ s,
+                                            int64_t ld_s, uint32_t rb, u32x4 (&v)[8]) {
+  u32x2 c[8];
+  float sc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(q + (int64_t)(rb * 8 + i) * ld_q));
+    sc[i] = s[(int64_t)(rb * 8 + i) * ld_s];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const u32x2 a = decode4(c[i].x, sc[i]), b = decode4(c[i].y, sc[i]);
+    v[i] = u32x4{a.x, a.y, b.x, b.y};
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward: a 128 x 128 tile of h, with the tiles of g and u that it comes from.
+// ---------------------------------------------------------------------------
+struct GatedBackward {
+  const uint16_t* dh;
+  int64_t ld_dh;
+  const uint8_t* qc;
+  int64_t ld_qc;
+  const float* sc;
+  const int32_t* used;
+  int64_t M;
+  CodesOut q, qT, qhT;
+};
+
+template <class S>
+__global__ __launch_bounds__(kTileThreads) void gated_backward_kernel(GatedBackward a, uint32_t row_tiles,
+                                                                      uint32_t col_tiles) {
+  __shared__ TileLds lds;
+  uint32_t rt, ct;
+  tile_of(blockIdx.x, col_tiles, tile_blocked(row_tiles, col_tiles), rt, ct);
+  if (rt >= used_tiles(a.used, a.M)) return;
+  const uint32_t rb = threadIdx.x >> 4, cb = threadIdx.x & 15;
+  const int64_t m0 = (int64_t)rt * 128, c0 = (int64_t)ct * 128, I = (int64_t)col_tiles * 128;
+  const uint32_t G = 2 * col_tiles;
+  u32x4 dh[8], g[8], u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    dh[i] = __builtin_nontemporal_load(
+        reinterpret_cast<const u32x4*>(a.dh + (m0 + rb * 8 + i) * a.ld_dh + c0 + cb * 8));
+  decode_tile(a.qc + m0 * a.ld_qc + c0 + cb * 8, a.ld_qc, a.sc + m0 * G + ct, G, rb, g);
+  decode_tile(a.qc + m0 * a.ld_qc + I + c0 + cb * 8, a.ld_qc, a.sc + m0 * G + col_tiles + ct, G, rb, u);
+  // g, u, dh -> dg, du, h, each in the place of the one that it replaces
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma clang fp contract(off)
+      float dg[2], du[2], h[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float gv = b ? bf16_hi(g[i][j]) : bf16_lo(g[i][j]), uv = b ? bf16_hi(u[i][j]) : bf16_lo(u[i][j]);
+        const float dv = b ? bf16_hi(dh[i][j]) : bf16_lo(dh[i][j]);
+        const float sig = sigmoid(gv), silu = gv * sig;
+        dg[b] = dv * uv * (sig * (1.0f + gv * (1.0f - sig)));
+        du[b] = dv * silu;
+        h[b] = silu * uv;
+      }
+      g[i][j] = bf16x2_rne(dg[0], dg[1]);
+      u[i][j] = bf16x2_rne(du[0], du[1]);
+      dh[i][j] = bf16x2_rne(h[0], h[1]);
+    }
+  }
+  tile_row_groups<S>(g, a.q.q + m0 * a.q.ld + c0 + cb * 8, a.q.ld, a.q.s + m0 * G + ct, G, rb, cb);
+  tile_row_groups<S>(u, a.q.q + m0 * a.q.ld + I + c0 + cb * 8, a.q.ld, a.q.s + m0 * G + col_tiles + ct, G, rb, cb);
+  tile_col_groups<S>(g, lds, a.qT.q + c0 * a.qT.ld + m0, a.qT.ld, a.qT.s + c0 * row_tiles + rt, row_tiles, rb, cb);
+  __syncthreads();
+  tile_col_groups<S>(u, lds, a.qT.q + (I + c0) * a.qT.ld + m0, a.qT.ld, a.qT.s + (I + c0) * row_tiles + rt, row_tiles,
+                     rb, cb);
+  __syncthreads();
+  tile_col_groups<S>(dh, lds, a.qhT.q + c0 * a.qhT.ld + m0, a.qhT.ld, a.qhT.s + c0 * row_tiles + rt, row_tiles, rb,
+                     cb);
+}
+
+template <class S>
+__global__ __launch_bounds__(kTileThreads) void requantize_kernel(const uint8_t* __restrict__ q, int64_t rows,
+                                                                  int64_t ld_q, const float* __restrict__ s,
+                                                                  const int32_t* __restrict__ used, CodesOut qT,
+                                                                  uint32_t row_tiles, uint32_t col_tiles) {
+  __shared__ TileLds lds;
+  uint32_t rt, ct;
+  tile_of(blockIdx.x, col_tiles, tile_blocked(row_tiles, col_tiles), rt, ct);
+  if (rt >= used_tiles(used, rows)) return;
+  const uint32_t rb = threadIdx.x >> 4, cb = threadIdx.x & 15;
+  const int64_t m0 = (int64_t)rt * 128, c0 = (int64_t)ct * 128;
+  u32x4 v[8];
+  decode_tile(q + m0 * ld_q + c0 + cb * 8, ld_q, s + m0 * col_tiles + ct, col_tiles, rb, v);
+  tile_col_groups<S>(v, lds, qT.q + c0 * qT.ld + m0, qT.ld, qT.s + c0 * row_tiles + rt, row_tiles, rb, cb);
+}
+
+template <class S>
+hipError_t forward(int64_t M, int64_t I, const uint16_t* gu, int64_t ld_gu, const int32_t* used, CodesOut q,
+                   CodesOut qc, hipStream_t stream) {
+  const uint32_t G = (uint32_t)(I / 128);
+  const uint32_t groups = (uint32_t)M * G, per = kGroupsPerWave * (kThreads / 64);
+  const dim3 grid((groups + per - 1) / per), block(kThreads);
+  if (qc.q)
+    hipLaunchKernelGGL((gated_forward_kernel<S, true>), grid, block, 0, stream, M, G, gu, ld_gu, used, q, qc);
+  else
+    hipLaunchKernelGGL((gated_forward_kernel<S, false>), grid, block, 0, stream, M, G, gu, ld_gu, used, q, qc);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gated_forward(int64_t M, int64_t I, const uint16_t* gu, int64_t ld_gu, const int32_t* used,
+                                CodesOut q, CodesOut qc, bool fp32_scale, hipStream_t stream) {
+  return fp32_scale ? forward<Fp32Scale>(M, I, gu, ld_gu, used, q, qc, stream)
+                    : forward<Pow2Scale>(M, I, gu, ld_gu, used, q, qc, stream);
+}
+
+hipError_t launch_gated_backward(int64_t M, int64_t I, const uint16_t* dh, int64_t ld_dh, const uint8_t* qc,
+                                 int64_t ld_qc, const float* sc, const int32_t* used, CodesOut q, CodesOut qT,
+                                 CodesOut qhT, bool fp32_scale, hipStream_t stream) {
+  const uint32_t row_tiles = (uint32_t)(M / 128), col_tiles = (uint32_t)(I / 128);
+  const GatedBackward a{dh, ld_dh, qc, ld_qc, sc, used, M, q, qT, qhT};
+  const dim3 grid(row_tiles * col_tiles), block(kTileThreads);
+  if (fp32_scale)
+    hipLaunchKernelGGL(gated_backward_kernel<Fp32Scale>, grid, block, 0, stream, a, row_tiles, col_tiles);
+  else
+    hipLaunchKernelGGL(gated_backward_kernel<Pow2Scale>, grid, block, 0, stream, a, row_tiles, col_tiles);
+  return hipGetLastError();
+}
+
+hipError_t launch_requantize_colgroup(const uint8_t* q, int64_t rows, int64_t cols, int64_t ld_q, const float* s,
+                                      const int32_t* used, CodesOut qT, bool fp32_scale, hipStream_t stream) {
+  const uint32_t row_tiles = (uint32_t)(rows / 128), col_tiles = (uint32_t)(cols / 128);
+  const dim3 grid(row_tiles * col_tiles), block(kTileThreads);
+  if (fp32_scale)
+    hipLaunchKernelGGL(requantize_kernel<Fp32Scale>, grid, block, 0, stream, q, rows, ld_q, s, used, qT, row_tiles,
+                       col_tiles);
+  else
+    hipLaunchKernelGGL(requantize_kernel<Pow2Scale>, grid, block, 0, stream, q, rows, ld_q, s, used, qT, row_tiles,
+                       col_tiles);
+  return hipGetLastError();
+}
+
+}  // namespace fp8blk

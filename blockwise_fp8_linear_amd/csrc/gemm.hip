@@ -45,6 +45,7 @@
 #include "fp8blk_device.h"
 #include "fp8blk_launch.h"
 #include "fp8blk_plan.h"
+#include "fp8grouped_device.h"
 
 namespace fp8blk {
 
@@ -553,6 +554,45 @@ __global__ __launch_bounds__(256) void gk_fixup_kernel(GemmArgs g, SkGeom sg, co
   }
 }
 
+// Every expert's product over its own segment of rows (Fprop and Dgrad of a
+// mixture): a persistent grid takes the tiles of all experts in turn, found by
+// the map that each workgroup makes at its start.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void grouped_rows_kernel(GroupedArgs a, int64_t tiles_n) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ GroupedLds map;
+  grouped_starts<C::THREADS>(map, a.offsets, a.E, a.g.I, C::BM, tiles_n);
+  const int64_t total = map.starts[a.E];
+  v4f acc[C::TM][C::TN];
+  for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+    const int64_t e = expert_of_tile(map, a.E, t);
+    const Segment s = segment_of(a.offsets, e, a.g.I);
+    const GemmArgs g = expert_rows(a, e, s);
+    int64_t i0, j0;
+    gk_tile_origin<C>(t - map.starts[e], (s.length + C::BM - 1) / C::BM, tiles_n, i0, j0);
+    gemm_tile<C>(g, lds, i0, j0, 0, g.R / 128, acc);
+    gk_store<C>(acc, g.out, g.J, g.I, g.J, g.out_f32, g.accumulate, i0, j0);
+  }
+}
+
+// Every expert's Wgrad: the reduction runs over its segment alone.  A segment
+// without rows leaves zeros.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void grouped_wgrad_kernel(GroupedArgs a, int64_t tiles_m, int64_t tiles_n) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int64_t tiles = tiles_m * tiles_n, total = a.E * tiles;
+  v4f acc[C::TM][C::TN];
+  for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+    const int64_t e = t / tiles;
+    const Segment s = segment_of(a.offsets, e, a.g.R);
+    int64_t i0, j0;
+    gk_tile_origin<C>(t - e * tiles, tiles_m, tiles_n, i0, j0);
+    gemm_tile<C>(a.g, lds, i0, j0, s.first / 128, (s.first + s.length) / 128, acc);
+    gk_store<C>(acc, element(a.g.out, e * a.out_stride, a.g.out_f32), a.g.J, a.g.I, a.g.J, a.g.out_f32,
+                a.g.accumulate, i0, j0);
+  }
+}
+
 // ------------------------------------------------------------ dispatch ----
 
 using PromoteBlock = Cfg<256, 128, 2, 2, true, false>;
@@ -609,6 +649,42 @@ hipError_t launch_gemm(const GemmArgs& g, GemmAlgo algo, hipStream_t stream) {
   if (g.bmode == BScale::Row)
     return algo == GemmAlgo::Promote ? launch_cfg_sk<PromoteRow>(g, stream) : launch_cfg_sk<ScaledRow>(g, stream);
   return algo == GemmAlgo::Promote ? launch_cfg<PromoteBlock>(g, stream) : launch_cfg<ScaledBlock>(g, stream);
+}
+
+template <class C>
+static hipError_t launch_grouped_rows_cfg(const GroupedArgs& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.g.J + C::BN - 1) / C::BN;
+  const int64_t most = (a.g.I / C::BM + a.E) * tiles_n;  // tiles of any segments of so many rows
+  static std::atomic<uint64_t> attr_set{0};
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_rows_kernel<C>), C::LDS, &attr_set))
+    return e;
+  hipLaunchKernelGGL(grouped_rows_kernel<C>, dim3((uint32_t)(most < kSkGrid ? most : kSkGrid)), dim3(C::THREADS),
+                     C::LDS, stream, a, tiles_n);
+  return hipGetLastError();
+}
+
+template <class C>
+static hipError_t launch_grouped_wgrad_cfg(const GroupedArgs& a, hipStream_t stream) {
+  const int64_t tiles_m = (a.g.I + C::BM - 1) / C::BM, tiles_n = (a.g.J + C::BN - 1) / C::BN;
+  const int64_t total = a.E * tiles_m * tiles_n;
+  static std::atomic<uint64_t> attr_set{0};
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_wgrad_kernel<C>), C::LDS, &attr_set))
+    return e;
+  hipLaunchKernelGGL(grouped_wgrad_kernel<C>, dim3((uint32_t)(total < kSkGrid ? total : kSkGrid)), dim3(C::THREADS),
+                     C::LDS, stream, a, tiles_m, tiles_n);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
+  const bool promote = algo == GemmAlgo::Promote;
+  if (a.g.bt)
+    return promote ? launch_grouped_rows_cfg<PromoteBlockBT>(a, stream) : launch_grouped_rows_cfg<ScaledBlockBT>(a, stream);
+  return promote ? launch_grouped_rows_cfg<PromoteBlock>(a, stream) : launch_grouped_rows_cfg<ScaledBlock>(a, stream);
+}
+
+hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
+  return algo == GemmAlgo::Promote ? launch_grouped_wgrad_cfg<PromoteRow>(a, stream)
+                                   : launch_grouped_wgrad_cfg<ScaledRow>(a, stream);
 }
 
 }  // namespace fp8blk
