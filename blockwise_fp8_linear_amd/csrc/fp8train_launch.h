@@ -74,5 +74,8 @@ struct GroupedArgs {
 };
 hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);   // Fprop, Dgrad
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);
+// All three on the 256x256 block-scaled-MFMA kernels (gemm_mx.hip): Fprop and
+// Dgrad for the shapes that gemm_mx_eligible(a.g) takes, Wgrad up to 2^22 rows.
+hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream);
 
 }  // namespace fp8blk

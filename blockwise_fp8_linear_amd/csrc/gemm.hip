@@ -677,12 +677,15 @@ static hipError_t launch_grouped_wgrad_cfg(const GroupedArgs& a, hipStream_t str
 
 hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
   const bool promote = algo == GemmAlgo::Promote;
+  if (!promote && gemm_mx_eligible(a.g)) return launch_grouped_mx(a, stream);
   if (a.g.bt)
     return promote ? launch_grouped_rows_cfg<PromoteBlockBT>(a, stream) : launch_grouped_rows_cfg<ScaledBlockBT>(a, stream);
   return promote ? launch_grouped_rows_cfg<PromoteBlock>(a, stream) : launch_grouped_rows_cfg<ScaledBlock>(a, stream);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
+  // per-lane 32-bit offsets: 256 rows of R bytes
+  if (algo == GemmAlgo::ScaledMfma && a.g.R <= (int64_t(1) << 22)) return launch_grouped_mx(a, stream);
   return algo == GemmAlgo::Promote ? launch_grouped_wgrad_cfg<PromoteRow>(a, stream)
                                    : launch_grouped_wgrad_cfg<ScaledRow>(a, stream);
 }

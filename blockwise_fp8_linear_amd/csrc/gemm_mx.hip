@@ -43,6 +43,7 @@
 #include "fp8blk_device.h"
 #include "fp8blk_launch.h"
 #include "fp8blk_plan.h"
+#include "fp8grouped_device.h"
 
 namespace fp8blk {
 
@@ -112,15 +113,19 @@ __device__ __forceinline__ void tile_origin(int64_t tile, int64_t tiles_m, int64
 }
 
 // The contraction of one output tile over the 128-blocks
-// [kb_begin, kb_begin + nkb_seg) (nkb_seg a multiple of 4) into acc, which it
-// zeroes first.  On return every direct load has landed; the LDS ring may
-// still be read by other waves until the next barrier.
+// [kb_begin, kb_begin + nkb_seg) (kb_begin and nkb_seg multiples of 4) into acc,
+// which it zeroes first.  On return every direct load has landed; the LDS ring
+// may still be read by other waves until the next barrier.
 // BT: B is stored [R][J] (the weight codes W[n][k] read as quantized, for
 // Dgrad) instead of [J][R]; weight-block scales only.
-template <bool BROW, bool BT = false>
+// RAGGED: any 128-blocks, at least one, from any of them on.  Their scales are
+// then not 16-byte aligned and are loaded one by one; the last group of four may
+// hold fewer blocks.
+template <bool BROW, bool BT = false, bool RAGGED = false>
 __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int64_t i0, int64_t j0, int64_t kb_begin,
                                             int64_t nkb_seg, v16f (&acc)[TM][TN]) {
   static_assert(!(BT && BROW), "the transposed-B layout is Dgrad's, with weight-block scales");
+  static_assert(!RAGGED || BROW, "weight-block scales are loaded for whole groups");
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t wm = wave >> 1, wn = wave & 1;
@@ -201,8 +206,18 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   }
   const uint32_t sc0 = lds0 + SLOTS * SLOT;
   auto issue_scales = [&](int q) {  // group q -> scale buffer q & 1
-    const int qc = q < ngroup ? q : ngroup - 1;
     const uint32_t buf = sc0 + (uint32_t)(q & 1) * SC_BYTES;
+    if constexpr (RAGGED) {
+      // [block of the group][row]; a block past the end loads the last one's
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = 4 * q + i < npair ? 4 * q + i : npair - 1;
+        dma4(baseSA + 4 * k, offSA, buf + i * 1024 + wave * 256);
+        dma4(baseSB + 4 * k, offSB, buf + 4096 + i * 1024 + wave * 256);
+      }
+      return;
+    }
+    const int qc = q < ngroup ? q : ngroup - 1;
     dma16(baseSA + 16 * qc, offSA, buf + wave * 1024);
     if constexpr (BROW) dma16(baseSB + 16 * qc, offSB, buf + 4096 + wave * 1024);
   };
@@ -273,6 +288,19 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   };
   auto read_scales = [&](int q, uint32_t* pa, uint32_t* pb) {
     const uint8_t* buf = sc_lds + (q & 1) * SC_BYTES;
+    if constexpr (RAGGED) {
+      const auto four = [](const uint8_t* p) {
+        u32x4 s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const uint32_t*>(p + i * 1024);
+        return pack_e8(s);
+      };
+#pragma unroll
+      for (int t = 0; t < TM; ++t) pa[t] = four(buf + (wm0 + t * 32 + l32) * 4);
+#pragma unroll
+      for (int t = 0; t < TN; ++t) pb[t] = four(buf + 4096 + (wn0 + t * 32 + l32) * 4);
+      return;
+    }
 #pragma unroll
     for (int t = 0; t < TM; ++t) pa[t] = pack_e8(*reinterpret_cast<const u32x4*>(buf + (wm0 + t * 32 + l32) * 16));
     if constexpr (BROW) {
@@ -346,22 +374,42 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
     }
   };
 
-  // One loop iteration = one group = four 128-blocks = eight 64-deep stages;
-  // op_sel (the byte of the packed scales) is a constant in each step.
-  for (int q = 0; q < ngroup; ++q) {
-    const int st = 8 * q;
-    issue_scales(q + 1);  // buffer (q+1)&1 was last read at the end of group q-2
-    stage_step(st + 0, IntC<0>{}, IntC<0>{});
-    stage_step(st + 1, IntC<1>{}, IntC<0>{});
-    stage_step(st + 2, IntC<0>{}, IntC<1>{});
-    stage_step(st + 3, IntC<1>{}, IntC<1>{});
-    stage_step(st + 4, IntC<0>{}, IntC<2>{});
-    stage_step(st + 5, IntC<1>{}, IntC<2>{});
-    stage_step(st + 6, IntC<0>{}, IntC<3>{});
-    stage_step(st + 7, IntC<1>{}, IntC<3>{});
-    // group q+1's scales were issued before the waits of this group's odd
-    // stages and every wave passed their barriers
-    read_scales(q + 1, sa_cur, sb_cur);
+  if constexpr (RAGGED) {
+    // One iteration = one 128-block.  The byte of the packed scales that it takes
+    // is shifted to the bottom: by op_sel, the last group's blocks would need
+    // copies of the stages behind the loop, and the compiler runs out of
+    // registers where they meet.
+    for (int p = 0; p < npair; ++p) {
+      if ((p & 3) == 0) issue_scales((p >> 2) + 1);
+      stage_step(2 * p, IntC<0>{}, IntC<0>{});
+      stage_step(2 * p + 1, IntC<1>{}, IntC<0>{});
+      if ((p & 3) == 3) {
+        read_scales((p >> 2) + 1, sa_cur, sb_cur);
+      } else {
+#pragma unroll
+        for (int t = 0; t < TM; ++t) sa_cur[t] >>= 8;
+#pragma unroll
+        for (int t = 0; t < TN; ++t) sb_cur[t] >>= 8;
+      }
+    }
+  } else {
+    // One loop iteration = one group = four 128-blocks = eight 64-deep stages;
+    // op_sel (the byte of the packed scales) is a constant in each step.
+    for (int q = 0; q < ngroup; ++q) {
+      const int st = 8 * q;
+      issue_scales(q + 1);  // buffer (q+1)&1 was last read at the end of group q-2
+      stage_step(st + 0, IntC<0>{}, IntC<0>{});
+      stage_step(st + 1, IntC<1>{}, IntC<0>{});
+      stage_step(st + 2, IntC<0>{}, IntC<1>{});
+      stage_step(st + 3, IntC<1>{}, IntC<1>{});
+      stage_step(st + 4, IntC<0>{}, IntC<2>{});
+      stage_step(st + 5, IntC<1>{}, IntC<2>{});
+      stage_step(st + 6, IntC<0>{}, IntC<3>{});
+      stage_step(st + 7, IntC<1>{}, IntC<3>{});
+      // group q+1's scales were issued before the waits of this group's odd
+      // stages and every wave passed their barriers
+      read_scales(q + 1, sa_cur, sb_cur);
+    }
   }
   wait_vmcnt<0>();  // no direct load may still target this workgroup's LDS at exit
 }
@@ -518,6 +566,17 @@ __device__ __forceinline__ void store_tile(const Dst& d, uint8_t* lds, int64_t i
 #pragma unroll
     for (int b = 0; b < TN; ++b) acc[a][b] = acc_in[a][b];
   store_tile_from<BATCH>(d, lds, i0, j0, [&](int a, int b) { return acc[a][b]; });
+}
+
+// A tile of zeros; what accumulates stays as it is.
+__device__ __forceinline__ void zero_tile(const Dst& d, int64_t i0, int64_t j0) {
+  if (d.acc) return;
+  const int64_t bytes = d.f32 ? 4 : 2, per = 16 / bytes, cols = d.cols - j0 < BN ? d.cols - j0 : BN;
+  const int64_t rows = d.rows - i0 < BM ? d.rows - i0 : BM;
+  for (int64_t k = threadIdx.x; k < rows * (cols / per); k += THREADS) {
+    const int64_t i = i0 + k / (cols / per), j = j0 + k % (cols / per) * per;
+    *reinterpret_cast<u32x4*>(static_cast<char*>(d.out) + (i * d.ld + j) * bytes) = u32x4{0, 0, 0, 0};
+  }
 }
 
 // One output tile per workgroup, the whole reduction (Fprop and Dgrad; BT:
@@ -769,6 +828,48 @@ __global__ __launch_bounds__(256) void bwd_fixup_kernel(GemmArgs gd, GemmArgs gw
   }
 }
 
+// Every expert's product over its own segment of rows (Fprop and Dgrad of a
+// mixture; BT: Dgrad from the weight codes as quantized): a persistent grid takes
+// the tiles of all experts in turn, found by the map that each workgroup makes at
+// its start.
+template <bool BT>
+__global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a, int64_t tiles_n) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  __shared__ GroupedLds map;
+  grouped_starts<THREADS>(map, a.offsets, a.E, a.g.I, BM, tiles_n);
+  const int64_t total = map.starts[a.E];
+  v16f acc[TM][TN];
+  for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+    const int64_t e = expert_of_tile(map, a.E, t);
+    const Segment s = segment_of(a.offsets, e, a.g.I);
+    const GemmArgs g = expert_rows(a, e, s);
+    int64_t i0, j0;
+    tile_origin(t - map.starts[e], (s.length + BM - 1) / BM, tiles_n, i0, j0);
+    lds_barrier();  // the previous tile's epilogue is done with LDS
+    mma_segment<false, BT>(g, lds, i0, j0, 0, g.R / 128, acc);
+    store_tile<1>(Dst{g.out, g.J, g.I, g.J, g.out_f32, g.accumulate}, lds, i0, j0, acc);
+  }
+}
+
+// Every expert's Wgrad, its reduction over its own segment alone: a tile a
+// workgroup, as the segments differ in length and the hardware's own order evens
+// that out.
+__global__ __launch_bounds__(THREADS) void grouped_mx_wgrad_kernel(GroupedArgs a, int64_t tiles_m, int64_t tiles_n) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int64_t t = xcd_remap(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n, e = t / tiles;
+  const Segment s = segment_of(a.offsets, e, a.g.R);
+  int64_t i0, j0;
+  tile_origin(t - e * tiles, tiles_m, tiles_n, i0, j0);
+  const Dst d{element(a.g.out, e * a.out_stride, a.g.out_f32), a.g.J, a.g.I, a.g.J, a.g.out_f32, a.g.accumulate};
+  if (s.length == 0) {
+    zero_tile(d, i0, j0);
+    return;
+  }
+  v16f acc[TM][TN];
+  mma_segment<true, false, true>(a.g, lds, i0, j0, s.first / 128, s.length / 128, acc);
+  store_tile<8>(d, lds, i0, j0, acc);
+}
+
 template <class K>
 hipError_t set_lds_attr(K* kernel, std::atomic<uint64_t>* done) {
   return ensure_lds_limit(reinterpret_cast<const void*>(kernel), LDS_BYTES, done);
@@ -816,7 +917,29 @@ hipError_t launch_bwd(const GemmArgs& gd, const GemmArgs& gw, float* ws, hipStre
   return hipGetLastError();
 }
 
+template <bool BT>
+hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.g.J + BN - 1) / BN;
+  const int64_t most = (a.g.I / BM + a.E) * tiles_n;  // tiles of any segments of so many rows
+  static std::atomic<uint64_t> attr_set{0};
+  if (hipError_t e = set_lds_attr(&grouped_mx_rows_kernel<BT>, &attr_set)) return e;
+  hipLaunchKernelGGL(grouped_mx_rows_kernel<BT>, dim3((uint32_t)(most < kSkGrid ? most : kSkGrid)), dim3(THREADS),
+                     LDS_BYTES, stream, a, tiles_n);
+  return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream) {
+  if (a.g.bmode == BScale::Block)
+    return a.g.bt ? launch_grouped_rows_mx<true>(a, stream) : launch_grouped_rows_mx<false>(a, stream);
+  const int64_t tiles_m = (a.g.I + BM - 1) / BM, tiles_n = (a.g.J + BN - 1) / BN, total = a.E * tiles_m * tiles_n;
+  static std::atomic<uint64_t> attr_set{0};
+  if (hipError_t e = set_lds_attr(&grouped_mx_wgrad_kernel, &attr_set)) return e;
+  hipLaunchKernelGGL(grouped_mx_wgrad_kernel, dim3((uint32_t)total), dim3(THREADS), LDS_BYTES, stream, a, tiles_m,
+                     tiles_n);
+  return hipGetLastError();
+}
 
 hipError_t launch_gemm_mx(const GemmArgs& g, hipStream_t stream) {
   if (g.bmode == BScale::Row) return launch_mx_streamk<true>(g, stream);

@@ -134,7 +134,7 @@ int fp8_moe_combine_backward(int64_t T, int64_t H, int64_t R, int k, const uint1
  *   scale_mode: the rule that made all the scales.
  * Rows of y and dx outside the segments are not written.  All operands dense,
  * 16-byte aligned (offsets 4-byte); R, N, K positive multiples of 128, R < 2^31,
- * N, K < 2^25, E <= FP8MOE_MAX_EXPERTS, R N, R K and E N K at most 2^40.
+ * N, K < 2^25, E <= FP8MOE_MAX_EXPERTS, R N and R K at most 2^40, E N K 2^38.
  * Results do not depend on how rows are spread over the other experts; sums are
  * fp32 with the accuracy of the GEMMs of fp8blk.h.
  */
