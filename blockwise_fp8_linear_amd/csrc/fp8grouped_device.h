@@ -75,6 +75,35 @@ __device__ __forceinline__ int64_t expert_of_tile(const GroupedLds& lds, int64_t
   return lo;
 }
 
+// The expert whose segment is the at-th longest, equal ones by index: every thread
+// of a workgroup calls it (which ends with a barrier).  Each counts the experts
+// before its own, four a step, so it is for a few hundred at most.
+constexpr int kGroupedOrderE = 256;
+struct GroupedOrder {
+  __attribute__((aligned(16))) int32_t blocks[kGroupedOrderE];  // of each expert; behind the last one -1
+  int found;
+};
+__device__ __forceinline__ int expert_by_load(GroupedOrder& lds, const int32_t* __restrict__ offsets, int E,
+                                              int64_t rows, int at) {
+  typedef int v4i __attribute__((ext_vector_type(4)));
+  const int e = threadIdx.x;
+  const int mine = e < E ? (int)(segment_of(offsets, e, rows).length / 128) : -1;
+  if (e < kGroupedOrderE) lds.blocks[e] = mine;
+  __syncthreads();
+  if (e < E) {
+    int before = 0;
+#pragma unroll 8
+    for (int o = 0; o < E; o += 4) {
+      const v4i b = *reinterpret_cast<const v4i*>(lds.blocks + o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) before += b[i] > mine || (b[i] == mine && o + i < e) ? 1 : 0;
+    }
+    if (before == at) lds.found = e;
+  }
+  __syncthreads();
+  return lds.found;
+}
+
 // Output element i of a matrix of fp32 or bf16.
 __device__ __forceinline__ void* element(void* out, int64_t i, bool f32) {
   return f32 ? (void*)(static_cast<float*>(out) + i) : (void*)(static_cast<uint16_t*>(out) + i);

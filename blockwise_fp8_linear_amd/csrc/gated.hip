@@ -109,23 +109,25 @@ __device__ __forceinline__ u32x2 decode4(uint32_t codes, float s) {
   return u32x2{bf16x2_rne(a[0] * s, a[1] * s), bf16x2_rne(b[0] * s, b[1] * s)};
 }
 
-// The thread's 8 x 8 values of a 128 x 128 tile from its codes.  q: the tile's
-// first row, the thread's first column; s: the tile's first row, its group.
-__device__ __forceinline__ void decode_tile(const uint8_t* __restrict__ q, int64_t ld_q, const float* __restrict__ s,
-                                            int64_t ld_s, uint32_t rb, u32x4 (&v)[8]) {
+// A thread's eight codes of each of its 8 rows of a 128 x 128 tile and the rows'
+// scales.  q: the tile's first row, the thread's first column; s: the tile's first
+// row, its group.
+struct CodesTile {
   u32x2 c[8];
-  float sc[8];
+  float s[8];
+  __device__ __forceinline__ void load(const uint8_t* __restrict__ q, int64_t ld_q, const float* __restrict__ sc,
+                                       int64_t ld_s, uint32_t rb) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(q + (int64_t)(rb * 8 + i) * ld_q));
-    sc[i] = s[(int64_t)(rb * 8 + i) * ld_s];
+    for (int i = 0; i < 8; ++i) {
+      c[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(q + (int64_t)(rb * 8 + i) * ld_q));
+      s[i] = sc[(int64_t)(rb * 8 + i) * ld_s];
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const u32x2 a = decode4(c[i].x, sc[i]), b = decode4(c[i].y, sc[i]);
-    v[i] = u32x4{a.x, a.y, b.x, b.y};
+  __device__ __forceinline__ u32x4 row(int i) const {
+    const u32x2 a = decode4(c[i].x, s[i]), b = decode4(c[i].y, s[i]);
+    return u32x4{a.x, a.y, b.x, b.y};
   }
-}
+};
 
 // ---------------------------------------------------------------------------
 // Backward: a 128 x 128 tile of h, with the tiles of g and u that it comes from.
@@ -141,69 +143,94 @@ struct GatedBackward {
   CodesOut q, qT, qhT;
 };
 
-template <class S>
-__global__ __launch_bounds__(kTileThreads) void gated_backward_kernel(GatedBackward a, uint32_t row_tiles,
-                                                                      uint32_t col_tiles) {
+// Two values rounded to bf16, now: the compiler would put the rounding off to where
+// the word is used and keep both values until then.
+__device__ __forceinline__ uint32_t rounded_here(float lo, float hi) {
+  uint32_t w = bf16x2_rne(lo, hi);
+  asm volatile("" : "+v"(w));
+  return w;
+}
+
+// dg, du and h of eight elements, two to a word.
+__device__ __forceinline__ void gated_row(u32x4 g, u32x4 u, u32x4 dh, u32x4& dg, u32x4& du, u32x4& h) {
+#pragma clang fp contract(off)
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float o[3][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const float gv = b ? bf16_hi(g[j]) : bf16_lo(g[j]), uv = b ? bf16_hi(u[j]) : bf16_lo(u[j]);
+      const float dv = b ? bf16_hi(dh[j]) : bf16_lo(dh[j]);
+      const float sig = sigmoid(gv), silu = gv * sig;
+      o[0][b] = dv * uv * (sig * (1.0f + gv * (1.0f - sig)));
+      o[1][b] = dv * silu;
+      o[2][b] = silu * uv;
+    }
+    dg[j] = rounded_here(o[0][0], o[0][1]);
+    du[j] = rounded_here(o[1][0], o[1][1]);
+    h[j] = rounded_here(o[2][0], o[2][1]);
+  }
+}
+
+template <class S, bool NT>
+__global__ __launch_bounds__(kTileThreads, 2) void gated_backward_kernel(GatedBackward a, TileGrid grid) {
   __shared__ TileLds lds;
+  const uint32_t row_tiles = grid.row_tiles, col_tiles = grid.col_tiles;
   uint32_t rt, ct;
-  tile_of(blockIdx.x, col_tiles, tile_blocked(row_tiles, col_tiles), rt, ct);
-  if (rt >= used_tiles(a.used, a.M)) return;
+  tile_of(blockIdx.x, col_tiles, grid.blocked, rt, ct);
+  if (ct >= col_tiles || rt >= used_tiles(a.used, a.M)) return;
   const uint32_t rb = threadIdx.x >> 4, cb = threadIdx.x & 15;
   const int64_t m0 = (int64_t)rt * 128, c0 = (int64_t)ct * 128, I = (int64_t)col_tiles * 128;
   const uint32_t G = 2 * col_tiles;
   u32x4 dh[8], g[8], u[8];
+  CodesTile cg, cu;
+  cg.load(a.qc + m0 * a.ld_qc + c0 + cb * 8, a.ld_qc, a.sc + m0 * G + ct, G, rb);
+  cu.load(a.qc + m0 * a.ld_qc + I + c0 + cb * 8, a.ld_qc, a.sc + m0 * G + col_tiles + ct, G, rb);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     dh[i] = __builtin_nontemporal_load(
         reinterpret_cast<const u32x4*>(a.dh + (m0 + rb * 8 + i) * a.ld_dh + c0 + cb * 8));
-  decode_tile(a.qc + m0 * a.ld_qc + c0 + cb * 8, a.ld_qc, a.sc + m0 * G + ct, G, rb, g);
-  decode_tile(a.qc + m0 * a.ld_qc + I + c0 + cb * 8, a.ld_qc, a.sc + m0 * G + col_tiles + ct, G, rb, u);
-  // g, u, dh -> dg, du, h, each in the place of the one that it replaces
+  // dg, du, and h in dh's place, row by row: the fence keeps the compiler from
+  // working on all rows at once, which takes 372 registers (one wave a SIMD)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma clang fp contract(off)
-      float dg[2], du[2], h[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const float gv = b ? bf16_hi(g[i][j]) : bf16_lo(g[i][j]), uv = b ? bf16_hi(u[i][j]) : bf16_lo(u[i][j]);
-        const float dv = b ? bf16_hi(dh[i][j]) : bf16_lo(dh[i][j]);
-        const float sig = sigmoid(gv), silu = gv * sig;
-        dg[b] = dv * uv * (sig * (1.0f + gv * (1.0f - sig)));
-        du[b] = dv * silu;
-        h[b] = silu * uv;
-      }
-      g[i][j] = bf16x2_rne(dg[0], dg[1]);
-      u[i][j] = bf16x2_rne(du[0], du[1]);
-      dh[i][j] = bf16x2_rne(h[0], h[1]);
-    }
+    __builtin_amdgcn_sched_barrier(0);
+    gated_row(cg.row(i), cu.row(i), dh[i], g[i], u[i], dh[i]);
   }
-  tile_row_groups<S>(g, a.q.q + m0 * a.q.ld + c0 + cb * 8, a.q.ld, a.q.s + m0 * G + ct, G, rb, cb);
-  tile_row_groups<S>(u, a.q.q + m0 * a.q.ld + I + c0 + cb * 8, a.q.ld, a.q.s + m0 * G + col_tiles + ct, G, rb, cb);
-  tile_col_groups<S>(g, lds, a.qT.q + c0 * a.qT.ld + m0, a.qT.ld, a.qT.s + c0 * row_tiles + rt, row_tiles, rb, cb);
+  __builtin_amdgcn_sched_barrier(0);
+  tile_row_groups<S, NT>(g, a.q.q + m0 * a.q.ld + c0 + cb * 8, a.q.ld, a.q.s + m0 * G + ct, G, rb, cb);
+  __builtin_amdgcn_sched_barrier(0);
+  tile_row_groups<S, NT>(u, a.q.q + m0 * a.q.ld + I + c0 + cb * 8, a.q.ld, a.q.s + m0 * G + col_tiles + ct, G, rb, cb);
+  __builtin_amdgcn_sched_barrier(0);
+  tile_col_groups<S, NT>(g, lds, a.qT.q + c0 * a.qT.ld + m0, a.qT.ld, a.qT.s + c0 * row_tiles + rt, row_tiles, rb, cb);
   __syncthreads();
-  tile_col_groups<S>(u, lds, a.qT.q + (I + c0) * a.qT.ld + m0, a.qT.ld, a.qT.s + (I + c0) * row_tiles + rt, row_tiles,
+  __builtin_amdgcn_sched_barrier(0);
+  tile_col_groups<S, NT>(u, lds, a.qT.q + (I + c0) * a.qT.ld + m0, a.qT.ld, a.qT.s + (I + c0) * row_tiles + rt, row_tiles,
                      rb, cb);
   __syncthreads();
-  tile_col_groups<S>(dh, lds, a.qhT.q + c0 * a.qhT.ld + m0, a.qhT.ld, a.qhT.s + c0 * row_tiles + rt, row_tiles, rb,
+  __builtin_amdgcn_sched_barrier(0);
+  tile_col_groups<S, NT>(dh, lds, a.qhT.q + c0 * a.qhT.ld + m0, a.qhT.ld, a.qhT.s + c0 * row_tiles + rt, row_tiles, rb,
                      cb);
 }
 
-template <class S>
+template <class S, bool NT>
 __global__ __launch_bounds__(kTileThreads) void requantize_kernel(const uint8_t* __restrict__ q, int64_t rows,
                                                                   int64_t ld_q, const float* __restrict__ s,
                                                                   const int32_t* __restrict__ used, CodesOut qT,
-                                                                  uint32_t row_tiles, uint32_t col_tiles) {
+                                                                  TileGrid grid) {
   __shared__ TileLds lds;
+  const uint32_t row_tiles = grid.row_tiles, col_tiles = grid.col_tiles;
   uint32_t rt, ct;
-  tile_of(blockIdx.x, col_tiles, tile_blocked(row_tiles, col_tiles), rt, ct);
-  if (rt >= used_tiles(used, rows)) return;
+  tile_of(blockIdx.x, col_tiles, grid.blocked, rt, ct);
+  if (ct >= col_tiles || rt >= used_tiles(used, rows)) return;
   const uint32_t rb = threadIdx.x >> 4, cb = threadIdx.x & 15;
   const int64_t m0 = (int64_t)rt * 128, c0 = (int64_t)ct * 128;
+  CodesTile c;
+  c.load(q + m0 * ld_q + c0 + cb * 8, ld_q, s + m0 * col_tiles + ct, col_tiles, rb);
   u32x4 v[8];
-  decode_tile(q + m0 * ld_q + c0 + cb * 8, ld_q, s + m0 * col_tiles + ct, col_tiles, rb, v);
-  tile_col_groups<S>(v, lds, qT.q + c0 * qT.ld + m0, qT.ld, qT.s + c0 * row_tiles + rt, row_tiles, rb, cb);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c.row(i);
+  tile_col_groups<S, NT>(v, lds, qT.q + c0 * qT.ld + m0, qT.ld, qT.s + c0 * row_tiles + rt, row_tiles, rb, cb);
 }
 
 template <class S>
@@ -219,6 +246,18 @@ hipError_t forward(int64_t M, int64_t I, const uint16_t* gu, int64_t ld_gu, cons
   return hipGetLastError();
 }
 
+template <class S, bool NT>
+void backward(const GatedBackward& a, const TileGrid& g, hipStream_t stream) {
+  hipLaunchKernelGGL((gated_backward_kernel<S, NT>), dim3(g.workgroups), dim3(kTileThreads), 0, stream, a, g);
+}
+
+template <class S, bool NT>
+void requantize(const uint8_t* q, int64_t rows, int64_t ld_q, const float* s, const int32_t* used, CodesOut qT,
+                const TileGrid& g, hipStream_t stream) {
+  hipLaunchKernelGGL((requantize_kernel<S, NT>), dim3(g.workgroups), dim3(kTileThreads), 0, stream, q, rows, ld_q, s,
+                     used, qT, g);
+}
+
 }  // namespace
 
 hipError_t launch_gated_forward(int64_t M, int64_t I, const uint16_t* gu, int64_t ld_gu, const int32_t* used,
@@ -230,26 +269,26 @@ hipError_t launch_gated_forward(int64_t M, int64_t I, const uint16_t* gu, int64_
 hipError_t launch_gated_backward(int64_t M, int64_t I, const uint16_t* dh, int64_t ld_dh, const uint8_t* qc,
                                  int64_t ld_qc, const float* sc, const int32_t* used, CodesOut q, CodesOut qT,
                                  CodesOut qhT, bool fp32_scale, hipStream_t stream) {
-  const uint32_t row_tiles = (uint32_t)(M / 128), col_tiles = (uint32_t)(I / 128);
+  const TileGrid g = tile_grid(M, I);
   const GatedBackward a{dh, ld_dh, qc, ld_qc, sc, used, M, q, qT, qhT};
-  const dim3 grid(row_tiles * col_tiles), block(kTileThreads);
+  const bool nt = 5 * M * I > kStoreNt;
   if (fp32_scale)
-    hipLaunchKernelGGL(gated_backward_kernel<Fp32Scale>, grid, block, 0, stream, a, row_tiles, col_tiles);
+    nt ? backward<Fp32Scale, true>(a, g, stream) : backward<Fp32Scale, false>(a, g, stream);
   else
-    hipLaunchKernelGGL(gated_backward_kernel<Pow2Scale>, grid, block, 0, stream, a, row_tiles, col_tiles);
+    nt ? backward<Pow2Scale, true>(a, g, stream) : backward<Pow2Scale, false>(a, g, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_requantize_colgroup(const uint8_t* q, int64_t rows, int64_t cols, int64_t ld_q, const float* s,
                                       const int32_t* used, CodesOut qT, bool fp32_scale, hipStream_t stream) {
-  const uint32_t row_tiles = (uint32_t)(rows / 128), col_tiles = (uint32_t)(cols / 128);
-  const dim3 grid(row_tiles * col_tiles), block(kTileThreads);
+  const TileGrid g = tile_grid(rows, cols);
+  const bool nt = rows * cols > kStoreNt;
   if (fp32_scale)
-    hipLaunchKernelGGL(requantize_kernel<Fp32Scale>, grid, block, 0, stream, q, rows, ld_q, s, used, qT, row_tiles,
-                       col_tiles);
+    nt ? requantize<Fp32Scale, true>(q, rows, ld_q, s, used, qT, g, stream)
+       : requantize<Fp32Scale, false>(q, rows, ld_q, s, used, qT, g, stream);
   else
-    hipLaunchKernelGGL(requantize_kernel<Pow2Scale>, grid, block, 0, stream, q, rows, ld_q, s, used, qT, row_tiles,
-                       col_tiles);
+    nt ? requantize<Pow2Scale, true>(q, rows, ld_q, s, used, qT, g, stream)
+       : requantize<Pow2Scale, false>(q, rows, ld_q, s, used, qT, g, stream);
   return hipGetLastError();
 }
 

@@ -852,14 +852,24 @@ __global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a,
 }
 
 // Every expert's Wgrad, its reduction over its own segment alone: a tile a
-// workgroup, as the segments differ in length and the hardware's own order evens
-// that out.
+// workgroup.  The segments differ in length.  So that no XCD gets the long ones
+// and the last tiles to start are short, the experts come in the order of their
+// loads, and their tiles in runs of WG_RUN (an XCD's 32 CUs share the panels of one
+// run in L2), dealt to the XCDs back and forth.
+constexpr int WG_RUN = 32;
+
 __global__ __launch_bounds__(THREADS) void grouped_mx_wgrad_kernel(GroupedArgs a, int64_t tiles_m, int64_t tiles_n) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  const int64_t t = xcd_remap(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n, e = t / tiles;
+  __shared__ GroupedOrder order;
+  const uint32_t xcd = blockIdx.x % 8, in = blockIdx.x / 8, turn = in / WG_RUN;
+  const int64_t t = ((int64_t)turn * 8 + (turn & 1 ? 7 - xcd : xcd)) * WG_RUN + in % WG_RUN;
+  const int64_t tiles = tiles_m * tiles_n, at = t / tiles;
+  if (at >= a.E) return;
+  static_assert(THREADS >= kGroupedOrderE, "a thread per expert");
+  const int64_t e = a.E <= kGroupedOrderE ? expert_by_load(order, a.offsets, (int)a.E, a.g.R, (int)at) : at;
   const Segment s = segment_of(a.offsets, e, a.g.R);
   int64_t i0, j0;
-  tile_origin(t - e * tiles, tiles_m, tiles_n, i0, j0);
+  tile_origin(t - at * tiles, tiles_m, tiles_n, i0, j0);
   const Dst d{element(a.g.out, e * a.out_stride, a.g.out_f32), a.g.J, a.g.I, a.g.J, a.g.out_f32, a.g.accumulate};
   if (s.length == 0) {
     zero_tile(d, i0, j0);
@@ -933,11 +943,12 @@ hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream) {
 hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream) {
   if (a.g.bmode == BScale::Block)
     return a.g.bt ? launch_grouped_rows_mx<true>(a, stream) : launch_grouped_rows_mx<false>(a, stream);
-  const int64_t tiles_m = (a.g.I + BM - 1) / BM, tiles_n = (a.g.J + BN - 1) / BN, total = a.E * tiles_m * tiles_n;
+  const int64_t tiles_m = (a.g.I + BM - 1) / BM, tiles_n = (a.g.J + BN - 1) / BN;
+  const int64_t turns = (a.E * tiles_m * tiles_n + 8 * WG_RUN - 1) / (8 * WG_RUN);
   static std::atomic<uint64_t> attr_set{0};
   if (hipError_t e = set_lds_attr(&grouped_mx_wgrad_kernel, &attr_set)) return e;
-  hipLaunchKernelGGL(grouped_mx_wgrad_kernel, dim3((uint32_t)total), dim3(THREADS), LDS_BYTES, stream, a, tiles_m,
-                     tiles_n);
+  hipLaunchKernelGGL(grouped_mx_wgrad_kernel, dim3((uint32_t)(turns * 8 * WG_RUN)), dim3(THREADS), LDS_BYTES, stream, a,
+                     tiles_m, tiles_n);
   return hipGetLastError();
 }
 

@@ -24,56 +24,64 @@ __device__ __forceinline__ uint32_t scaled2(uint32_t v, float w) {
   return bf16x2_rne(bf16_lo(v) * w, bf16_hi(v) * w);
 }
 
-// Eight values of sorted row r, from column c on: zeros where the row has no
-// choice of its own.
-template <bool W>
-__device__ __forceinline__ u32x4 gathered(const GatherArgs& a, int32_t src, int64_t n, int64_t c) {
-  if (src < 0 || src >= n) return u32x4{0, 0, 0, 0};
-  u32x4 v = *reinterpret_cast<const u32x4*>(a.x + (int64_t)((uint32_t)src / (uint32_t)a.k) * a.ld_x + c);
-  if constexpr (W) {
-    const float w = a.weights[src];
-    v = u32x4{scaled2(v.x, w), scaled2(v.y, w), scaled2(v.z, w), scaled2(v.w, w)};
-  }
-  return v;
-}
-
 // ---------------------------------------------------------------------------
-// Row groups only: 16 lanes to a group, four rows' groups a wave and step.
+// Row groups only.  A wave takes kRowCols columns of a run of rows: everything
+// about a row (its source, its addresses, its weight) is the same for the whole
+// wave and costs no vector instructions, of which the quantizing alone takes 35 a
+// KiB -- with a row per 16 lanes instead the kernel was bound by them (16384 tokens
+// to 8 experts each, 2048 wide: 126 us).  A row's source has to be there before
+// its values can be loaded, so the run's sources come first, in one load, and the
+// next row's values are on the way while one is quantized.
 // ---------------------------------------------------------------------------
-constexpr int kRowUnroll = 4;
-constexpr int kGroupsPerWave = 4 * kRowUnroll;
+constexpr int kRowSteps = 4, kRowCols = kRowSteps * 512;
+constexpr int kMaxRun = 16;
 
-template <class S, bool W>
-__global__ __launch_bounds__(kThreads) void gather_rows_kernel(GatherArgs a) {
-  const uint32_t lane = threadIdx.x & 63, sub = lane >> 4, l16 = lane & 15;
-  const uint32_t G = (uint32_t)(a.H / 128);
-  const uint32_t rows = (uint32_t)used_tiles(a.used, a.R) * 128, total = rows * G;
-  const uint32_t g0 = (blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)) * kGroupsPerWave;
-  if (g0 >= total) return;
-  const int64_t n = a.T * a.k;
-  u32x4 v[kRowUnroll];
-  uint32_t row[kRowUnroll], grp[kRowUnroll];
-  int32_t src[kRowUnroll];
+template <class S, bool W, bool NT>
+__global__ __launch_bounds__(kThreads) void gather_rows_kernel(GatherArgs a, uint32_t run, uint32_t parts) {
+  const uint32_t lane = threadIdx.x & 63, l16 = lane & 15;
+  const uint32_t item = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t part = item % parts;
+  const int64_t r0 = (int64_t)(item / parts) * run, rows = (int64_t)used_tiles(a.used, a.R) * 128;
+  if (r0 >= rows) return;
+  const int n_rows = (int)(rows - r0 < run ? rows - r0 : run);
+  const int64_t n = a.T * a.k, G = a.H / 128;
+  const int32_t c0 = (int32_t)(part * kRowCols + lane * 8);  // the lane's first column
+  // lane i: the i-th row's source and weight
+  int32_t src = (int)lane < n_rows ? a.source[r0 + lane] : -1;
+  if (src >= n) src = -1;
+  float weight = 1.0f;
+  if constexpr (W) weight = src >= 0 ? a.weights[src] : 0.0f;
+  const auto load = [&](int i, u32x4 (&v)[kRowSteps]) {
+    const int32_t s = __builtin_amdgcn_readlane(src, i);
+    if (s < 0) {
 #pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u) {
-    const uint32_t g = g0 + u * 4 + sub, gg = g < total ? g : 0;
-    row[u] = gg / G;
-    grp[u] = gg - row[u] * G;
-    src[u] = a.source[row[u]];
-  }
+      for (int u = 0; u < kRowSteps; ++u) v[u] = u32x4{0, 0, 0, 0};
+      return;
+    }
+    const uint16_t* row = a.x + (int64_t)((uint32_t)s / (uint32_t)a.k) * a.ld_x;
 #pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u) v[u] = gathered<W>(a, src[u], n, grp[u] * 128 + l16 * 8);
+    for (int u = 0; u < kRowSteps; ++u)
+      v[u] = c0 + u * 512 < a.H ? *reinterpret_cast<const u32x4*>(row + c0 + u * 512) : u32x4{0, 0, 0, 0};
+  };
+  u32x4 v[kRowSteps], w[kRowSteps];
+  load(0, v);
+  for (int i = 0; i < n_rows; ++i) {
+    if (i + 1 < n_rows) load(i + 1, w);
+    const float wt = W ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), i)) : 1.0f;
+    uint8_t* const q = a.q.q + (r0 + i) * a.q.ld;
+    float* const s = a.q.s + (r0 + i) * G;
 #pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u) {
-    uint32_t m = pk_max_u16(pk_max_u16(abs2(v[u].x), abs2(v[u].y)), pk_max_u16(abs2(v[u].z), abs2(v[u].w)));
-    m = row16_max(max(m & 0xFFFFu, m >> 16));
-    const S sc(m);
-    uint2 o;
-    o.x = quant4(v[u].x, v[u].y, sc);
-    o.y = quant4(v[u].z, v[u].w, sc);
-    if (g0 + u * 4 + sub < total) {
-      *reinterpret_cast<uint2*>(a.q.q + (int64_t)row[u] * a.q.ld + grp[u] * 128 + l16 * 8) = o;
-      if (l16 == 0) a.q.s[(int64_t)row[u] * G + grp[u]] = sc.s;
+    for (int u = 0; u < kRowSteps; ++u) {
+      u32x4 x = v[u];
+      if constexpr (W) x = u32x4{scaled2(x.x, wt), scaled2(x.y, wt), scaled2(x.z, wt), scaled2(x.w, wt)};
+      uint32_t m = pk_max_u16(pk_max_u16(abs2(x.x), abs2(x.y)), pk_max_u16(abs2(x.z), abs2(x.w)));
+      m = row16_max(max(m & 0xFFFFu, m >> 16));
+      const S sc(m);
+      if (c0 + u * 512 < a.H) {
+        store_codes<NT>(q + c0 + u * 512, tile_u32x2{quant4(x.x, x.y, sc), quant4(x.z, x.w, sc)});
+        if (l16 == 0) s[(c0 + u * 512) >> 7] = sc.s;
+      }
+      v[u] = w[u];
     }
   }
 }
@@ -81,23 +89,39 @@ __global__ __launch_bounds__(kThreads) void gather_rows_kernel(GatherArgs a) {
 // ---------------------------------------------------------------------------
 // Both orientations: a 128 x 128 tile a workgroup, as the one-pass quantizer.
 // ---------------------------------------------------------------------------
-template <class S, bool W>
-__global__ __launch_bounds__(kTileThreads) void gather_both_kernel(GatherArgs a, uint32_t row_tiles,
-                                                                   uint32_t col_tiles) {
+// Eight values of the sorted row of choice src, from column c on: zeros where it
+// is none.  A choice's token is its number over k, by the multiplier 2^32 / k
+// rounded up, exact for choices below 2^28 and k up to 16.
+template <bool W>
+__device__ __forceinline__ u32x4 gathered(const GatherArgs& a, int32_t src, int64_t n, uint32_t per_k, int64_t c) {
+  if (src < 0 || src >= n) return u32x4{0, 0, 0, 0};
+  const uint32_t t = a.k > 1 ? __umulhi((uint32_t)src, per_k) : (uint32_t)src;
+  u32x4 v = *reinterpret_cast<const u32x4*>(a.x + (int64_t)t * a.ld_x + c);
+  if constexpr (W) {
+    const float w = a.weights[src];
+    v = u32x4{scaled2(v.x, w), scaled2(v.y, w), scaled2(v.z, w), scaled2(v.w, w)};
+  }
+  return v;
+}
+
+template <class S, bool W, bool NT>
+__global__ __launch_bounds__(kTileThreads) void gather_both_kernel(GatherArgs a, TileGrid grid) {
   __shared__ TileLds lds;
+  const uint32_t row_tiles = grid.row_tiles, col_tiles = grid.col_tiles;
   uint32_t rt, ct;
-  tile_of(blockIdx.x, col_tiles, false, rt, ct);
-  if (rt >= used_tiles(a.used, a.R)) return;
+  tile_of(blockIdx.x, col_tiles, grid.blocked, rt, ct);
+  if (ct >= col_tiles || rt >= used_tiles(a.used, a.R)) return;
   const uint32_t rb = threadIdx.x >> 4, cb = threadIdx.x & 15;
   const int64_t m0 = (int64_t)rt * 128, c0 = (int64_t)ct * 128, n = a.T * a.k;
+  const uint32_t per_k = (uint32_t)(((uint64_t(1) << 32) + a.k - 1) / (uint32_t)a.k);
   int32_t src[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) src[i] = a.source[m0 + rb * 8 + i];
   u32x4 v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = gathered<W>(a, src[i], n, c0 + cb * 8);
-  tile_row_groups<S>(v, a.q.q + m0 * a.q.ld + c0 + cb * 8, a.q.ld, a.q.s + m0 * col_tiles + ct, col_tiles, rb, cb);
-  tile_col_groups<S>(v, lds, a.qT.q + c0 * a.qT.ld + m0, a.qT.ld, a.qT.s + c0 * row_tiles + rt, row_tiles, rb, cb);
+  for (int i = 0; i < 8; ++i) v[i] = gathered<W>(a, src[i], n, per_k, c0 + cb * 8);
+  tile_row_groups<S, NT>(v, a.q.q + m0 * a.q.ld + c0 + cb * 8, a.q.ld, a.q.s + m0 * col_tiles + ct, col_tiles, rb, cb);
+  tile_col_groups<S, NT>(v, lds, a.qT.q + c0 * a.qT.ld + m0, a.qT.ld, a.qT.s + c0 * row_tiles + rt, row_tiles, rb, cb);
 }
 
 // ---------------------------------------------------------------------------
@@ -155,20 +179,41 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(int64_t T, int64_t H,
   }
 }
 
-// A workgroup takes a token: its waves share the columns, 512 at a time, and
-// their sums meet in LDS, in wave order.  Each of the k sums is a lane's, then
-// the wave's, then the workgroup's, in an order that H alone decides.
+// The wave's sums of eight values: lane i gets the i-th (as does every lane whose
+// number ends like i's).  A lane passes on the half of its sums that belongs to the
+// other side of each exchange: 10 exchanges instead of 48.
+static_assert(kBatch == 8, "three halvings");
+__device__ __forceinline__ float sums8(const float (&v)[kBatch], uint32_t lane) {
+  float a[4], b[2];
+  const bool b4 = lane & 4, b2 = lane & 2, b1 = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = (b4 ? v[i + 4] : v[i]) + __shfl_xor(b4 ? v[i] : v[i + 4], 4, 64);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) b[i] = (b2 ? a[i + 2] : a[i]) + __shfl_xor(b2 ? a[i] : a[i + 2], 2, 64);
+  float s = (b1 ? b[1] : b[0]) + __shfl_xor(b1 ? b[0] : b[1], 1, 64);
+  s += __shfl_xor(s, 8, 64);
+  s += __shfl_xor(s, 16, 64);
+  return s + __shfl_xor(s, 32, 64);
+}
+
+// WAVES waves share a token's columns, 512 at a time, and their sums meet in LDS,
+// in wave order (one wave a token where there are tokens enough to fill the GPU:
+// no barrier, and nothing waits for the slowest of four).  Each of the k sums is a
+// lane's, then the wave's, then the token's, in an order that H and WAVES decide.
 constexpr int kMaxK = 16;
 
-__global__ __launch_bounds__(kThreads) void dweights_kernel(int64_t H, int64_t R, int k,
+template <int WAVES>
+__global__ __launch_bounds__(kThreads) void dweights_kernel(int64_t T, int64_t H, int64_t R, int k,
                                                             const uint16_t* __restrict__ dy, int64_t ld_dy,
                                                             const uint16_t* __restrict__ z, int64_t ld_z,
                                                             const int32_t* __restrict__ rows,
                                                             float* __restrict__ dweights) {
-  __shared__ float part[kThreads / 64][kMaxK];
+  __shared__ float part[WAVES][kMaxK];
   const uint32_t lane = threadIdx.x & 63;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = blockIdx.x;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WAVES;
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / 64 / WAVES) +
+                    __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / WAVES;
+  if (t >= T) return;  // one wave a token: nobody waits for it
   for (int i0 = 0; i0 < k; i0 += kBatch) {
     float acc[kBatch] = {};
     int32_t r[kBatch];
@@ -177,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void dweights_kernel(int64_t H, int64_t R
       r[i] = i0 + i < k ? rows[t * k + i0 + i] : -1;
       if (r[i] >= R) r[i] = -1;
     }
-    for (int64_t c = wave * 512 + lane * 8; c < H; c += (kThreads / 64) * 512) {
+    for (int64_t c = wave * 512 + lane * 8; c < H; c += WAVES * 512) {
       const u32x4 d = *reinterpret_cast<const u32x4*>(dy + t * ld_dy + c);
       u32x4 v[kBatch];
 #pragma unroll
@@ -193,33 +238,43 @@ __global__ __launch_bounds__(kThreads) void dweights_kernel(int64_t H, int64_t R
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) acc[i] += __shfl_xor(acc[i], d, 64);
-      if (lane == 0 && i0 + i < k) part[wave][i0 + i] = acc[i];
+    const float mine = sums8(acc, lane);
+    if ((int)lane < kBatch && i0 + (int)lane < k) {
+      if constexpr (WAVES == 1) dweights[t * k + i0 + lane] = mine;
+      else part[wave][i0 + lane] = mine;
     }
   }
-  __syncthreads();
-  if (threadIdx.x < (uint32_t)k) {
-    float sum = 0.0f;
+  if constexpr (WAVES > 1) {
+    static_assert(WAVES * 64 == kThreads, "a workgroup a token");
+    __syncthreads();
+    if (threadIdx.x < (uint32_t)k) {
+      float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) sum += part[w][threadIdx.x];
-    dweights[t * k + threadIdx.x] = sum;
+      for (int w = 0; w < WAVES; ++w) sum += part[w][threadIdx.x];
+      dweights[t * k + threadIdx.x] = sum;
+    }
   }
+}
+
+template <class S, bool W, bool NT>
+hipError_t gather_as(const GatherArgs& a, hipStream_t stream) {
+  if (a.qT.q) {
+    const TileGrid g = tile_grid(a.R, a.H);
+    hipLaunchKernelGGL((gather_both_kernel<S, W, NT>), dim3(g.workgroups), dim3(kTileThreads), 0, stream, a, g);
+  } else {
+    // as many rows a wave as leave 8192 waves, which fill the GPU
+    const int64_t parts = (a.H + kRowCols - 1) / kRowCols, most = a.R * parts / 8192;
+    const int64_t run = most < 1 ? 1 : most < kMaxRun ? most : kMaxRun;
+    const int64_t waves = (a.R + run - 1) / run * parts, per = kThreads / 64;
+    hipLaunchKernelGGL((gather_rows_kernel<S, W, NT>), dim3((uint32_t)((waves + per - 1) / per)), dim3(kThreads), 0,
+                       stream, a, (uint32_t)run, (uint32_t)parts);
+  }
+  return hipGetLastError();
 }
 
 template <class S, bool W>
 hipError_t gather(const GatherArgs& a, hipStream_t stream) {
-  const uint32_t row_tiles = (uint32_t)(a.R / 128), col_tiles = (uint32_t)(a.H / 128);
-  if (a.qT.q) {
-    hipLaunchKernelGGL((gather_both_kernel<S, W>), dim3(row_tiles * col_tiles), dim3(kTileThreads), 0, stream, a,
-                       row_tiles, col_tiles);
-  } else {
-    const uint32_t groups = (uint32_t)a.R * col_tiles, per = kGroupsPerWave * (kThreads / 64);
-    hipLaunchKernelGGL((gather_rows_kernel<S, W>), dim3((groups + per - 1) / per), dim3(kThreads), 0, stream, a);
-  }
-  return hipGetLastError();
+  return a.R * a.H * (a.qT.q ? 2 : 1) > kStoreNt ? gather_as<S, W, true>(a, stream) : gather_as<S, W, false>(a, stream);
 }
 
 }  // namespace
@@ -241,8 +296,12 @@ hipError_t launch_moe_combine(int64_t T, int64_t H, int64_t R, int k, const uint
 hipError_t launch_moe_combine_dweights(int64_t T, int64_t H, int64_t R, int k, const uint16_t* dy, int64_t ld_dy,
                                        const uint16_t* z, int64_t ld_z, const int32_t* rows, float* dweights,
                                        hipStream_t stream) {
-  hipLaunchKernelGGL(dweights_kernel, dim3((uint32_t)T), dim3(kThreads), 0, stream, H, R, k, dy, ld_dy, z, ld_z, rows,
-                     dweights);
+  if (T >= 4096)
+    hipLaunchKernelGGL(dweights_kernel<1>, dim3((uint32_t)((T + 3) / 4)), dim3(kThreads), 0, stream, T, H, R, k, dy,
+                       ld_dy, z, ld_z, rows, dweights);
+  else
+    hipLaunchKernelGGL(dweights_kernel<4>, dim3((uint32_t)T), dim3(kThreads), 0, stream, T, H, R, k, dy, ld_dy, z, ld_z,
+                       rows, dweights);
   return hipGetLastError();
 }
 
