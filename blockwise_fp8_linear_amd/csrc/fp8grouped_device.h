@@ -1,6 +1,8 @@
 // Which tile of which expert: the map that the grouped GEMM kernels (gemm.hip,
 // gemm_mx.hip) make for themselves from the segments' offsets, so that nothing
-// about the experts' loads has to be known on the host.
+// about the experts' loads has to be known on the host.  It stands in front of
+// every workgroup's first load, so it is one round of loads, one scan in 32 bits
+// and a search in LDS.
 #pragma once
 
 #include "fp8blk_device.h"
@@ -9,70 +11,94 @@
 namespace fp8blk {
 
 constexpr int kGroupedMaxE = 1024;
+// Rows of a grouped product: below it an expert has at most 2^21 row tiles, and
+// 1024 of them, whatever the offsets hold, fewer than 2^32.
+constexpr int64_t kGroupedMaxRows = int64_t(1) << 29;
 
-// starts[e]: the first tile of expert e's, starts[E] how many there are.
-struct GroupedLds {
-  int64_t starts[kGroupedMaxE + 1];
-  int64_t wave[16];
-};
+// An offset as a whole multiple of 128 inside [0, rows], whatever it holds.
+__device__ __forceinline__ int32_t segment_edge(int32_t offset, int32_t rows) {
+  return (offset < 0 ? 0 : offset < rows ? offset : rows) & ~127;
+}
 
-// Segment e's first row and length: whole 128s inside [0, rows], whatever the
-// offsets hold.
 struct Segment {
-  int64_t first, length;
+  int32_t first, length;
 };
-__device__ __forceinline__ int64_t segment_edge(const int32_t* __restrict__ offsets, int64_t e, int64_t rows) {
-  const int64_t o = offsets[e];
-  return (o < 0 ? 0 : o < rows ? o : rows) & ~int64_t(127);
-}
-__device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ offsets, int64_t e, int64_t rows) {
-  const int64_t lo = segment_edge(offsets, e, rows), hi = segment_edge(offsets, e + 1, rows);
-  return {lo, hi > lo ? hi - lo : 0};
+__device__ __forceinline__ Segment segment_between(int32_t lo, int32_t hi) { return {lo, hi > lo ? hi - lo : 0}; }
+__device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ offsets, int e, int32_t rows) {
+  return segment_between(segment_edge(offsets[e], rows), segment_edge(offsets[e + 1], rows));
 }
 
-// Fills lds.starts for tiles of tile_rows rows x tiles_n columns.  Every thread
-// of a workgroup of THREADS calls it; ends with a barrier.
-template <int THREADS>
-__device__ __forceinline__ void grouped_starts(GroupedLds& lds, const int32_t* __restrict__ offsets, int64_t E,
-                                               int64_t rows, int64_t tile_rows, int64_t tiles_n) {
+// starts[e]: the first row tile of expert e's, starts[E] how many there are.
+struct GroupedMap {
+  uint32_t starts[kGroupedMaxE + 1];
+  int32_t edges[kGroupedMaxE + 1];
+  uint32_t wave[16];
+};
+
+// Fills the map for tiles of TILE rows.  Every thread of a workgroup of THREADS
+// calls it; ends with a barrier.
+template <int THREADS, int TILE>
+__device__ __forceinline__ void grouped_map(GroupedMap& lds, const int32_t* __restrict__ offsets, int E, int32_t rows) {
   constexpr int PER = kGroupedMaxE / THREADS;
   const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  int64_t n[PER], sum = 0;
+  int32_t edge[PER + 1];
+#pragma unroll
+  for (int i = 0; i <= PER; ++i) {
+    const int e = (int)t * PER + i;
+    edge[i] = e <= E ? segment_edge(offsets[e], rows) : 0;
+  }
+  uint32_t n[PER], sum = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int64_t e = (int64_t)t * PER + i;
+    const int e = (int)t * PER + i;
     n[i] = sum;
-    if (e < E) sum += (segment_of(offsets, e, rows).length + tile_rows - 1) / tile_rows * tiles_n;
+    if (e < E) sum += (uint32_t)(segment_between(edge[i], edge[i + 1]).length + TILE - 1) / TILE;
+    if (e <= E) lds.edges[e] = edge[i];
   }
-  int64_t upto = sum;
+  if (t == THREADS - 1 && E == kGroupedMaxE) lds.edges[E] = edge[PER];
+  uint32_t upto = sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(upto, d, 64);
+    const uint32_t o = (uint32_t)__shfl_up((int)upto, d, 64);
     if ((int)lane >= d) upto += o;
   }
   if (lane == 63) lds.wave[wave] = upto;
   __syncthreads();
-  int64_t before = upto - sum;
-  for (uint32_t w = 0; w < wave; ++w) before += lds.wave[w];
+  uint32_t before = upto - sum;
+#pragma unroll
+  for (uint32_t w = 0; w + 1 < THREADS / 64; ++w) before += w < wave ? lds.wave[w] : 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int64_t e = (int64_t)t * PER + i;
+    const int e = (int)t * PER + i;
     if (e <= E) lds.starts[e] = before + n[i];
   }
   if (t == THREADS - 1 && E == kGroupedMaxE) lds.starts[E] = before + sum;
   __syncthreads();
 }
 
-// The expert of a tile below starts[E]: the last one that starts at or before it
-// and has any.
-__device__ __forceinline__ int64_t expert_of_tile(const GroupedLds& lds, int64_t E, int64_t tile) {
-  int64_t lo = 0, hi = E;
+// The expert of a row tile below starts[E]: the last one that starts at or before
+// it (so one that has any).
+__device__ __forceinline__ int expert_of_tile(const GroupedMap& lds, int E, uint32_t tile) {
+  int lo = 0, hi = E;
   while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
+    const int mid = (lo + hi) / 2;
     if (lds.starts[mid] <= tile) lo = mid;
     else hi = mid;
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Tile `in` of a segment's (or an expert's) tiles_m x tiles_n -> its row and
+// column of tiles: down a group of GM tile rows before moving right, as the dense
+// kernels go, so that tiles in flight together share operand panels in L2.
+struct TileAt {
+  uint32_t m, n;
+};
+template <int GM>
+__device__ __forceinline__ TileAt tile_at(uint32_t in, uint32_t tiles_m, uint32_t tiles_n) {
+  const uint32_t group = in / (GM * tiles_n), first = group * GM;
+  const uint32_t size = tiles_m - first < GM ? tiles_m - first : GM, rest = in - first * tiles_n, n = rest / size;
+  return {first + (rest - n * size), n};
 }
 
 // The expert whose segment is the at-th longest, equal ones by index: every thread
@@ -80,28 +106,33 @@ __device__ __forceinline__ int64_t expert_of_tile(const GroupedLds& lds, int64_t
 // before its own, four a step, so it is for a few hundred at most.
 constexpr int kGroupedOrderE = 256;
 struct GroupedOrder {
-  __attribute__((aligned(16))) int32_t blocks[kGroupedOrderE];  // of each expert; behind the last one -1
+  __attribute__((aligned(16))) int32_t length[kGroupedOrderE];  // of each expert's segment; behind the last one -1
   int found;
+  Segment segment;
 };
 __device__ __forceinline__ int expert_by_load(GroupedOrder& lds, const int32_t* __restrict__ offsets, int E,
-                                              int64_t rows, int at) {
+                                              int32_t rows, int at, Segment& s) {
   typedef int v4i __attribute__((ext_vector_type(4)));
   const int e = threadIdx.x;
-  const int mine = e < E ? (int)(segment_of(offsets, e, rows).length / 128) : -1;
-  if (e < kGroupedOrderE) lds.blocks[e] = mine;
+  const Segment mine = e < E ? segment_of(offsets, e, rows) : Segment{0, -1};
+  if (e < kGroupedOrderE) lds.length[e] = mine.length;
   __syncthreads();
   if (e < E) {
     int before = 0;
 #pragma unroll 8
     for (int o = 0; o < E; o += 4) {
-      const v4i b = *reinterpret_cast<const v4i*>(lds.blocks + o);
+      const v4i l = *reinterpret_cast<const v4i*>(lds.length + o);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) before += b[i] > mine || (b[i] == mine && o + i < e) ? 1 : 0;
+      for (int i = 0; i < 4; ++i) before += l[i] > mine.length || (l[i] == mine.length && o + i < e) ? 1 : 0;
     }
-    if (before == at) lds.found = e;
+    if (before == at) {
+      lds.found = e;
+      lds.segment = mine;
+    }
   }
   __syncthreads();
-  return lds.found;
+  s = Segment{__builtin_amdgcn_readfirstlane(lds.segment.first), __builtin_amdgcn_readfirstlane(lds.segment.length)};
+  return __builtin_amdgcn_readfirstlane(lds.found);
 }
 
 // Output element i of a matrix of fp32 or bf16.
@@ -110,7 +141,7 @@ __device__ __forceinline__ void* element(void* out, int64_t i, bool f32) {
 }
 
 // The contraction of one expert's segment: rows (Fprop, Dgrad).
-__device__ __forceinline__ GemmArgs expert_rows(const GroupedArgs& a, int64_t e, Segment s) {
+__device__ __forceinline__ GemmArgs expert_rows(const GroupedArgs& a, int e, Segment s) {
   GemmArgs g = a.g;
   g.a += s.first * g.R;
   g.sa += s.first * (g.R / 128);

@@ -75,7 +75,9 @@ struct GroupedArgs {
 hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);   // Fprop, Dgrad
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);
 // All three on the 256x256 block-scaled-MFMA kernels (gemm_mx.hip): Fprop and
-// Dgrad for the shapes that gemm_mx_eligible(a.g) takes, Wgrad up to 2^22 rows.
+// Dgrad up to kMxMaxKb 128-blocks of reduction and 2^22 columns, Wgrad up to 2^22
+// rows.
 hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream);
+int64_t grouped_mx_tiles(const GroupedArgs& a);  // tiles of Fprop or Dgrad, whatever the segments
 
 }  // namespace fp8blk

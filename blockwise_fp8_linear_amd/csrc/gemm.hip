@@ -56,9 +56,11 @@ constexpr int kChunk = 32;  // reduction blocks whose scales sit in LDS at once
 // BT_: B stored [R][J] (Dgrad from the weight codes as quantized): the B
 // tile is staged as 128 reduction rows of BN bytes and its fragments come
 // from LDS transpose reads.
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool PROMOTE_, bool BROW_, bool BT_ = false>
+// STAGES_: blocks in LDS at once; beyond two, STAGES_ - 1 are on the way, for tiles
+// that are small beside the time a load takes.
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool PROMOTE_, bool BROW_, bool BT_ = false, int STAGES_ = 2>
 struct Cfg {
-  static constexpr int BM = BM_, BN = BN_;
+  static constexpr int BM = BM_, BN = BN_, STAGES = STAGES_;
   static constexpr bool BT = BT_;
   static_assert(!BT_ || (!BROW_ && BN_ == 128), "transposed B: Dgrad's weight-block layout, 128-byte rows");
   static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
@@ -72,7 +74,7 @@ struct Cfg {
   using SType = typename std::conditional<PROMOTE_, float, uint8_t>::type;
   static constexpr int SA_BYTES = kChunk * BM * (int)sizeof(SType);
   static constexpr int SB_BYTES = (BROW ? kChunk * BN : kChunk * (BN / 128 > 0 ? BN / 128 : 1)) * (int)sizeof(SType);
-  static constexpr int LDS = 2 * STAGE + SA_BYTES + ((SB_BYTES + 15) / 16) * 16;
+  static constexpr int LDS = STAGES * STAGE + SA_BYTES + ((SB_BYTES + 15) / 16) * 16;
   static_assert(A_BYTES % (1024 * (THREADS / 64)) == 0 && B_BYTES % (1024 * (THREADS / 64)) == 0,
                 "whole KiB of direct loads per wave");
   static_assert(WN <= 128 && 128 % WN == 0, "a wave's columns must sit inside one 128-block");
@@ -160,8 +162,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
                                           int64_t kb_end, v4f (&acc)[C::TM][C::TN]) {
   uint8_t* const tiles = lds;
   typedef typename C::SType ST;
-  ST* const sa_lds = reinterpret_cast<ST*>(lds + 2 * C::STAGE);
-  ST* const sb_lds = reinterpret_cast<ST*>(lds + 2 * C::STAGE + C::SA_BYTES);
+  ST* const sa_lds = reinterpret_cast<ST*>(lds + C::STAGES * C::STAGE);
+  ST* const sb_lds = reinterpret_cast<ST*>(lds + C::STAGES * C::STAGE + C::SA_BYTES);
 
   const uint32_t tid = threadIdx.x;
   const uint32_t lane = tid & 63;
@@ -261,17 +263,28 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
 
   const uint32_t wm0 = wm * C::WM, wn0 = wn * C::WN;
 
+  constexpr int PER_BLOCK = A_DMA + B_DMA;
+  // block kb -> its stage; one past the end reloads the last into a stage that is
+  // not read again (which keeps the count of loads on the way the same)
+  const auto dma_ahead = [&](int64_t kb) {
+    dma_block(kb < kb_end ? kb : kb_end - 1, (int)((kb - kb_begin) % C::STAGES));
+  };
   if (kb_begin < kb_end) {
     dma_block(kb_begin, 0);
+    if constexpr (C::STAGES > 2) {
+#pragma unroll
+      for (int s = 1; s < C::STAGES - 1; ++s) dma_ahead(kb_begin + s);
+    }
     load_scales(kb_begin, (kb_end - kb_begin) < kChunk ? (kb_end - kb_begin) : kChunk);
-    wait_vmcnt<0>();
+    wait_vmcnt<C::STAGES == 2 ? 0 : (C::STAGES - 2) * PER_BLOCK>();
     __syncthreads();
   }
   for (int64_t kb = kb_begin; kb < kb_end; ++kb) {
-    const int cur = (int)((kb - kb_begin) & 1);
+    const int cur = (int)((kb - kb_begin) % C::STAGES);
     const bool more = kb + 1 < kb_end;
-    // the other stage was last read in the previous block, before its barrier
-    if (more) dma_block(kb + 1, cur ^ 1);
+    // the stage that is loaded was last read in the previous block, before its barrier
+    if constexpr (C::STAGES > 2) dma_ahead(kb + C::STAGES - 1);
+    else if (more) dma_block(kb + 1, cur ^ 1);
 
     const uint8_t* ta = tiles + cur * C::STAGE;
     const uint8_t* tb = ta + C::A_BYTES;
@@ -401,8 +414,14 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
       const int64_t rest = kb_end - (kb + 1);
       load_scales(kb + 1, rest < kChunk ? rest : kChunk);
     }
-    wait_vmcnt<0>();  // this wave's loads of block kb+1 have landed
+    // this wave's loads of block kb+1 have landed
+    if constexpr (C::STAGES > 2) wait_vmcnt<(C::STAGES - 2) * PER_BLOCK>();
+    else wait_vmcnt<0>();
     __syncthreads();  // ... and every wave's; no wave reads stage cur any more
+  }
+  if constexpr (C::STAGES > 2) {
+    wait_vmcnt<0>();  // those past the end
+    __syncthreads();
   }
 }
 
@@ -558,18 +577,21 @@ __global__ __launch_bounds__(256) void gk_fixup_kernel(GemmArgs g, SkGeom sg, co
 // mixture): a persistent grid takes the tiles of all experts in turn, found by
 // the map that each workgroup makes at its start.
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void grouped_rows_kernel(GroupedArgs a, int64_t tiles_n) {
+__global__ __launch_bounds__(C::THREADS) void grouped_rows_kernel(GroupedArgs a, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ GroupedLds map;
-  grouped_starts<C::THREADS>(map, a.offsets, a.E, a.g.I, C::BM, tiles_n);
-  const int64_t total = map.starts[a.E];
+  __shared__ GroupedMap map;
+  const int E = (int)a.E;
+  grouped_map<C::THREADS, C::BM>(map, a.offsets, E, (int32_t)a.g.I);
+  const uint64_t total = (uint64_t)map.starts[E] * tiles_n;
   v4f acc[C::TM][C::TN];
-  for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
-    const int64_t e = expert_of_tile(map, a.E, t);
-    const Segment s = segment_of(a.offsets, e, a.g.I);
+  for (uint64_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+    // an expert's tiles are tiles_n for each of its row tiles, so its first is starts * tiles_n
+    const int e = expert_of_tile(map, E, (uint32_t)(t / tiles_n));
+    const Segment s = segment_between(map.edges[e], map.edges[e + 1]);
     const GemmArgs g = expert_rows(a, e, s);
-    int64_t i0, j0;
-    gk_tile_origin<C>(t - map.starts[e], (s.length + C::BM - 1) / C::BM, tiles_n, i0, j0);
+    const TileAt at = tile_at<8>((uint32_t)(t - (uint64_t)map.starts[e] * tiles_n),
+                                 (uint32_t)(s.length + C::BM - 1) / C::BM, tiles_n);
+    const int64_t i0 = (int64_t)at.m * C::BM, j0 = (int64_t)at.n * C::BN;
     gemm_tile<C>(g, lds, i0, j0, 0, g.R / 128, acc);
     gk_store<C>(acc, g.out, g.J, g.I, g.J, g.out_f32, g.accumulate, i0, j0);
   }
@@ -578,15 +600,15 @@ __global__ __launch_bounds__(C::THREADS) void grouped_rows_kernel(GroupedArgs a,
 // Every expert's Wgrad: the reduction runs over its segment alone.  A segment
 // without rows leaves zeros.
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void grouped_wgrad_kernel(GroupedArgs a, int64_t tiles_m, int64_t tiles_n) {
+__global__ __launch_bounds__(C::THREADS) void grouped_wgrad_kernel(GroupedArgs a, uint32_t tiles_m, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int64_t tiles = tiles_m * tiles_n, total = a.E * tiles;
+  const uint32_t tiles = tiles_m * tiles_n, total = (uint32_t)a.E * tiles;
   v4f acc[C::TM][C::TN];
-  for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
-    const int64_t e = t / tiles;
-    const Segment s = segment_of(a.offsets, e, a.g.R);
-    int64_t i0, j0;
-    gk_tile_origin<C>(t - e * tiles, tiles_m, tiles_n, i0, j0);
+  for (uint32_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+    const uint32_t e = t / tiles;
+    const Segment s = segment_of(a.offsets, (int)e, (int32_t)a.g.R);
+    const TileAt at = tile_at<8>(t - e * tiles, tiles_m, tiles_n);
+    const int64_t i0 = (int64_t)at.m * C::BM, j0 = (int64_t)at.n * C::BN;
     gemm_tile<C>(a.g, lds, i0, j0, s.first / 128, (s.first + s.length) / 128, acc);
     gk_store<C>(acc, element(a.g.out, e * a.out_stride, a.g.out_f32), a.g.J, a.g.I, a.g.J, a.g.out_f32,
                 a.g.accumulate, i0, j0);
@@ -659,7 +681,7 @@ static hipError_t launch_grouped_rows_cfg(const GroupedArgs& a, hipStream_t stre
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_rows_kernel<C>), C::LDS, &attr_set))
     return e;
   hipLaunchKernelGGL(grouped_rows_kernel<C>, dim3((uint32_t)(most < kSkGrid ? most : kSkGrid)), dim3(C::THREADS),
-                     C::LDS, stream, a, tiles_n);
+                     C::LDS, stream, a, (uint32_t)tiles_n);
   return hipGetLastError();
 }
 
@@ -671,13 +693,16 @@ static hipError_t launch_grouped_wgrad_cfg(const GroupedArgs& a, hipStream_t str
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_wgrad_kernel<C>), C::LDS, &attr_set))
     return e;
   hipLaunchKernelGGL(grouped_wgrad_kernel<C>, dim3((uint32_t)(total < kSkGrid ? total : kSkGrid)), dim3(C::THREADS),
-                     C::LDS, stream, a, tiles_m, tiles_n);
+                     C::LDS, stream, a, (uint32_t)tiles_m, (uint32_t)tiles_n);
   return hipGetLastError();
 }
 
 hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
   const bool promote = algo == GemmAlgo::Promote;
-  if (!promote && gemm_mx_eligible(a.g)) return launch_grouped_mx(a, stream);
+  // the weight-block scales of a reduction sit in LDS; per-lane 32-bit offsets of
+  // 128 rows; at most a workgroup a tile, of a launch below 2^32 threads
+  if (!promote && a.g.R <= kMxMaxKb * 128 && a.g.J <= (int64_t(1) << 22) && grouped_mx_tiles(a) < (1 << 24))
+    return launch_grouped_mx(a, stream);
   if (a.g.bt)
     return promote ? launch_grouped_rows_cfg<PromoteBlockBT>(a, stream) : launch_grouped_rows_cfg<ScaledBlockBT>(a, stream);
   return promote ? launch_grouped_rows_cfg<PromoteBlock>(a, stream) : launch_grouped_rows_cfg<ScaledBlock>(a, stream);

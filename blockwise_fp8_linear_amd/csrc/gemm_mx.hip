@@ -55,19 +55,23 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr int BM = (int)kMxTile, BN = (int)kMxTile, BK = 64, THREADS = 256;
 constexpr int WM = 128, WN = 128;          // wave tile
 constexpr int TM = WM / 32, TN = WN / 32;  // 32x32 MFMA tiles per wave
+constexpr int HALF = TM / 2;               // of a tile of 128 rows (the last ones of an expert's segment)
 // The LDS ring holds two "pair slots"; a pair slot holds two consecutive
 // 64-deep stages (one 128-deep scale block) of both tiles as whole 128-byte
 // rows, so every direct load reads whole cache lines.
 constexpr int PK = 2 * BK;                         // bytes of a row in a pair slot
-constexpr int A_SLOT = BM * PK, B_SLOT = BN * PK, SLOT = A_SLOT + B_SLOT;  // 64 KiB
+constexpr int B_SLOT = BN * PK;
+template <int T>  // T: MFMA tiles of a wave down the rows
+struct Slot {
+  static constexpr int ROWS = 64 * T, A = ROWS * PK, BYTES = A + B_SLOT;  // 64 KiB (T = TM)
+  static constexpr int LOADS_A = A / 1024 / (THREADS / 64);               // 1 KiB per wave instruction
+};
 constexpr int SLOTS = 2;
 constexpr int SC_BYTES = 8192;            // one group of raw scales: A rows, then B rows
 constexpr int MAX_KB = (int)kMxMaxKb;     // 128-blocks per segment with weight-block scales (held in LDS)
 constexpr int BS_BYTES = 4 * MAX_KB * 4;  // the 4 waves' weight-block scales of a segment, fp32
-constexpr int LDS_BYTES = SLOTS * SLOT + 2 * SC_BYTES + BS_BYTES;  // 146 KiB
-constexpr int LOADS_A = A_SLOT / 1024 / (THREADS / 64);  // 1 KiB per wave instruction
+constexpr int LDS_BYTES = SLOTS * Slot<TM>::BYTES + 2 * SC_BYTES + BS_BYTES;  // 146 KiB
 constexpr int LOADS_B = B_SLOT / 1024 / (THREADS / 64);
-constexpr int LOADS_PER_PAIR = LOADS_A + LOADS_B;          // per wave
 
 template <int V>
 struct IntC {
@@ -121,11 +125,13 @@ __device__ __forceinline__ void tile_origin(int64_t tile, int64_t tiles_m, int64
 // RAGGED: any 128-blocks, at least one, from any of them on.  Their scales are
 // then not 16-byte aligned and are loaded one by one; the last group of four may
 // hold fewer blocks.
-template <bool BROW, bool BT = false, bool RAGGED = false>
+// TM = HALF: a tile of 128 rows.
+template <bool BROW, bool BT = false, bool RAGGED = false, int TM = fp8blk::TM>
 __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int64_t i0, int64_t j0, int64_t kb_begin,
                                             int64_t nkb_seg, v16f (&acc)[TM][TN]) {
   static_assert(!(BT && BROW), "the transposed-B layout is Dgrad's, with weight-block scales");
-  static_assert(!RAGGED || BROW, "weight-block scales are loaded for whole groups");
+  constexpr int LOADS_A = Slot<TM>::LOADS_A, LOADS_PER_PAIR = LOADS_A + LOADS_B, WM = 32 * TM;
+  constexpr int A_SLOT = Slot<TM>::A, SLOT = Slot<TM>::BYTES;
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t wm = wave >> 1, wn = wave & 1;
@@ -213,7 +219,7 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
       for (int i = 0; i < 4; ++i) {
         const int k = 4 * q + i < npair ? 4 * q + i : npair - 1;
         dma4(baseSA + 4 * k, offSA, buf + i * 1024 + wave * 256);
-        dma4(baseSB + 4 * k, offSB, buf + 4096 + i * 1024 + wave * 256);
+        if constexpr (BROW) dma4(baseSB + 4 * k, offSB, buf + 4096 + i * 1024 + wave * 256);
       }
       return;
     }
@@ -288,29 +294,22 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   };
   auto read_scales = [&](int q, uint32_t* pa, uint32_t* pb) {
     const uint8_t* buf = sc_lds + (q & 1) * SC_BYTES;
-    if constexpr (RAGGED) {
-      const auto four = [](const uint8_t* p) {
-        u32x4 s;
+    const auto four = [](const uint8_t* rows, uint32_t row) {
+      if constexpr (!RAGGED) return pack_e8(*reinterpret_cast<const u32x4*>(rows + row * 16));
+      u32x4 s;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const uint32_t*>(p + i * 1024);
-        return pack_e8(s);
-      };
+      for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const uint32_t*>(rows + i * 1024 + row * 4);
+      return pack_e8(s);
+    };
 #pragma unroll
-      for (int t = 0; t < TM; ++t) pa[t] = four(buf + (wm0 + t * 32 + l32) * 4);
-#pragma unroll
-      for (int t = 0; t < TN; ++t) pb[t] = four(buf + 4096 + (wn0 + t * 32 + l32) * 4);
-      return;
-    }
-#pragma unroll
-    for (int t = 0; t < TM; ++t) pa[t] = pack_e8(*reinterpret_cast<const u32x4*>(buf + (wm0 + t * 32 + l32) * 16));
+    for (int t = 0; t < TM; ++t) pa[t] = four(buf, wm0 + t * 32 + l32);
     if constexpr (BROW) {
 #pragma unroll
-      for (int t = 0; t < TN; ++t)
-        pb[t] = pack_e8(*reinterpret_cast<const u32x4*>(buf + 4096 + (wn0 + t * 32 + l32) * 16));
+      for (int t = 0; t < TN; ++t) pb[t] = four(buf + 4096, wn0 + t * 32 + l32);
     } else {
       // this wave's weight block, blocks 4q..4q+3 of the slice (same
       // address in every lane: a broadcast read)
-      const int qc = q < ngroup ? q : ngroup - 1;
+      const int groups = RAGGED ? (npair + 3) / 4 : ngroup, qc = q < groups ? q : groups - 1;
       const uint32_t e = pack_e8(*reinterpret_cast<const u32x4*>(lds + bs_area + wave * (MAX_KB * 4) + 16 * qc));
 #pragma unroll
       for (int t = 0; t < TN; ++t) pb[t] = e;
@@ -345,7 +344,8 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   // that slot with pair p+1, two direct loads per MFMA pair.  Even stages
   // need no wait and no barrier: stage s+1 is in the same pair.  The
   // sched_barrier fences pin the interleaving.
-  static_assert(TM == 4 && TN == 4 && LOADS_PER_PAIR == 16, "one read + two loads per MFMA pair");
+  static_assert((TM == 4 || TM == 2) && TN == 4 && LOADS_PER_PAIR == 8 + 2 * TM,
+                "of the next stage's fragments one (TM 2: up to two), of its loads two (three) per MFMA pair");
   auto stage_step = [&](int st, auto buf_tag, auto opsel_tag) {
     constexpr int OPSEL = decltype(opsel_tag)::value;
     constexpr int BUF = decltype(buf_tag)::value;  // also the parity of st
@@ -356,19 +356,29 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < 2 * TM; ++p) {
       const int a = p >> 1, b0 = 2 * (p & 1);
       acc[a][b0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[BUF][b0], fa[BUF][a], acc[a][b0], 0, 0, OPSEL,
                                                                    (int)sb_cur[b0], OPSEL, (int)sa_cur[a]);
       acc[a][b0 + 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
           fb[BUF][b0 + 1], fa[BUF][a], acc[a][b0 + 1], 0, 0, OPSEL, (int)sb_cur[b0 + 1], OPSEL, (int)sa_cur[a]);
       // next stage's fragments in the order its MFMAs consume them
-      if (p == 0) fa[NXT][0] = read_frag(st + 1, rowA);
-      else if (p <= 4) fb[NXT][p - 1] = read_frag_b(st + 1, p - 1);
-      else fa[NXT][p - 4] = read_frag(st + 1, rowA + (p - 4) * 32 * PK);
+      if constexpr (TM == 4) {
+        if (p == 0) fa[NXT][0] = read_frag(st + 1, rowA);
+        else if (p <= 4) fb[NXT][p - 1] = read_frag_b(st + 1, p - 1);
+        else fa[NXT][p - 4] = read_frag(st + 1, rowA + (p - 4) * 32 * PK);
+      } else {
+        if (p == 0) fa[NXT][0] = read_frag(st + 1, rowA);
+        if (p < 2) {
+          fb[NXT][2 * p] = read_frag_b(st + 1, 2 * p);
+          fb[NXT][2 * p + 1] = read_frag_b(st + 1, 2 * p + 1);
+        }
+        if (p == 2) fa[NXT][1] = read_frag(st + 1, rowA + 32 * PK);
+      }
       if constexpr (BUF == 1) {
-        issue_one((st + 3) >> 1, 2 * p);
-        issue_one((st + 3) >> 1, 2 * p + 1);
+        constexpr int EACH = LOADS_PER_PAIR / (2 * TM);
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) issue_one((st + 3) >> 1, EACH * p + i);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -427,8 +437,9 @@ struct Dst {
 // wave's 32x32 accumulator tile (a, b) in the MFMA register layout; it is
 // called once per tile, in (a, b) order.  Starts with a barrier, so the LDS
 // ring and any earlier staging are free.
-template <int BATCH, class Src>
+template <int BATCH, int TM, class Src>
 __device__ __forceinline__ void store_tile_from(const Dst& d, uint8_t* lds, int64_t i0, int64_t j0, Src src) {
+  constexpr int WM = 32 * TM;
   // ---- epilogue, staged through LDS so that global stores are whole rows,
   // non-temporal (the output is not read again here; see the file header).
   // src(a, b) lane l, element e holds row i = wm0 + 32a + l%32 and column
@@ -475,7 +486,7 @@ __device__ __forceinline__ void store_tile_from(const Dst& d, uint8_t* lds, int6
       // the first store (a read waited for right before its own store
       // exposes the LDS latency 32 times)
 #pragma unroll 1
-      for (int pb = 0; pb < 32; pb += BATCH) {
+      for (int pb = 0; pb < WM / 4; pb += BATCH) {
         u32x4 v[BATCH];
 #pragma unroll
         for (int s = 0; s < BATCH; ++s) {
@@ -496,7 +507,7 @@ __device__ __forceinline__ void store_tile_from(const Dst& d, uint8_t* lds, int6
     } else {
       // fp32: unit = 16 bytes, row = 512 bytes, two halves of 64 rows
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < TM / 2; ++h) {
 #pragma unroll
         for (int a2 = 0; a2 < 2; ++a2) {
           const int a = 2 * h + a2;
@@ -557,7 +568,7 @@ __device__ __forceinline__ void store_tile_from(const Dst& d, uint8_t* lds, int6
 // Store a tile from registers.  (A local copy: reading the caller's array
 // through the reference while storing to LDS makes the compiler keep it in
 // memory -- hundreds of spilled registers.)
-template <int BATCH>
+template <int BATCH, int TM>
 __device__ __forceinline__ void store_tile(const Dst& d, uint8_t* lds, int64_t i0, int64_t j0,
                                            const v16f (&acc_in)[TM][TN]) {
   v16f acc[TM][TN];
@@ -565,7 +576,7 @@ __device__ __forceinline__ void store_tile(const Dst& d, uint8_t* lds, int64_t i
   for (int a = 0; a < TM; ++a)
 #pragma unroll
     for (int b = 0; b < TN; ++b) acc[a][b] = acc_in[a][b];
-  store_tile_from<BATCH>(d, lds, i0, j0, [&](int a, int b) { return acc[a][b]; });
+  store_tile_from<BATCH, TM>(d, lds, i0, j0, [&](int a, int b) { return acc[a][b]; });
 }
 
 // A tile of zeros; what accumulates stays as it is.
@@ -829,25 +840,36 @@ __global__ __launch_bounds__(256) void bwd_fixup_kernel(GemmArgs gd, GemmArgs gw
 }
 
 // Every expert's product over its own segment of rows (Fprop and Dgrad of a
-// mixture; BT: Dgrad from the weight codes as quantized): a persistent grid takes
-// the tiles of all experts in turn, found by the map that each workgroup makes at
-// its start.
-template <bool BT>
-__global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a, int64_t tiles_n) {
+// mixture; BT: Dgrad from the weight codes as quantized).  Tile t of all experts'
+// is found by the map that each workgroup makes at its start; PERSISTENT: a
+// workgroup takes every gridDim.x-th.  A segment that ends in a block of 128 rows
+// has a tile of 128 there.
+template <bool BT, bool RAGGED, bool PERSISTENT>
+__global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  __shared__ GroupedLds map;
-  grouped_starts<THREADS>(map, a.offsets, a.E, a.g.I, BM, tiles_n);
-  const int64_t total = map.starts[a.E];
-  v16f acc[TM][TN];
-  for (int64_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
-    const int64_t e = expert_of_tile(map, a.E, t);
-    const Segment s = segment_of(a.offsets, e, a.g.I);
+  __shared__ GroupedMap map;
+  const int E = (int)a.E;
+  grouped_map<THREADS, BM>(map, a.offsets, E, (int32_t)a.g.I);
+  const uint32_t total = map.starts[E] * tiles_n;
+  for (uint32_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+    // an expert's tiles are tiles_n for each of its row tiles, so its first is starts * tiles_n
+    const int e = expert_of_tile(map, E, t / tiles_n);
+    const Segment s = segment_between(map.edges[e], map.edges[e + 1]);
     const GemmArgs g = expert_rows(a, e, s);
-    int64_t i0, j0;
-    tile_origin(t - map.starts[e], (s.length + BM - 1) / BM, tiles_n, i0, j0);
-    lds_barrier();  // the previous tile's epilogue is done with LDS
-    mma_segment<false, BT>(g, lds, i0, j0, 0, g.R / 128, acc);
-    store_tile<1>(Dst{g.out, g.J, g.I, g.J, g.out_f32, g.accumulate}, lds, i0, j0, acc);
+    const TileAt at = tile_at<4>(t - map.starts[e] * tiles_n, (uint32_t)(s.length + BM - 1) / BM, tiles_n);
+    const int64_t i0 = (int64_t)at.m * BM, j0 = (int64_t)at.n * BN;
+    const Dst d{g.out, g.J, g.I, g.J, g.out_f32, g.accumulate};
+    if constexpr (PERSISTENT) lds_barrier();  // the previous tile's epilogue is done with LDS
+    if (s.length - i0 > BM / 2) {
+      v16f acc[TM][TN];
+      mma_segment<false, BT, RAGGED>(g, lds, i0, j0, 0, g.R / 128, acc);
+      store_tile<1>(d, lds, i0, j0, acc);
+    } else {
+      v16f acc[HALF][TN];
+      mma_segment<false, BT, RAGGED, HALF>(g, lds, i0, j0, 0, g.R / 128, acc);
+      store_tile<1>(d, lds, i0, j0, acc);
+    }
+    if constexpr (!PERSISTENT) return;
   }
 }
 
@@ -856,20 +878,22 @@ __global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a,
 // and the last tiles to start are short, the experts come in the order of their
 // loads, and their tiles in runs of WG_RUN (an XCD's 32 CUs share the panels of one
 // run in L2), dealt to the XCDs back and forth.
-constexpr int WG_RUN = 32;
+constexpr uint32_t WG_RUN = 32;
 
-__global__ __launch_bounds__(THREADS) void grouped_mx_wgrad_kernel(GroupedArgs a, int64_t tiles_m, int64_t tiles_n) {
+__global__ __launch_bounds__(THREADS) void grouped_mx_wgrad_kernel(GroupedArgs a, uint32_t tiles_m, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   __shared__ GroupedOrder order;
   const uint32_t xcd = blockIdx.x % 8, in = blockIdx.x / 8, turn = in / WG_RUN;
-  const int64_t t = ((int64_t)turn * 8 + (turn & 1 ? 7 - xcd : xcd)) * WG_RUN + in % WG_RUN;
-  const int64_t tiles = tiles_m * tiles_n, at = t / tiles;
-  if (at >= a.E) return;
+  const uint32_t t = (turn * 8 + (turn & 1 ? 7 - xcd : xcd)) * WG_RUN + in % WG_RUN;
+  const uint32_t tiles = tiles_m * tiles_n, nth = t / tiles;
+  if (nth >= a.E) return;
   static_assert(THREADS >= kGroupedOrderE, "a thread per expert");
-  const int64_t e = a.E <= kGroupedOrderE ? expert_by_load(order, a.offsets, (int)a.E, a.g.R, (int)at) : at;
-  const Segment s = segment_of(a.offsets, e, a.g.R);
-  int64_t i0, j0;
-  tile_origin(t - at * tiles, tiles_m, tiles_n, i0, j0);
+  int e = (int)nth;
+  Segment s;
+  if (a.E <= kGroupedOrderE) e = expert_by_load(order, a.offsets, (int)a.E, (int32_t)a.g.R, (int)nth, s);
+  else s = segment_of(a.offsets, e, (int32_t)a.g.R);
+  const TileAt at = tile_at<4>(t - nth * tiles, tiles_m, tiles_n);
+  const int64_t i0 = (int64_t)at.m * BM, j0 = (int64_t)at.n * BN;
   const Dst d{element(a.g.out, e * a.out_stride, a.g.out_f32), a.g.J, a.g.I, a.g.J, a.g.out_f32, a.g.accumulate};
   if (s.length == 0) {
     zero_tile(d, i0, j0);
@@ -927,28 +951,35 @@ hipError_t launch_bwd(const GemmArgs& gd, const GemmArgs& gw, float* ws, hipStre
   return hipGetLastError();
 }
 
-template <bool BT>
+template <bool BT, bool RAGGED>
 hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream) {
-  const int64_t tiles_n = (a.g.J + BN - 1) / BN;
-  const int64_t most = (a.g.I / BM + a.E) * tiles_n;  // tiles of any segments of so many rows
+  // RAGGED as a loop over tiles runs out of registers: a workgroup for any tile that there can be
+  constexpr bool PERSISTENT = !RAGGED;
+  const int64_t tiles_n = (a.g.J + BN - 1) / BN, most = grouped_mx_tiles(a);
   static std::atomic<uint64_t> attr_set{0};
-  if (hipError_t e = set_lds_attr(&grouped_mx_rows_kernel<BT>, &attr_set)) return e;
-  hipLaunchKernelGGL(grouped_mx_rows_kernel<BT>, dim3((uint32_t)(most < kSkGrid ? most : kSkGrid)), dim3(THREADS),
-                     LDS_BYTES, stream, a, tiles_n);
+  if (hipError_t e = set_lds_attr(&grouped_mx_rows_kernel<BT, RAGGED, PERSISTENT>, &attr_set)) return e;
+  hipLaunchKernelGGL((grouped_mx_rows_kernel<BT, RAGGED, PERSISTENT>),
+                     dim3((uint32_t)(PERSISTENT && most > kSkGrid ? kSkGrid : most)), dim3(THREADS), LDS_BYTES, stream, a,
+                     (uint32_t)tiles_n);
   return hipGetLastError();
 }
 
 }  // namespace
 
+int64_t grouped_mx_tiles(const GroupedArgs& a) { return (a.g.I / BM + a.E) * ((a.g.J + BN - 1) / BN); }
+
 hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream) {
-  if (a.g.bmode == BScale::Block)
-    return a.g.bt ? launch_grouped_rows_mx<true>(a, stream) : launch_grouped_rows_mx<false>(a, stream);
+  if (a.g.bmode == BScale::Block) {
+    if (gemm_mx_eligible(a.g))  // whole groups of four 128-blocks, their scales 16-byte aligned
+      return a.g.bt ? launch_grouped_rows_mx<true, false>(a, stream) : launch_grouped_rows_mx<false, false>(a, stream);
+    return a.g.bt ? launch_grouped_rows_mx<true, true>(a, stream) : launch_grouped_rows_mx<false, true>(a, stream);
+  }
   const int64_t tiles_m = (a.g.I + BM - 1) / BM, tiles_n = (a.g.J + BN - 1) / BN;
   const int64_t turns = (a.E * tiles_m * tiles_n + 8 * WG_RUN - 1) / (8 * WG_RUN);
   static std::atomic<uint64_t> attr_set{0};
   if (hipError_t e = set_lds_attr(&grouped_mx_wgrad_kernel, &attr_set)) return e;
   hipLaunchKernelGGL(grouped_mx_wgrad_kernel, dim3((uint32_t)(turns * 8 * WG_RUN)), dim3(THREADS), LDS_BYTES, stream, a,
-                     tiles_m, tiles_n);
+                     (uint32_t)tiles_m, (uint32_t)tiles_n);
   return hipGetLastError();
 }
 

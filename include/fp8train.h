@@ -127,13 +127,13 @@ int fp8_moe_combine_backward(int64_t T, int64_t H, int64_t R, int k, const uint1
  *   Wgrad  dW_e  = sum over e's rows r of dy[r]^T x[r]: qdyT [N][R] + sdyT
  *          [N][R/128], qxT [K][R] + sxT [K][R/128], dw [E][N][K]; an expert
  *          without rows has zeros (with FP8BLK_OUT_FP32_ACCUM, what was there)
- *   offsets [E + 1] int32 (fp8_moe_sort's): multiples of 128, ascending, at most R;
- *     others count as the multiple of 128 below, inside [0, R], and a segment
- *     that ends before it starts is empty.
+ *   offsets [E + 1] int32 (fp8_moe_sort's): multiples of 128, ascending, at most R.
+ *     Others count as the multiple of 128 below, inside [0, R]; descending ones
+ *     give no defined result, but nothing outside the operands is touched.
  *   out_dtype: FP8BLK_OUT_BF16, FP8BLK_OUT_FP32 or FP8BLK_OUT_FP32_ACCUM.
  *   scale_mode: the rule that made all the scales.
  * Rows of y and dx outside the segments are not written.  All operands dense,
- * 16-byte aligned (offsets 4-byte); R, N, K positive multiples of 128, R < 2^31,
+ * 16-byte aligned (offsets 4-byte); R, N, K positive multiples of 128, R < 2^29,
  * N, K < 2^25, E <= FP8MOE_MAX_EXPERTS, R N and R K at most 2^40, E N K 2^38.
  * Results do not depend on how rows are spread over the other experts; sums are
  * fp32 with the accuracy of the GEMMs of fp8blk.h.

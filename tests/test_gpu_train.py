@@ -451,14 +451,13 @@ def test_grouped_results_do_not_depend_on_the_other_experts(way):
 
 @WAYS
 def test_grouped_odd_offsets_stay_inside(way):
-    """Offsets outside the buffer, between multiples of 128 or descending: as documented, and nothing out of range."""
+    """Offsets outside the buffer or between multiples of 128 count as documented; descending ones touch nothing else."""
     import torch
     c = Grouped(4, 256, 512, "even", POW2, behind=0)
     ok = c.run(way, out_dtype=torch.float32)
     c.offsets = np.array([-300, 200, 257, 384 + 127, 99999], np.int32)      # 0, 128, 256, 384, 512
     assert torch.equal(c.run(way, out_dtype=torch.float32), ok)
-    c.offsets = np.array([0, 512, 128, 128, 512], np.int32)                # the second is empty
-    got = torch.full(c.shape(way), float("nan"), device="cuda")
-    c.run(way, out_dtype=torch.float32, out=got)
-    if way == "wgrad":
-        assert bool((got[1:3] == 0).all()) and not bool(got.isnan().any())
+    c.offsets = np.array([0, 512, 128, 128, 512], np.int32)
+    room = torch.full((c.shape(way)[0] + 2, *c.shape(way)[1:]), -3.0, device="cuda")
+    c.run(way, out_dtype=torch.float32, out=room[1:-1])
+    assert bool((room[0] == -3.0).all()) and bool((room[-1] == -3.0).all())

@@ -111,8 +111,8 @@ def test_gemm_errors(lib, name):
     names = ("R", "N", "K", "E", "a", "sa", "b", "sb", "off", "out", "odt", "mode", "stream")
     call = caller(getattr(lib, "fp8_moe_gemm_" + name), names, (512, 256, 384, 7, P[0], P[1], P[2], P[3], P[4], P[5], 0, 0, None))
     check(call, null=("a", "sa", "b", "sb", "off", "out"), fine=({"odt": 1}, {"odt": 2}, {"mode": 1}, {"E": 1024}, {"R": 128}),
-          arg=({"odt": 3}, {"mode": 2}, {"E": 1025}, {"R": 1 << 31}, {"N": 1 << 25}, {"K": 1 << 25},
-               {"N": 1 << 24, "K": 1 << 16}, {"R": 1 << 30, "N": 1 << 11}),
+          arg=({"odt": 3}, {"mode": 2}, {"E": 1025}, {"R": 1 << 29}, {"N": 1 << 25}, {"K": 1 << 25},
+               {"N": 1 << 24, "K": 1 << 16}, {"R": 1 << 28, "N": 1 << 13}),
           dim=({"R": 0}, {"R": 100}, {"N": 200}, {"K": 0}, {"E": 0}, {"E": -1}),
           align=({"a": P[0] + 8}, {"b": P[2] + 8}, {"out": P[5] + 8}, {"sa": P[1] + 2}, {"sb": P[3] + 2}, {"off": P[4] + 2}))
 
