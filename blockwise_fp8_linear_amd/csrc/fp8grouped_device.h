@@ -88,6 +88,21 @@ __device__ __forceinline__ int expert_of_tile(const GroupedMap& lds, int E, uint
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// The tiles of one workgroup: at, at + step, ... below end.  How many there are is known on the device alone, so the
+// XCDs (which get the workgroups in turn) have a run of tiles each by that count:
+// by the grid, the last XCDs would have none.  The grid is a multiple of 8.
+struct TileRun {
+  uint32_t at, end, step;
+};
+__device__ __forceinline__ TileRun tile_run(uint32_t total) {
+  const uint32_t xcd = blockIdx.x % 8, per = (total + 7) / 8, first = xcd * per;
+  const uint32_t end = total < first ? first : total - first < per ? total : first + per;
+  return {first + blockIdx.x / 8, end, gridDim.x / 8};
+}
+inline uint32_t grouped_grid(int64_t tiles, int64_t most) {  // up to `most`, a multiple of 8
+  return (uint32_t)(tiles < most ? (tiles + 7) / 8 * 8 : most);
+}
+
 // Tile `in` of a segment's (or an expert's) tiles_m x tiles_n -> its row and
 // column of tiles: down a group of GM tile rows before moving right, as the dense
 // kernels go, so that tiles in flight together share operand panels in L2.

@@ -582,15 +582,14 @@ __global__ __launch_bounds__(C::THREADS) void grouped_rows_kernel(GroupedArgs a,
   __shared__ GroupedMap map;
   const int E = (int)a.E;
   grouped_map<C::THREADS, C::BM>(map, a.offsets, E, (int32_t)a.g.I);
-  const uint64_t total = (uint64_t)map.starts[E] * tiles_n;
+  const TileRun run = tile_run(map.starts[E] * tiles_n);
   v4f acc[C::TM][C::TN];
-  for (uint64_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+  for (uint32_t t = run.at; t < run.end; t += run.step) {
     // an expert's tiles are tiles_n for each of its row tiles, so its first is starts * tiles_n
-    const int e = expert_of_tile(map, E, (uint32_t)(t / tiles_n));
+    const int e = expert_of_tile(map, E, t / tiles_n);
     const Segment s = segment_between(map.edges[e], map.edges[e + 1]);
     const GemmArgs g = expert_rows(a, e, s);
-    const TileAt at = tile_at<8>((uint32_t)(t - (uint64_t)map.starts[e] * tiles_n),
-                                 (uint32_t)(s.length + C::BM - 1) / C::BM, tiles_n);
+    const TileAt at = tile_at<8>(t - map.starts[e] * tiles_n, (uint32_t)(s.length + C::BM - 1) / C::BM, tiles_n);
     const int64_t i0 = (int64_t)at.m * C::BM, j0 = (int64_t)at.n * C::BN;
     gemm_tile<C>(g, lds, i0, j0, 0, g.R / 128, acc);
     gk_store<C>(acc, g.out, g.J, g.I, g.J, g.out_f32, g.accumulate, i0, j0);
@@ -680,8 +679,8 @@ static hipError_t launch_grouped_rows_cfg(const GroupedArgs& a, hipStream_t stre
   static std::atomic<uint64_t> attr_set{0};
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_rows_kernel<C>), C::LDS, &attr_set))
     return e;
-  hipLaunchKernelGGL(grouped_rows_kernel<C>, dim3((uint32_t)(most < kSkGrid ? most : kSkGrid)), dim3(C::THREADS),
-                     C::LDS, stream, a, (uint32_t)tiles_n);
+  hipLaunchKernelGGL(grouped_rows_kernel<C>, dim3(grouped_grid(most, kSkGrid)), dim3(C::THREADS), C::LDS, stream, a,
+                     (uint32_t)tiles_n);
   return hipGetLastError();
 }
 

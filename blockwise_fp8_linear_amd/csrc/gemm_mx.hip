@@ -61,16 +61,21 @@ constexpr int HALF = TM / 2;               // of a tile of 128 rows (the last on
 // rows, so every direct load reads whole cache lines.
 constexpr int PK = 2 * BK;                         // bytes of a row in a pair slot
 constexpr int B_SLOT = BN * PK;
-template <int T>  // T: MFMA tiles of a wave down the rows
-struct Slot {
-  static constexpr int ROWS = 64 * T, A = ROWS * PK, BYTES = A + B_SLOT;  // 64 KiB (T = TM)
-  static constexpr int LOADS_A = A / 1024 / (THREADS / 64);               // 1 KiB per wave instruction
-};
-constexpr int SLOTS = 2;
-constexpr int SC_BYTES = 8192;            // one group of raw scales: A rows, then B rows
 constexpr int MAX_KB = (int)kMxMaxKb;     // 128-blocks per segment with weight-block scales (held in LDS)
 constexpr int BS_BYTES = 4 * MAX_KB * 4;  // the 4 waves' weight-block scales of a segment, fp32
-constexpr int LDS_BYTES = SLOTS * Slot<TM>::BYTES + 2 * SC_BYTES + BS_BYTES;  // 146 KiB
+// The ring for T MFMA tiles of a wave down the rows.  A tile of 128 rows is soon
+// computed, so its loads run two pairs ahead, in a third slot: an expert with few
+// rows waits for its weights alone.
+template <int T>
+struct Ring {
+  static constexpr int ROWS = 64 * T, SLOTS = T == TM ? 2 : 3;
+  static constexpr int A = ROWS * PK, SLOT = A + B_SLOT;     // 64 KiB (T = TM) or 48
+  static constexpr int LOADS_A = A / 1024 / (THREADS / 64);  // 1 KiB per wave instruction
+  static constexpr int SC = T == TM ? 8192 : 16 * ROWS;      // one group of raw scales: A rows, then B rows (T = TM)
+  static constexpr int BYTES = SLOTS * SLOT + 2 * SC + BS_BYTES;
+};
+constexpr int LDS_BYTES = Ring<TM>::BYTES;  // 146 KiB
+constexpr int LDS_BYTES_ROWS = Ring<HALF>::BYTES > LDS_BYTES ? Ring<HALF>::BYTES : LDS_BYTES;  // 150 KiB
 constexpr int LOADS_B = B_SLOT / 1024 / (THREADS / 64);
 
 template <int V>
@@ -130,8 +135,10 @@ template <bool BROW, bool BT = false, bool RAGGED = false, int TM = fp8blk::TM>
 __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int64_t i0, int64_t j0, int64_t kb_begin,
                                             int64_t nkb_seg, v16f (&acc)[TM][TN]) {
   static_assert(!(BT && BROW), "the transposed-B layout is Dgrad's, with weight-block scales");
-  constexpr int LOADS_A = Slot<TM>::LOADS_A, LOADS_PER_PAIR = LOADS_A + LOADS_B, WM = 32 * TM;
-  constexpr int A_SLOT = Slot<TM>::A, SLOT = Slot<TM>::BYTES;
+  static_assert(!BROW || TM == fp8blk::TM, "a tile of 128 rows has no room for B's row scales");
+  typedef Ring<TM> Rg;
+  constexpr int LOADS_A = Rg::LOADS_A, LOADS_PER_PAIR = LOADS_A + LOADS_B, WM = 32 * TM;
+  constexpr int SLOTS = Rg::SLOTS, A_SLOT = Rg::A, SLOT = Rg::SLOT, SC_BYTES = Rg::SC;
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t wm = wave >> 1, wn = wave & 1;
@@ -181,7 +188,7 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   // issue_one(p, u): the wave's u-th direct load of pair p (u < LOADS_A: A).
   auto issue_one = [&](int pr, int u) {
     const int pc = pr < npair ? pr : npair - 1;
-    const uint32_t slot = lds0 + (uint32_t)(pr % SLOTS) * SLOT;
+    const uint32_t slot = lds0 + (uint32_t)pr % SLOTS * SLOT;
     if (u < LOADS_A)
       dma16(baseA + (int64_t)pc * PK, offLA[u], slot + (wave * LOADS_A + u) * 1024);
     else
@@ -213,12 +220,13 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   const uint32_t sc0 = lds0 + SLOTS * SLOT;
   auto issue_scales = [&](int q) {  // group q -> scale buffer q & 1
     const uint32_t buf = sc0 + (uint32_t)(q & 1) * SC_BYTES;
+    if (wave * 64 >= Rg::ROWS) return;  // a tile of 128 rows: two waves' rows
     if constexpr (RAGGED) {
       // [block of the group][row]; a block past the end loads the last one's
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = 4 * q + i < npair ? 4 * q + i : npair - 1;
-        dma4(baseSA + 4 * k, offSA, buf + i * 1024 + wave * 256);
+        dma4(baseSA + 4 * k, offSA, buf + i * 4 * Rg::ROWS + wave * 256);
         if constexpr (BROW) dma4(baseSB + 4 * k, offSB, buf + 4096 + i * 1024 + wave * 256);
       }
       return;
@@ -238,7 +246,7 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   // the second chunk sits 16 bytes after or before the first (signed!)
   const int32_t hiOff = ((swzl & 1) ? -16 : 16);
   auto read_frag = [&](int st, uint32_t off) {
-    const uint8_t* p = lds + ((st >> 1) % SLOTS) * SLOT + off + ((st & 1) ? cA1 : cA0);
+    const uint8_t* p = lds + (uint32_t)(st >> 1) % SLOTS * SLOT + off + ((st & 1) ? cA1 : cA0);
     const u32x4 lo = *reinterpret_cast<const u32x4*>(p);
     const u32x4 hi = *reinterpret_cast<const u32x4*>(p + hiOff);
     return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
@@ -252,7 +260,7 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   const uint32_t bt_q = lane >> 4, bt_s = lane & 15;
   const uint32_t bt_row = (32 * (bt_q >> 1) + (bt_s >> 1)) * 256 + 8 * (bt_s & 1);
   auto read_frag_bt = [&](int st, int t) {
-    const uint8_t* p = lds + ((st >> 1) % SLOTS) * SLOT + A_SLOT + bt_row + (st & 1) * 64 * 256 +
+    const uint8_t* p = lds + (uint32_t)(st >> 1) % SLOTS * SLOT + A_SLOT + bt_row + (st & 1) * 64 * 256 +
                        (((((wn0 >> 4) + 2 * t + (bt_q & 1)) ^ (2 * (bt_s >> 1))) << 4));
     v8i f;
 #pragma unroll
@@ -298,7 +306,7 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
       if constexpr (!RAGGED) return pack_e8(*reinterpret_cast<const u32x4*>(rows + row * 16));
       u32x4 s;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const uint32_t*>(rows + i * 1024 + row * 4);
+      for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const uint32_t*>(rows + i * 4 * Rg::ROWS + row * 4);
       return pack_e8(s);
     };
 #pragma unroll
@@ -328,9 +336,9 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   // pairs 0 and 1; then pair 0 and group 0 visible
   if constexpr (!BROW) issue_block_scales();
   issue_scales(0);
-  issue_pair(0);
-  issue_pair(1);
-  wait_vmcnt<LOADS_PER_PAIR>();  // everything but pair 1 has landed
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) issue_pair(s);
+  wait_vmcnt<(SLOTS - 1) * LOADS_PER_PAIR>();  // everything but the pairs behind pair 0 has landed
   lds_barrier();
   read_frags(0, fa[0], fb[0]);
   read_scales(0, sa_cur, sb_cur);
@@ -346,12 +354,13 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   // sched_barrier fences pin the interleaving.
   static_assert((TM == 4 || TM == 2) && TN == 4 && LOADS_PER_PAIR == 8 + 2 * TM,
                 "of the next stage's fragments one (TM 2: up to two), of its loads two (three) per MFMA pair");
+  // (Three slots: pair p+1 is on the way then, and pair p+2 the one refilled.)
   auto stage_step = [&](int st, auto buf_tag, auto opsel_tag) {
     constexpr int OPSEL = decltype(opsel_tag)::value;
     constexpr int BUF = decltype(buf_tag)::value;  // also the parity of st
     constexpr int NXT = BUF ^ 1;
     if constexpr (BUF == 1) {
-      wait_vmcnt<0>();  // this wave's part of pair (st+1)/2 (and older) has landed
+      wait_vmcnt<(SLOTS - 2) * LOADS_PER_PAIR>();  // this wave's part of pair (st+1)/2 (and older) has landed
       lds_barrier();    // ... and every wave's
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -378,7 +387,7 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
       if constexpr (BUF == 1) {
         constexpr int EACH = LOADS_PER_PAIR / (2 * TM);
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) issue_one((st + 3) >> 1, EACH * p + i);
+        for (int i = 0; i < EACH; ++i) issue_one(((st + 1) >> 1) + SLOTS - 1, EACH * p + i);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -841,26 +850,30 @@ __global__ __launch_bounds__(256) void bwd_fixup_kernel(GemmArgs gd, GemmArgs gw
 
 // Every expert's product over its own segment of rows (Fprop and Dgrad of a
 // mixture; BT: Dgrad from the weight codes as quantized).  Tile t of all experts'
-// is found by the map that each workgroup makes at its start; PERSISTENT: a
-// workgroup takes every gridDim.x-th.  A segment that ends in a block of 128 rows
-// has a tile of 128 there.
-template <bool BT, bool RAGGED, bool PERSISTENT>
+// is found by the map that each workgroup makes at its start.  A segment that ends
+// in a block of 128 rows has a tile of 128 there; where all tiles are of 128 rows
+// and there is still at most one a CU, all of them are.
+template <bool BT, bool RAGGED>
 __global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   __shared__ GroupedMap map;
   const int E = (int)a.E;
   grouped_map<THREADS, BM>(map, a.offsets, E, (int32_t)a.g.I);
-  const uint32_t total = map.starts[E] * tiles_n;
-  for (uint32_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+  const uint32_t blocks = (uint32_t)(map.edges[E] - map.edges[0]) / 128;  // of ascending segments
+  const uint32_t halves = blocks <= (uint32_t)kSkGrid && blocks * tiles_n <= (uint32_t)kSkGrid ? 1 : 0;
+  const TileRun run = tile_run((map.starts[E] << halves) * tiles_n);
+  for (uint32_t t = run.at; t < run.end; t += run.step) {
+    const uint32_t tile = t >> halves;
     // an expert's tiles are tiles_n for each of its row tiles, so its first is starts * tiles_n
-    const int e = expert_of_tile(map, E, t / tiles_n);
+    const int e = expert_of_tile(map, E, tile / tiles_n);
     const Segment s = segment_between(map.edges[e], map.edges[e + 1]);
     const GemmArgs g = expert_rows(a, e, s);
-    const TileAt at = tile_at<4>(t - map.starts[e] * tiles_n, (uint32_t)(s.length + BM - 1) / BM, tiles_n);
-    const int64_t i0 = (int64_t)at.m * BM, j0 = (int64_t)at.n * BN;
+    const TileAt at = tile_at<4>(tile - map.starts[e] * tiles_n, (uint32_t)(s.length + BM - 1) / BM, tiles_n);
+    const int64_t i0 = (int64_t)at.m * BM + (halves ? (t & 1) * (BM / 2) : 0), j0 = (int64_t)at.n * BN;
+    if (i0 >= s.length) continue;
     const Dst d{g.out, g.J, g.I, g.J, g.out_f32, g.accumulate};
-    if constexpr (PERSISTENT) lds_barrier();  // the previous tile's epilogue is done with LDS
-    if (s.length - i0 > BM / 2) {
+    lds_barrier();  // the previous tile's epilogue is done with LDS
+    if (!halves && s.length - i0 > BM / 2) {
       v16f acc[TM][TN];
       mma_segment<false, BT, RAGGED>(g, lds, i0, j0, 0, g.R / 128, acc);
       store_tile<1>(d, lds, i0, j0, acc);
@@ -869,7 +882,8 @@ __global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a,
       mma_segment<false, BT, RAGGED, HALF>(g, lds, i0, j0, 0, g.R / 128, acc);
       store_tile<1>(d, lds, i0, j0, acc);
     }
-    if constexpr (!PERSISTENT) return;
+    // RAGGED, as a loop, runs out of registers: its grid has a workgroup for any tile
+    if constexpr (RAGGED) return;
   }
 }
 
@@ -953,14 +967,15 @@ hipError_t launch_bwd(const GemmArgs& gd, const GemmArgs& gw, float* ws, hipStre
 
 template <bool BT, bool RAGGED>
 hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream) {
-  // RAGGED as a loop over tiles runs out of registers: a workgroup for any tile that there can be
-  constexpr bool PERSISTENT = !RAGGED;
-  const int64_t tiles_n = (a.g.J + BN - 1) / BN, most = grouped_mx_tiles(a);
+  // in halves there are at most 2 kSkGrid
+  const int64_t tiles_n = (a.g.J + BN - 1) / BN, tiles = grouped_mx_tiles(a);
+  const int64_t most = !RAGGED ? kSkGrid : tiles > 2 * kSkGrid ? (tiles + 7) / 8 * 8 : 2 * kSkGrid;
   static std::atomic<uint64_t> attr_set{0};
-  if (hipError_t e = set_lds_attr(&grouped_mx_rows_kernel<BT, RAGGED, PERSISTENT>, &attr_set)) return e;
-  hipLaunchKernelGGL((grouped_mx_rows_kernel<BT, RAGGED, PERSISTENT>),
-                     dim3((uint32_t)(PERSISTENT && most > kSkGrid ? kSkGrid : most)), dim3(THREADS), LDS_BYTES, stream, a,
-                     (uint32_t)tiles_n);
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_mx_rows_kernel<BT, RAGGED>),
+                                      LDS_BYTES_ROWS, &attr_set))
+    return e;
+  hipLaunchKernelGGL((grouped_mx_rows_kernel<BT, RAGGED>), dim3(grouped_grid(2 * tiles, most)), dim3(THREADS),
+                     LDS_BYTES_ROWS, stream, a, (uint32_t)tiles_n);
   return hipGetLastError();
 }
 
