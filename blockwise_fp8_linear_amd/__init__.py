@@ -476,7 +476,8 @@ def fp8_block_gemm_backward_w_noalloc(qdy, sdy, qw, sw, qdyT, sdyT, qxT, sxT, dx
 _MOE = ("fp8_linear", "fp8_linear_workspace_size", "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_experts",
         "fp8_moe_layer", "fp8_moe_workspace_size", "FP8_LINEAR_FP32_ROWS", "FP8MOE_BF16", "FP8MOE_FP32", "FP8MOE_MAX_EXPERTS",
         "FP8MOE_MAX_TOPK", "FP8MOE_MAX_TOKENS")
-_TRAIN = ("fp8_moe_sorted_rows", "fp8_moe_sort_workspace_size", "fp8_moe_sort", "fp8_moe_gather", "fp8_moe_combine",
+_TRAIN = ("fp8_moe_sorted_rows", "fp8_moe_sort_workspace_size", "fp8_moe_sort", "fp8_moe_gather",
+          "fp8_moe_gather_workspace_size", "fp8_moe_combine",
           "fp8_moe_combine_backward", "fp8_moe_gemm_fprop", "fp8_moe_gemm_dgrad", "fp8_moe_gemm_wgrad",
           "fp8_gated_forward", "fp8_gated_backward", "fp8_requantize_colgroup")
 

@@ -135,14 +135,23 @@ int fp8_moe_sort(int64_t T, int64_t E, int k, const int32_t* ids, int32_t* rows,
                                 static_cast<int32_t*>(workspace), stream));
 }
 
+size_t fp8_moe_gather_workspace_size(int64_t T, int64_t H, int64_t R, int k, int transpose) {
+  return check_sorted(T, H, R, k) == FP8BLK_OK ? gather_order_bytes(T, H, R, k, transpose != 0) : (size_t)-1;
+}
+
 int fp8_moe_gather(int64_t T, int64_t H, int64_t R, int k, const uint16_t* x, int64_t ld_x, const int32_t* source,
                    const float* weights, const int32_t* used, uint8_t* q, int64_t ld_q, float* s, uint8_t* qT,
-                   int64_t ld_qT, float* sT, int scale_mode, hipStream_t stream) {
+                   int64_t ld_qT, float* sT, int scale_mode, void* workspace, size_t ws_bytes, hipStream_t stream) {
   const CodesOut rows{q, ld_q, s}, cols{qT, ld_qT, sT};
   if (int rc = check_gather(T, H, R, k, x, ld_x, source, weights, used, rows, cols, scale_mode)) return rc;
+  const size_t need = gather_order_bytes(T, H, R, k, qT != nullptr);
+  if (need > 0 && (!workspace || ws_bytes < need)) return FP8BLK_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return FP8BLK_ERR_ALIGN;
   if (int rc = check_device()) return rc;
   return finish(launch_moe_gather(
-      GatherArgs{T, H, R, k, x, ld_x, source, weights, used, rows, cols, scale_mode == FP8BLK_SCALE_FP32}, stream));
+      GatherArgs{T, H, R, k, x, ld_x, source, weights, used, rows, cols, scale_mode == FP8BLK_SCALE_FP32,
+                 need > 0 ? static_cast<uint32_t*>(workspace) : nullptr},
+      stream));
 }
 
 int fp8_moe_combine(int64_t T, int64_t H, int64_t R, int k, const uint16_t* z, int64_t ld_z, const int32_t* rows,
@@ -172,7 +181,8 @@ int fp8_moe_combine_backward(int64_t T, int64_t H, int64_t R, int k, const uint1
   if (!aligned4(rows) || !aligned4(dweights)) return FP8BLK_ERR_ALIGN;
   if (int rc = check_device()) return rc;
   if (hipError_t e = launch_moe_gather(
-          GatherArgs{T, H, R, k, dy, ld_dy, source, weights, used, r, c, scale_mode == FP8BLK_SCALE_FP32}, stream))
+          GatherArgs{T, H, R, k, dy, ld_dy, source, weights, used, r, c, scale_mode == FP8BLK_SCALE_FP32, nullptr},
+          stream))
     return finish(e);
   return finish(launch_moe_combine_dweights(T, H, R, k, dy, ld_dy, z, ld_z, rows, dweights, stream));
 }

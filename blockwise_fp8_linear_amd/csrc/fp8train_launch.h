@@ -46,7 +46,22 @@ struct GatherArgs {
   const int32_t* used;
   CodesOut q, qT;
   bool fp32_scale;
+  uint32_t* order;  // the workspace of gather_order_bytes(), or null where that is 0
 };
+// Row groups of many rows are gathered in the order of their tokens, in runs of a
+// few rows, which a first launch finds: where x outgrows two XCDs' L2 and its
+// rows are read several times over.
+constexpr int64_t kOrderRuns = 32768;
+inline int64_t order_run(int64_t R) {
+  const int64_t least = (R + kOrderRuns - 1) / kOrderRuns;
+  return least <= 4 ? 4 : (least + 7) / 8 * 8;
+}
+inline bool gather_ordered(int64_t T, int64_t H, int64_t R, int k, bool both) {
+  return !both && k > 1 && T * H * 2 > (int64_t(8) << 20) && R >= 2 * T && order_run(R) <= 64;
+}
+inline size_t gather_order_bytes(int64_t T, int64_t H, int64_t R, int k, bool both) {
+  return gather_ordered(T, H, R, k, both) ? (size_t)((R + order_run(R) - 1) / order_run(R)) * sizeof(uint32_t) : 0;
+}
 hipError_t launch_moe_gather(const GatherArgs& a, hipStream_t stream);
 
 hipError_t launch_moe_combine(int64_t T, int64_t H, int64_t R, int k, const uint16_t* z, int64_t ld_z,

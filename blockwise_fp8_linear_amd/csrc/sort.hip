@@ -109,10 +109,19 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(int64_t n, int E, 
     const uint32_t part = t / (uint32_t)E, e = t - part * (uint32_t)E;
     if (part < parts) {
       int32_t all = 0, mine = 0;
-      for (uint32_t b = part; b < gridDim.x; b += parts) {
-        const int32_t v = counts[(int64_t)b * E + e];
-        all += v;
-        mine += b < blockIdx.x ? v : 0;
+      // eight on the way at a time
+      for (uint32_t b0 = part; b0 < gridDim.x; b0 += 8 * parts) {
+        int32_t v[8];
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u) {
+          const uint32_t b = b0 + u * parts;
+          v[u] = b < gridDim.x ? counts[(int64_t)b * E + e] : 0;
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u) {
+          all += v[u];
+          mine += b0 + u * parts < blockIdx.x ? v[u] : 0;
+        }
       }
       part_total[part * E + e] = all;
       part_before[part * E + e] = mine;
@@ -141,10 +150,18 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(int64_t n, int E, 
       offsets[t] = at;
       if (t == (uint32_t)E - 1) offsets[E] = end;
     }
-    // padding, an expert's by one workgroup
-    if (t % gridDim.x == blockIdx.x)
-      for (int32_t r = at + total; r < at + length; ++r) source[r] = -1;
   }
+  // padding: an expert's by one wave of one workgroup
+  __syncthreads();  // wave_sum has been read
+  int32_t* const pad_from = &wave_count[0][0];
+  int32_t* const pad_to = &wave_count[kWaves / 2][0];
+  if (t < (uint32_t)E) {
+    pad_from[t] = at + total;
+    pad_to[t] = at + length;
+  }
+  __syncthreads();
+  for (uint32_t e = blockIdx.x + wave * gridDim.x; e < (uint32_t)E; e += kWaves * gridDim.x)
+    for (int32_t r = pad_from[e] + (int32_t)lane; r < pad_to[e]; r += 64) source[r] = -1;
   for (int64_t r = end + (int64_t)blockIdx.x * kThreads + t; r < R; r += (int64_t)gridDim.x * kThreads) source[r] = -1;
 
   int32_t next = at + before;  // the row of expert t's next choice

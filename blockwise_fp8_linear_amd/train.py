@@ -37,7 +37,7 @@ def _functions():
     gemm = [i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, i32, i32, vp]
     sig = {
         "fp8_moe_sort": [i64, i64, i32, vp, vp, vp, vp, vp, sz, vp],
-        "fp8_moe_gather": [i64, i64, i64, i32, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, vp, i32, vp],
+        "fp8_moe_gather": [i64, i64, i64, i32, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, vp, i32, vp, sz, vp],
         "fp8_moe_combine": [i64, i64, i64, i32, vp, i64, vp, vp, vp, i32, vp],
         "fp8_moe_combine_backward": [i64, i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, i64, vp, vp,
                                      i32, vp],
@@ -54,6 +54,8 @@ def _functions():
     for name in ("fp8_moe_sorted_rows", "fp8_moe_sort_workspace_size"):
         f = getattr(lib, name)
         f.argtypes, f.restype = [i64, i64, i32], sz
+    lib.fp8_moe_gather_workspace_size.argtypes = [i64, i64, i64, i32, i32]
+    lib.fp8_moe_gather_workspace_size.restype = sz
     _FUNCTIONS = lib
     return lib
 
@@ -147,8 +149,20 @@ def fp8_moe_sort(ids, E, rows=None, source=None, offsets=None, workspace=None, s
     return rows, source, offsets
 
 
+@functools.lru_cache(maxsize=4096)
+def _gather_need(T, H, R, k, transpose):
+    return _functions().fp8_moe_gather_workspace_size(T, H, R, k, transpose)
+
+
+def fp8_moe_gather_workspace_size(T: int, H: int, R: int, topk: int, transpose: bool = False) -> int:
+    need = _gather_need(T, H, R, topk, 1 if transpose else 0)
+    if _invalid(need):
+        raise ValueError(f"fp8_moe_gather_workspace_size: no such gather: T {T}, H {H}, R {R}, topk {topk}")
+    return int(need)
+
+
 def fp8_moe_gather(x, source, topk, used=None, weights=None, transpose=False, q=None, s=None, qT=None, sT=None,
-                   stream=None, scale_mode=_fb.FP8BLK_SCALE_POW2):
+                   workspace=None, stream=None, scale_mode=_fb.FP8BLK_SCALE_POW2):
     """The tokens' rows in sorted order, quantized.  x bf16 [T,H] (row stride may
     exceed H), source int32 [R] -> (q uint8 [R,H], s fp32 [R,H/128]), or with
     transpose (q, s, qT uint8 [H,R], sT fp32 [H,R/128]): the codes that
@@ -168,8 +182,10 @@ def fp8_moe_gather(x, source, topk, used=None, weights=None, transpose=False, q=
     pqT, ldT, psT = None, 0, None
     if transpose:
         qT, pqT, ldT, sT, psT = _codes(qT, sT, H, R, "qT", x, index, stream)
-    rc = _functions().fp8_moe_gather(T, H, R, topk, x.data_ptr(), ld, psource, pw, pused, pq, ldq, ps, pqT, ldT, psT,
-                                     scale_mode, _stream(stream, index))
+    lib = _functions()
+    keep, ws, size = _scratch(_gather_need(T, H, R, topk, 1 if transpose else 0), workspace, x, index, stream)
+    rc = lib.fp8_moe_gather(T, H, R, topk, x.data_ptr(), ld, psource, pw, pused, pq, ldq, ps, pqT, ldT, psT, scale_mode,
+                            ws, size, _stream(stream, index))
     if rc:
         _fb._check(rc)
     return (q, s, qT, sT) if transpose else (q, s)

@@ -80,6 +80,8 @@ int fp8_moe_sort(int64_t T, int64_t E, int k, const int32_t *ids, int32_t *rows,
  *     fp8_quantize_rowgroup of those rows
  *   qT [H][R] codes (row stride ld_qT >= R, multiple of 16), sT [H][R/128]: as
  *     fp8_quantize_colgroup of them; both NULL to skip
+ *   workspace: at least fp8_moe_gather_workspace_size(T, H, R, k, qT != NULL)
+ *     bytes, 16-byte aligned; may be NULL when that size is 0.
  *   H and R positive multiples of 128; 1 <= k <= FP8MOE_MAX_TOPK; T < 2^24,
  *   R < 2^31, R H < 2^37, T ceil(H / 512) < 2^25; T ld_x, R ld_q and H ld_qT at
  *   most 2^40.
@@ -87,7 +89,11 @@ int fp8_moe_sort(int64_t T, int64_t E, int k, const int32_t *ids, int32_t *rows,
 int fp8_moe_gather(int64_t T, int64_t H, int64_t R, int k, const uint16_t *x, int64_t ld_x,
                    const int32_t *source, const float *weights, const int32_t *used,
                    uint8_t *q, int64_t ld_q, float *s, uint8_t *qT, int64_t ld_qT, float *sT,
-                   int scale_mode, hipStream_t stream);
+                   int scale_mode, void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of fp8_moe_gather, with (transpose != 0) or without qT and sT
+ * ((size_t)-1 for an invalid shape). */
+size_t fp8_moe_gather_workspace_size(int64_t T, int64_t H, int64_t R, int k, int transpose);
 
 /*
  * Sorted rows back to their tokens: y[t] = sum_i weights[t][i] z[rows[t][i]], in

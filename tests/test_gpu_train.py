@@ -154,6 +154,26 @@ def test_gather_used_and_sources_of_no_choice(used):
             expect_cols(r[2], r[3], rows, POW2, end)
 
 
+@MODES
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("T,E,k,H,part", [(4000, 20, 4, 1152, 1.0), (2100, 300, 3, 2176, 0.7)])
+def test_gather_in_the_order_of_tokens(T, E, k, H, part, weighted, mode):
+    """Sizes that are gathered in the order of their tokens; a device count that ends inside a run's rows and in padding,
+    sources of no choice, and a source that stands in many rows."""
+    rng = synth.rng_for(36, T, H)
+    R = fb.fp8_moe_sorted_rows(T, E, k)
+    assert fb.fp8_moe_gather_workspace_size(T, H, R, k) > 0
+    _, source, offsets = train_ref.sort(choice(T, E, k, "odd", rng), E, R)
+    source[rng.integers(0, R, 200)] = 5
+    source[rng.integers(0, R, 50)] = [-7, T * k, 2 ** 31 - 1, -2 ** 31, -1] * 10
+    bits, x = activations(T, H, T, H + 8)
+    w = rng.standard_normal((T, k)).astype(np.float32) if weighted else None
+    used = int(offsets[-1] * part) // 128 * 128
+    q, s = fb.fp8_moe_gather(x, dev(source), k, used=limit(used), weights=None if w is None else dev(w),
+                             q=codes_buffer(R, H, 16), s=scales_buffer(R, H // 128), scale_mode=mode)
+    expect_rows(q, s, train_ref.gathered(bits, source, k, w), mode, used)
+
+
 # ------------------------------------------------------------------ combine --
 
 def combine_case(T, E, k, H, ld=None):

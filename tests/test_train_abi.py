@@ -16,7 +16,7 @@ import train_ref
 from blockwise_fp8_linear_amd import train
 from test_moe_abi import BAD, EALIGN, EARG, EDIM, ENULL, EWS, NOGPU, P, ROOT, bf16, caller, f32, i32, refused, u8, z
 
-NAMES = {"fp8_moe_sorted_rows", "fp8_moe_sort_workspace_size", "fp8_moe_sort", "fp8_moe_gather", "fp8_moe_combine",
+NAMES = {"fp8_moe_sorted_rows", "fp8_moe_gather_workspace_size", "fp8_moe_sort_workspace_size", "fp8_moe_sort", "fp8_moe_gather", "fp8_moe_combine",
          "fp8_moe_combine_backward", "fp8_moe_gemm_fprop", "fp8_moe_gemm_dgrad", "fp8_moe_gemm_wgrad",
          "fp8_gated_forward", "fp8_gated_backward", "fp8_requantize_colgroup"}
 BIG = 1 << 62
@@ -72,12 +72,13 @@ def test_sort_sizes(lib):
     assert lib.fp8_moe_sort_workspace_size(7, 8, 2) == 0      # one workgroup counts for itself
 
 
-GATHER = ("T", "H", "R", "k", "x", "ld", "src", "w", "used", "q", "ldq", "s", "qT", "ldT", "sT", "mode", "stream")
+GATHER = ("T", "H", "R", "k", "x", "ld", "src", "w", "used", "q", "ldq", "s", "qT", "ldT", "sT", "mode", "ws", "wsb",
+          "stream")
 
 
 def test_gather_errors(lib):
     call = caller(lib.fp8_moe_gather, GATHER, (5, 256, 512, 2, P[0], 256, P[1], None, None, P[2], 256, P[3], P[4], 512,
-                                               P[5], 0, None))
+                                               P[5], 0, None, 0, None))
     check(call, null=("x", "src", "q", "s", "qT", "sT"), fine=({"qT": None, "sT": None, "ldT": 0}, {"w": P[6], "mode": 1},
                                                                {"used": P[7], "ld": 264, "ldq": 272, "ldT": 528}),
           arg=({"mode": 2}, {"k": 17}, {"T": 1 << 24}, {"R": 1 << 31, "ldT": 1 << 31}, {"ld": 248}, {"ldq": 240}, {"ldT": 496},
@@ -87,6 +88,19 @@ def test_gather_errors(lib):
           dim=({"T": 0}, {"k": 0}, {"H": 0}, {"H": 200}, {"R": 0}, {"R": 100}),
           align=({"x": P[0] + 8}, {"ld": 260}, {"q": P[2] + 4}, {"ldq": 264}, {"s": P[3] + 2}, {"qT": P[4] + 8}, {"ldT": 520},
                  {"sT": P[5] + 1}, {"src": P[1] + 2}, {"w": P[6] + 2}, {"used": P[7] + 1}))
+
+
+def test_gather_workspace(lib):
+    q = lib.fp8_moe_gather_workspace_size
+    assert q(5, 256, 512, 2, 0) == q(5, 256, 512, 2, 1) == q(16384, 2048, 139264, 8, 1) == 0
+    need = q(16384, 2048, 139264, 8, 0)
+    assert need > 0 and fb.fp8_moe_gather_workspace_size(16384, 2048, 139264, 8) == need
+    for bad in ((0, 256, 512, 2), (5, 200, 512, 2), (5, 256, 100, 2), (5, 256, 512, 17), (1 << 24, 256, 512, 2)):
+        assert q(*bad, 0) == BAD, bad
+        refused("no such gather", fb.fp8_moe_gather_workspace_size, *bad)
+    call = caller(lib.fp8_moe_gather, GATHER, (16384, 2048, 139264, 8, P[0], 2048, P[1], None, None, P[2], 2048, P[3], None, 0,
+                                               None, 0, P[4], need, None))
+    assert call() in NOGPU and call(ws=None) == EWS and call(wsb=need - 1) == EWS and call(ws=P[4] + 8) == EALIGN
 
 
 def test_combine_errors(lib):
@@ -150,7 +164,7 @@ def test_header_is_c(tmp_path):
                    "  if (fp8_moe_sorted_rows(7, 8, 2) != 1536) return 1;\n"
                    "  if (fp8_moe_sort_workspace_size(0, 8, 2) != (size_t)-1) return 2;\n"
                    "  if (fp8_moe_sort(1, 1, 1, 0, 0, 0, 0, 0, 0, 0) != FP8BLK_ERR_NULL) return 3;\n"
-                   "  if (fp8_moe_gather(1, 128, 128, 1, 0, 128, 0, 0, 0, 0, 128, 0, 0, 0, 0, 7, 0) != FP8BLK_ERR_ARG) return 4;\n"
+                   "  if (fp8_moe_gather(1, 128, 128, 1, 0, 128, 0, 0, 0, 0, 128, 0, 0, 0, 0, 7, 0, 0, 0) != FP8BLK_ERR_ARG) return 4;\n"
                    "  if (fp8_moe_combine(1, 128, 128, 1, 0, 128, 0, 0, 0, 0, 0) != FP8BLK_ERR_NULL) return 5;\n"
                    "  if (fp8_moe_combine_backward(1, 128, 128, 1, 0, 128, 0, 128, 0, 0, 0, 0, 0, 128, 0, 0, 128, 0, 0, 0, 0) "
                    "!= FP8BLK_ERR_NULL) return 6;\n"
@@ -191,6 +205,7 @@ def host_stand_ins(monkeypatch):
         monkeypatch.setattr(m, "_index", lambda x, name: -1 if isinstance(x, torch.Tensor) else pytest.fail(name))
     monkeypatch.setattr(train, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(train, "_sort_sizes", lambda T, E, k: (512, 64))
+    monkeypatch.setattr(train, "_gather_need", lambda *a: 64)
 
 
 def test_binding_sorted(host_stand_ins):
@@ -215,6 +230,7 @@ def test_binding_sorted(host_stand_ins):
     refused("qT: the last", fb.fp8_moe_gather, x, source, k, transpose=True, qT=z((R, H), u8).t())
     refused("scales of qT: must be contiguous", fb.fp8_moe_gather, x, source, k, transpose=True, sT=z((R // 128, H), f32).t())
     refused("topk", fb.fp8_moe_gather, x, source, 2 ** 32 + 2)
+    refused("workspace", fb.fp8_moe_gather, x, source, k, workspace=3)
     refused("z: expected", fb.fp8_moe_combine, z((R, H), f32), rows)
     refused("rows: expected torch.int32", fb.fp8_moe_combine, zz, rows.long())
     refused("weights: expected shape", fb.fp8_moe_combine, zz, rows, z((T + 1, k), f32))
