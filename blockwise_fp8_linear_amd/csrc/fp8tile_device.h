@@ -37,6 +37,50 @@ __device__ __forceinline__ void store_codes(uint8_t* p, V v) {
   else *reinterpret_cast<V*>(p) = v;
 }
 
+// The amax / 448 rule with fewer instructions, for scales in [2^-64, infinity):
+// Fp32Scale's quotient without its factor, its clamp and its sign.  y = x r is
+// corrected by (x - s y) r, formed as -(s y - x) r + y: where x is a zero, s y - x
+// is +0 and the sum keeps y's sign.  The amax's own quotient may exceed 448 by an
+// ulp and rounds to 448 without the clamp.  Half of what a tile of this rule takes
+// goes into the quotients, and with Fp32Scale the kernels are bound by them.
+struct Fp32Quotient {
+  static constexpr bool kScaledCvt = false;
+  float s, r;
+  __device__ __forceinline__ explicit Fp32Quotient(uint32_t amax_bits) {
+    s = amax_bits == 0 ? 1.0f : __uint_as_float(amax_bits << 16) / 448.0f;
+    r = 1.0f / s;
+  }
+  __device__ __forceinline__ bool fits() const { return s >= 0x1p-64f && s < INFINITY; }
+  __device__ __forceinline__ float operator()(float x) const {
+    const float y = x * r;
+    return __builtin_fmaf(-__builtin_fmaf(s, y, -x), r, y);
+  }
+};
+
+// f(scale) for the group of this amax: under the amax / 448 rule with the short
+// quotient where the whole wave's groups fit it.  Returns the scale that is stored.
+template <class S, class F>
+__device__ __forceinline__ float with_scale(uint32_t amax_bits, F f) {
+  if constexpr (S::kScaledCvt) {
+    const S sc(amax_bits);
+    f(sc);
+    return sc.s;
+  } else {
+    const Fp32Quotient sc(amax_bits);
+    if (__builtin_amdgcn_ballot_w64(!sc.fits()) == 0) f(sc);
+    else f(S(amax_bits));
+    return sc.s;
+  }
+}
+
+// Eight values of a group of 128 that 16 lanes hold -> their codes and the scale.
+template <class S>
+__device__ __forceinline__ float quant_group(u32x4 v, tile_u32x2& o) {
+  uint32_t m = pk_max_u16(pk_max_u16(abs2(v.x), abs2(v.y)), pk_max_u16(abs2(v.z), abs2(v.w)));
+  m = row16_max(max(m & 0xFFFFu, m >> 16));
+  return with_scale<S>(m, [&](const auto& sc) { o = tile_u32x2{quant4(v.x, v.y, sc), quant4(v.z, v.w, sc)}; });
+}
+
 // Row groups.  q: the tile's first row and the thread's first column; s: the
 // tile's first row and its group; G: groups per row of s.
 template <class S, bool NT = false>
@@ -44,13 +88,10 @@ __device__ __forceinline__ void tile_row_groups(const u32x4 (&v)[8], uint8_t* __
                                                 float* __restrict__ s, uint32_t G, uint32_t rb, uint32_t cb) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    uint32_t m = pk_max_u16(pk_max_u16(abs2(v[i].x), abs2(v[i].y)), pk_max_u16(abs2(v[i].z), abs2(v[i].w)));
-    m = max(m & 0xFFFFu, m >> 16);
-    m = row16_max(m);
-    const S sc(m);
-    store_codes<NT>(q + (int64_t)(rb * 8 + i) * ld_q,
-                    tile_u32x2{quant4(v[i].x, v[i].y, sc), quant4(v[i].z, v[i].w, sc)});
-    if (cb == 0) s[(int64_t)(rb * 8 + i) * G] = sc.s;
+    tile_u32x2 o;
+    const float scale = quant_group<S>(v[i], o);
+    store_codes<NT>(q + (int64_t)(rb * 8 + i) * ld_q, o);
+    if (cb == 0) s[(int64_t)(rb * 8 + i) * G] = scale;
   }
 }
 
@@ -86,26 +127,27 @@ __device__ __forceinline__ void tile_col_groups(const u32x4 (&v)[8], TileLds& ld
     cm[w] = pk_max_u16(pk_max_u16(lds.red[0][cb][w], lds.red[1][cb][w]),
                        pk_max_u16(lds.red[2][cb][w], lds.red[3][cb][w]));
   // column j's amax is half j % 2 of cm[j / 2]
-  const S inv[8] = {S(cm[0] & 0xFFFFu), S(cm[0] >> 16), S(cm[1] & 0xFFFFu), S(cm[1] >> 16),
-                    S(cm[2] & 0xFFFFu), S(cm[2] >> 16), S(cm[3] & 0xFFFFu), S(cm[3] >> 16)};
+  const auto amax = [&](int j) { return j & 1 ? cm[j >> 1] >> 16 : cm[j >> 1] & 0xFFFFu; };
   // The thread's 8x8 codes, one column at a time (rows 0..3 and 4..7 of
   // column j, each with the column's scale: word j / 2 of each row, half
   // j % 2), go through LDS as tq[column][row block], the 8-byte unit
   // XOR-swizzled by the column block cb, and leave as whole 128-byte lines of
   // qT: 8 lanes per column, 16 bytes (two row blocks) each.
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  const auto column = [&](int j, const auto& sc) {
     const int m = j >> 1;
     uint32_t a, b;
     if (j & 1) {
-      a = quant4_col<1>(v[0][m], v[1][m], v[2][m], v[3][m], inv[j]);
-      b = quant4_col<1>(v[4][m], v[5][m], v[6][m], v[7][m], inv[j]);
+      a = quant4_col<1>(v[0][m], v[1][m], v[2][m], v[3][m], sc);
+      b = quant4_col<1>(v[4][m], v[5][m], v[6][m], v[7][m], sc);
     } else {
-      a = quant4_col<0>(v[0][m], v[1][m], v[2][m], v[3][m], inv[j]);
-      b = quant4_col<0>(v[4][m], v[5][m], v[6][m], v[7][m], inv[j]);
+      a = quant4_col<0>(v[0][m], v[1][m], v[2][m], v[3][m], sc);
+      b = quant4_col<0>(v[4][m], v[5][m], v[6][m], v[7][m], sc);
     }
     lds.tq[cb * 8 + j][rb ^ cb] = make_uint2(a, b);
-  }
+  };
+  float scale[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) scale[j] = with_scale<S>(amax(j), [&](const auto& sc) { column(j, sc); });
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -117,7 +159,7 @@ __device__ __forceinline__ void tile_col_groups(const u32x4 (&v)[8], TileLds& ld
   }
   if (rb == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sT[(int64_t)(cb * 8 + j) * G] = inv[j].s;
+    for (int j = 0; j < 8; ++j) sT[(int64_t)(cb * 8 + j) * G] = scale[j];
   }
 }
 

@@ -34,17 +34,6 @@ __device__ __forceinline__ float gated(float g, float u) {
   return g * sigmoid(g) * u;
 }
 
-// Eight bf16 of a group of 128 that 16 lanes hold, quantized.
-template <class S>
-__device__ __forceinline__ S quant_group(u32x4 v, uint2& o) {
-  uint32_t m = pk_max_u16(pk_max_u16(abs2(v.x), abs2(v.y)), pk_max_u16(abs2(v.z), abs2(v.w)));
-  m = row16_max(max(m & 0xFFFFu, m >> 16));
-  const S sc(m);
-  o.x = quant4(v.x, v.y, sc);
-  o.y = quant4(v.z, v.w, sc);
-  return sc;
-}
-
 // ---------------------------------------------------------------------------
 // Forward: 16 lanes to a group of 128 columns of g and of u, and of h.
 // ---------------------------------------------------------------------------
@@ -77,24 +66,24 @@ __global__ __launch_bounds__(kThreads) void gated_forward_kernel(int64_t M, uint
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       h[j] = bf16x2_rne(gated(bf16_lo(g[i][j]), bf16_lo(u[i][j])), gated(bf16_hi(g[i][j]), bf16_hi(u[i][j])));
-    uint2 oh, og, ou;
-    const S sh = quant_group<S>(h, oh);
+    u32x2 oh, og, ou;
+    const float sh = quant_group<S>(h, oh);
     const bool live = g0 + i * 4 + sub < total;
     const int64_t r = row[i];
     const int64_t c = grp[i] * 128 + l16 * 8;
     if (live) {
-      *reinterpret_cast<uint2*>(q.q + r * q.ld + c) = oh;
-      if (l16 == 0) q.s[r * G + grp[i]] = sh.s;
+      *reinterpret_cast<u32x2*>(q.q + r * q.ld + c) = oh;
+      if (l16 == 0) q.s[r * G + grp[i]] = sh;
     }
     if constexpr (KEEP) {
-      const S sg = quant_group<S>(g[i], og);
-      const S su = quant_group<S>(u[i], ou);
+      const float sg = quant_group<S>(g[i], og);
+      const float su = quant_group<S>(u[i], ou);
       if (live) {
-        *reinterpret_cast<uint2*>(qc.q + r * qc.ld + c) = og;
-        *reinterpret_cast<uint2*>(qc.q + r * qc.ld + I + c) = ou;
+        *reinterpret_cast<u32x2*>(qc.q + r * qc.ld + c) = og;
+        *reinterpret_cast<u32x2*>(qc.q + r * qc.ld + I + c) = ou;
         if (l16 == 0) {
-          qc.s[r * 2 * G + grp[i]] = sg.s;
-          qc.s[r * 2 * G + G + grp[i]] = su.s;
+          qc.s[r * 2 * G + grp[i]] = sg;
+          qc.s[r * 2 * G + G + grp[i]] = su;
         }
       }
     }

@@ -143,12 +143,11 @@ __global__ __launch_bounds__(kThreads) void gather_rows_kernel(GatherArgs a, uin
     for (int u = 0; u < kRowSteps; ++u) {
       u32x4 x = v[u];
       if constexpr (W) x = u32x4{scaled2(x.x, wt), scaled2(x.y, wt), scaled2(x.z, wt), scaled2(x.w, wt)};
-      uint32_t m = pk_max_u16(pk_max_u16(abs2(x.x), abs2(x.y)), pk_max_u16(abs2(x.z), abs2(x.w)));
-      m = row16_max(max(m & 0xFFFFu, m >> 16));
-      const S sc(m);
+      tile_u32x2 o;
+      const float scale = quant_group<S>(x, o);
       if (c0 + u * 512 < a.H) {
-        store_codes<NT>(q + c0 + u * 512, tile_u32x2{quant4(x.x, x.y, sc), quant4(x.z, x.w, sc)});
-        if (l16 == 0) s[(c0 + u * 512) >> 7] = sc.s;
+        store_codes<NT>(q + c0 + u * 512, o);
+        if (l16 == 0) s[(c0 + u * 512) >> 7] = scale;
       }
       v[u] = w[u];
     }

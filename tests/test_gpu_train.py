@@ -174,6 +174,60 @@ def test_gather_in_the_order_of_tokens(T, E, k, H, part, weighted, mode):
     expect_rows(q, s, train_ref.gathered(bits, source, k, w), mode, used)
 
 
+def groups_of_every_quotient():
+    """bf16 bits [groups, 128]: for each mantissa of the amax, elements of every mantissa and sign in 20 octaves below it
+    (the quotient's rounding depends on the mantissas alone), and for every exponent of the amax some of them."""
+    rows = []
+    for m in range(128):
+        top = (127 << 7) | m
+        rest = np.arange(top - 20 * 128, top + 1)
+        rest = np.concatenate([rest, rest | 0x8000, [0, 0x8000]])
+        rest = np.concatenate([rest, np.zeros(-rest.size % 127, rest.dtype)]).reshape(-1, 127)
+        rows.append(np.concatenate([np.full((rest.shape[0], 1), top), rest], 1))
+    rng = synth.rng_for(38)
+    top = np.arange(0, 0x7F80, 37)
+    rest = np.maximum(top[:, None] - rng.integers(0, 2500, (top.size, 127)), 0) | (rng.integers(0, 2, (top.size, 127)) << 15)
+    rows.append(np.concatenate([top[:, None], rest], 1))
+    return np.concatenate(rows).astype(np.uint16)
+
+
+def test_short_quotient_gives_the_rule():
+    """The amax / 448 codes of the kernels that take the short quotient (both forms of the gather, the gated unit's
+    checkpoint) are the oracle's for every mantissa of the amax and the element."""
+    x = groups_of_every_quotient()
+    x = np.concatenate([x, np.zeros((-len(x) % 128, 128), np.uint16)])
+    n = len(x)
+    xt, source = dev_bf16(x), dev(np.arange(n, dtype=np.int32))
+    q, s = fb.fp8_moe_gather(xt, source, 1, scale_mode=FP32)
+    expect_rows(q, s, x, FP32, n)
+    q, s, qT, sT = fb.fp8_moe_gather(xt, source, 1, transpose=True, scale_mode=FP32)
+    expect_rows(q, s, x, FP32, n)
+    expect_cols(qT, sT, x, FP32, n)
+    across = np.ascontiguousarray(x.T)          # the groups down the columns of one block
+    q, s, qT, sT = fb.fp8_moe_gather(dev_bf16(across), dev(np.arange(128, dtype=np.int32)), 1, transpose=True, scale_mode=FP32)
+    expect_rows(q, s, across, FP32, 128)
+    expect_cols(qT, sT, across, FP32, 128)
+    gu = np.concatenate([x, x[::-1]], 1)
+    _, _, qc, sc = fb.fp8_gated_forward(dev_bf16(gu), scale_mode=FP32)
+    expect_rows(qc, sc, gu, FP32, n)
+
+
+@MODES
+def test_values_that_are_not_finite(mode):
+    """Codes and scales of the library's own quantizers, NaN and infinities in some groups and none in others."""
+    import torch
+    x = f64(activations(256, 384, 90)[0])
+    x[3, 5], x[40, 200], x[41, 300], x[130:140, 7] = np.nan, np.inf, -np.inf, np.nan
+    xt = torch.from_numpy(x.astype(np.float32)).cuda().bfloat16()
+    want = fb.fp8_quantize_rowgroup(xt, scale_mode=mode) + fb.fp8_quantize_colgroup(xt, scale_mode=mode)
+    source = dev(np.arange(256, dtype=np.int32))
+    got = fb.fp8_moe_gather(xt, source, 1, transpose=True, scale_mode=mode)
+    assert all(torch.equal(g.view(torch.uint8) if g.dtype is torch.uint8 else g.view(torch.int32),
+                           w.view(torch.uint8) if w.dtype is torch.uint8 else w.view(torch.int32)) for g, w in zip(got, want))
+    one = fb.fp8_moe_gather(xt, source, 1, scale_mode=mode)
+    assert torch.equal(one[0], want[0]) and torch.equal(one[1].view(torch.int32), want[1].view(torch.int32))
+
+
 # ------------------------------------------------------------------ combine --
 
 def combine_case(T, E, k, H, ld=None):
