@@ -203,7 +203,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void gated_backward_kernel(GatedBa
 }
 
 template <class S, bool NT>
-__global__ __launch_bounds__(kTileThreads) void requantize_kernel(const uint8_t* __restrict__ q, int64_t rows,
+__global__ __launch_bounds__(kTileThreads, 8) void requantize_kernel(const uint8_t* __restrict__ q, int64_t rows,
                                                                   int64_t ld_q, const float* __restrict__ s,
                                                                   const int32_t* __restrict__ used, CodesOut qT,
                                                                   TileGrid grid) {
