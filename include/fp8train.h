@@ -34,9 +34,9 @@
  * outside [0, rows] counts as the nearer end.  Where groups of 128 rows are
  * quantized, or rows are multiplied, it is rounded up to a multiple of 128.
  *
- * Values that are not finite go through as in the quantizers of fp8blk.h: a
- * group with a NaN or an infinity has its scale from that value and NaN at its
- * place.
+ * Values that are not finite: a group of 128 with a NaN or an infinity has the
+ * codes and the scale that the quantizers of fp8blk.h give it, and leaves the
+ * other groups as they are.
  */
 #ifndef FP8TRAIN_H
 #define FP8TRAIN_H
@@ -171,8 +171,7 @@ int fp8_gated_forward(int64_t M, int64_t I, const uint16_t *gu, int64_t ld_gu, c
 
 /*
  * The gated unit's gradient from the checkpoint: with g and u what its codes
- * stand for (rounded to bf16, which only scales that are no powers of two need)
- * and sig = 1 / (1 + e^-g),
+ * stand for (rounded to bf16 where the scales are amax / 448) and sig = 1 / (1 + e^-g),
  *   du = dh g sig,  dg = dh u sig (1 + g (1 - sig)),
  * each rounded to bf16 once and quantized in both orientations, and h =
  * bf16(g sig u) once more, in the orientation that the second linear's Wgrad
