@@ -206,8 +206,9 @@ __device__ __forceinline__ void tile_of(uint32_t bid, uint32_t col_tiles, bool b
 
 // The same order for any shape, with workgroups that find no tile (rt or ct past
 // the end): blocks that the shape fills in part, and up to 7 whole ones.  Taken
-// where at least kTileSomeBlocks blocks make those few.
-constexpr uint32_t kTileSomeBlocks = 96;
+// where at least kTileSomeBlocks blocks make those few, and a launch of all of them
+// stays below 2^32 threads.
+constexpr uint32_t kTileSomeBlocks = 96, kTileMostBlocks = 1 << 16;
 struct TileGrid {
   uint32_t row_tiles, col_tiles;
   bool blocked;
@@ -217,7 +218,7 @@ inline TileGrid tile_grid(int64_t rows, int64_t cols) {
   TileGrid g{(uint32_t)(rows / 128), (uint32_t)(cols / 128), false, 0};
   const uint32_t blocks = (g.row_tiles + kTileBlockRows - 1) / kTileBlockRows *
                           ((g.col_tiles + kTileBlockCols - 1) / kTileBlockCols);
-  g.blocked = blocks >= kTileSomeBlocks && g.col_tiles >= kTileBlockCols / 2;
+  g.blocked = blocks >= kTileSomeBlocks && blocks <= kTileMostBlocks && g.col_tiles >= kTileBlockCols / 2;
   g.workgroups = g.blocked ? (blocks + 7) / 8 * 8 * kTileBlockCols * kTileBlockRows : g.row_tiles * g.col_tiles;
   return g;
 }
