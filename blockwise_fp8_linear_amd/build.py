@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8blk.so")
-SOURCES = ["quant.hip", "gemm.hip", "gemm_mx.hip", "scratch.hip", "rows.hip", "route.hip", "moe.hip", "sort.hip",
+SOURCES = ["quant.hip", "gemm.hip", "gemm_mx.hip", "grouped_wgrad.hip", "scratch.hip", "rows.hip", "route.hip", "moe.hip", "sort.hip",
            "sorted.hip", "gated.hip", "plan.cpp", "api.cpp", "api_moe.cpp", "api_train.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

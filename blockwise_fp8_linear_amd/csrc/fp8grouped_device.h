@@ -116,40 +116,6 @@ __device__ __forceinline__ TileAt tile_at(uint32_t in, uint32_t tiles_m, uint32_
   return {first + (rest - n * size), n};
 }
 
-// The expert whose segment is the at-th longest, equal ones by index: every thread
-// of a workgroup calls it (which ends with a barrier).  Each counts the experts
-// before its own, four a step, so it is for a few hundred at most.
-constexpr int kGroupedOrderE = 256;
-struct GroupedOrder {
-  __attribute__((aligned(16))) int32_t length[kGroupedOrderE];  // of each expert's segment; behind the last one -1
-  int found;
-  Segment segment;
-};
-__device__ __forceinline__ int expert_by_load(GroupedOrder& lds, const int32_t* __restrict__ offsets, int E,
-                                              int32_t rows, int at, Segment& s) {
-  typedef int v4i __attribute__((ext_vector_type(4)));
-  const int e = threadIdx.x;
-  const Segment mine = e < E ? segment_of(offsets, e, rows) : Segment{0, -1};
-  if (e < kGroupedOrderE) lds.length[e] = mine.length;
-  __syncthreads();
-  if (e < E) {
-    int before = 0;
-#pragma unroll 8
-    for (int o = 0; o < E; o += 4) {
-      const v4i l = *reinterpret_cast<const v4i*>(lds.length + o);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) before += l[i] > mine.length || (l[i] == mine.length && o + i < e) ? 1 : 0;
-    }
-    if (before == at) {
-      lds.found = e;
-      lds.segment = mine;
-    }
-  }
-  __syncthreads();
-  s = Segment{__builtin_amdgcn_readfirstlane(lds.segment.first), __builtin_amdgcn_readfirstlane(lds.segment.length)};
-  return __builtin_amdgcn_readfirstlane(lds.found);
-}
-
 // Output element i of a matrix of fp32 or bf16.
 __device__ __forceinline__ void* element(void* out, int64_t i, bool f32) {
   return f32 ? (void*)(static_cast<float*>(out) + i) : (void*)(static_cast<uint16_t*>(out) + i);

@@ -89,10 +89,11 @@ struct GroupedArgs {
 };
 hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);   // Fprop, Dgrad
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);
-// All three on the 256x256 block-scaled-MFMA kernels (gemm_mx.hip): Fprop and
-// Dgrad up to kMxMaxKb 128-blocks of reduction and 2^22 columns, Wgrad up to 2^22
-// rows.
-hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream);
+// On the block-scaled MFMA, tiles of 256x256: Fprop and Dgrad (gemm_mx.hip) up to
+// kMxMaxKb 128-blocks of reduction and 2^22 columns, Wgrad (grouped_wgrad.hip) up to
+// 2^22 rows.
+hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream);
+hipError_t launch_grouped_wgrad_mx(const GroupedArgs& a, hipStream_t stream);
 int64_t grouped_mx_tiles(const GroupedArgs& a);  // tiles of Fprop or Dgrad, whatever the segments
 
 }  // namespace fp8blk

@@ -701,15 +701,17 @@ hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t 
   // the weight-block scales of a reduction sit in LDS; per-lane 32-bit offsets of
   // 128 rows; at most a workgroup a tile, of a launch below 2^32 threads
   if (!promote && a.g.R <= kMxMaxKb * 128 && a.g.J <= (int64_t(1) << 22) && grouped_mx_tiles(a) < (1 << 24))
-    return launch_grouped_mx(a, stream);
+    return launch_grouped_rows_mx(a, stream);
   if (a.g.bt)
     return promote ? launch_grouped_rows_cfg<PromoteBlockBT>(a, stream) : launch_grouped_rows_cfg<ScaledBlockBT>(a, stream);
   return promote ? launch_grouped_rows_cfg<PromoteBlock>(a, stream) : launch_grouped_rows_cfg<ScaledBlock>(a, stream);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
-  // per-lane 32-bit offsets: 256 rows of R bytes
-  if (algo == GemmAlgo::ScaledMfma && a.g.R <= (int64_t(1) << 22)) return launch_grouped_mx(a, stream);
+  // per-lane 32-bit offsets: 256 rows of R bytes; scales in 16-byte groups of four
+  const auto quads = [](const float* s) { return reinterpret_cast<uintptr_t>(s) % 16 == 0; };
+  if (algo == GemmAlgo::ScaledMfma && a.g.R <= (int64_t(1) << 22) && a.g.R % 512 == 0 && quads(a.g.sa) && quads(a.g.sb))
+    return launch_grouped_wgrad_mx(a, stream);
   return algo == GemmAlgo::Promote ? launch_grouped_wgrad_cfg<PromoteRow>(a, stream)
                                    : launch_grouped_wgrad_cfg<ScaledRow>(a, stream);
 }

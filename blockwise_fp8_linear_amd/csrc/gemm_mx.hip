@@ -135,7 +135,7 @@ template <bool BROW, bool BT = false, bool RAGGED = false, int TM = fp8blk::TM>
 __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int64_t i0, int64_t j0, int64_t kb_begin,
                                             int64_t nkb_seg, v16f (&acc)[TM][TN]) {
   static_assert(!(BT && BROW), "the transposed-B layout is Dgrad's, with weight-block scales");
-  static_assert(!BROW || TM == fp8blk::TM, "a tile of 128 rows has no room for B's row scales");
+  static_assert(!BROW || (TM == fp8blk::TM && !RAGGED), "row scales of B: whole groups, tiles of 256 rows");
   typedef Ring<TM> Rg;
   constexpr int LOADS_A = Rg::LOADS_A, LOADS_PER_PAIR = LOADS_A + LOADS_B, WM = 32 * TM;
   constexpr int SLOTS = Rg::SLOTS, A_SLOT = Rg::A, SLOT = Rg::SLOT, SC_BYTES = Rg::SC;
@@ -227,7 +227,6 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
       for (int i = 0; i < 4; ++i) {
         const int k = 4 * q + i < npair ? 4 * q + i : npair - 1;
         dma4(baseSA + 4 * k, offSA, buf + i * 4 * Rg::ROWS + wave * 256);
-        if constexpr (BROW) dma4(baseSB + 4 * k, offSB, buf + 4096 + i * 1024 + wave * 256);
       }
       return;
     }
@@ -588,17 +587,6 @@ __device__ __forceinline__ void store_tile(const Dst& d, uint8_t* lds, int64_t i
   store_tile_from<BATCH, TM>(d, lds, i0, j0, [&](int a, int b) { return acc[a][b]; });
 }
 
-// A tile of zeros; what accumulates stays as it is.
-__device__ __forceinline__ void zero_tile(const Dst& d, int64_t i0, int64_t j0) {
-  if (d.acc) return;
-  const int64_t bytes = d.f32 ? 4 : 2, per = 16 / bytes, cols = d.cols - j0 < BN ? d.cols - j0 : BN;
-  const int64_t rows = d.rows - i0 < BM ? d.rows - i0 : BM;
-  for (int64_t k = threadIdx.x; k < rows * (cols / per); k += THREADS) {
-    const int64_t i = i0 + k / (cols / per), j = j0 + k % (cols / per) * per;
-    *reinterpret_cast<u32x4*>(static_cast<char*>(d.out) + (i * d.ld + j) * bytes) = u32x4{0, 0, 0, 0};
-  }
-}
-
 // One output tile per workgroup, the whole reduction (Fprop and Dgrad; BT:
 // Dgrad from the weight codes as quantized).
 template <bool BROW, bool BT = false>
@@ -887,37 +875,6 @@ __global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a,
   }
 }
 
-// Every expert's Wgrad, its reduction over its own segment alone: a tile a
-// workgroup.  The segments differ in length.  So that no XCD gets the long ones
-// and the last tiles to start are short, the experts come in the order of their
-// loads, and their tiles in runs of WG_RUN (an XCD's 32 CUs share the panels of one
-// run in L2), dealt to the XCDs back and forth.
-constexpr uint32_t WG_RUN = 32;
-
-__global__ __launch_bounds__(THREADS) void grouped_mx_wgrad_kernel(GroupedArgs a, uint32_t tiles_m, uint32_t tiles_n) {
-  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  __shared__ GroupedOrder order;
-  const uint32_t xcd = blockIdx.x % 8, in = blockIdx.x / 8, turn = in / WG_RUN;
-  const uint32_t t = (turn * 8 + (turn & 1 ? 7 - xcd : xcd)) * WG_RUN + in % WG_RUN;
-  const uint32_t tiles = tiles_m * tiles_n, nth = t / tiles;
-  if (nth >= a.E) return;
-  static_assert(THREADS >= kGroupedOrderE, "a thread per expert");
-  int e = (int)nth;
-  Segment s;
-  if (a.E <= kGroupedOrderE) e = expert_by_load(order, a.offsets, (int)a.E, (int32_t)a.g.R, (int)nth, s);
-  else s = segment_of(a.offsets, e, (int32_t)a.g.R);
-  const TileAt at = tile_at<4>(t - nth * tiles, tiles_m, tiles_n);
-  const int64_t i0 = (int64_t)at.m * BM, j0 = (int64_t)at.n * BN;
-  const Dst d{element(a.g.out, e * a.out_stride, a.g.out_f32), a.g.J, a.g.I, a.g.J, a.g.out_f32, a.g.accumulate};
-  if (s.length == 0) {
-    zero_tile(d, i0, j0);
-    return;
-  }
-  v16f acc[TM][TN];
-  mma_segment<true, false, true>(a.g, lds, i0, j0, s.first / 128, s.length / 128, acc);
-  store_tile<8>(d, lds, i0, j0, acc);
-}
-
 template <class K>
 hipError_t set_lds_attr(K* kernel, std::atomic<uint64_t>* done) {
   return ensure_lds_limit(reinterpret_cast<const void*>(kernel), LDS_BYTES, done);
@@ -966,7 +923,7 @@ hipError_t launch_bwd(const GemmArgs& gd, const GemmArgs& gw, float* ws, hipStre
 }
 
 template <bool BT, bool RAGGED>
-hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream) {
+hipError_t launch_grouped_rows_as(const GroupedArgs& a, hipStream_t stream) {
   // in halves there are at most 2 kSkGrid
   const int64_t tiles_n = (a.g.J + BN - 1) / BN, tiles = grouped_mx_tiles(a);
   const int64_t most = !RAGGED ? kSkGrid : tiles > 2 * kSkGrid ? (tiles + 7) / 8 * 8 : 2 * kSkGrid;
@@ -983,19 +940,10 @@ hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream) {
 
 int64_t grouped_mx_tiles(const GroupedArgs& a) { return (a.g.I / BM + a.E) * ((a.g.J + BN - 1) / BN); }
 
-hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream) {
-  if (a.g.bmode == BScale::Block) {
-    if (gemm_mx_eligible(a.g))  // whole groups of four 128-blocks, their scales 16-byte aligned
-      return a.g.bt ? launch_grouped_rows_mx<true, false>(a, stream) : launch_grouped_rows_mx<false, false>(a, stream);
-    return a.g.bt ? launch_grouped_rows_mx<true, true>(a, stream) : launch_grouped_rows_mx<false, true>(a, stream);
-  }
-  const int64_t tiles_m = (a.g.I + BM - 1) / BM, tiles_n = (a.g.J + BN - 1) / BN;
-  const int64_t turns = (a.E * tiles_m * tiles_n + 8 * WG_RUN - 1) / (8 * WG_RUN);
-  static std::atomic<uint64_t> attr_set{0};
-  if (hipError_t e = set_lds_attr(&grouped_mx_wgrad_kernel, &attr_set)) return e;
-  hipLaunchKernelGGL(grouped_mx_wgrad_kernel, dim3((uint32_t)(turns * 8 * WG_RUN)), dim3(THREADS), LDS_BYTES, stream, a,
-                     (uint32_t)tiles_m, (uint32_t)tiles_n);
-  return hipGetLastError();
+hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream) {
+  if (gemm_mx_eligible(a.g))  // whole groups of four 128-blocks, their scales 16-byte aligned
+    return a.g.bt ? launch_grouped_rows_as<true, false>(a, stream) : launch_grouped_rows_as<false, false>(a, stream);
+  return a.g.bt ? launch_grouped_rows_as<true, true>(a, stream) : launch_grouped_rows_as<false, true>(a, stream);
 }
 
 hipError_t launch_gemm_mx(const GemmArgs& g, hipStream_t stream) {
