@@ -432,7 +432,7 @@ hipError_t launch_grouped_wgrad_mx(const GroupedArgs& a, hipStream_t stream) {
   // As many tiles a workgroup as leave the fewest rounds of the GPU's CUs, up to
   // kMostEach: a workgroup with one of the longest segments then still starts early,
   // and others take what it leaves.
-  constexpr int64_t kMostEach = 4, kWhole = 8 * RUN;
+  constexpr int64_t kMostEach = 8, kWhole = 8 * RUN;
   int64_t each = 1, best = INT64_MAX;
   for (int64_t n = 1; n <= kMostEach; ++n) {
     const int64_t rounds = ((tiles + n - 1) / n + kSkGrid - 1) / kSkGrid * n;

@@ -5,6 +5,7 @@ the header is C, and the binding refuses operands that disagree with the sizes i
 would pass."""
 import ctypes
 import os
+import re
 import shutil
 import subprocess
 
@@ -307,3 +308,19 @@ def test_host_checks_under_sanitizers(tmp_path):
                     os.path.join(csrc, "api_train.cpp"), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout[-4000:] + r.stderr[-4000:]
+
+
+def test_grouped_wgrad_uses_no_scratch(tmp_path):
+    """grouped_wgrad.hip counts on its registers: a spill would go through memory beside its direct loads."""
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    if not os.path.exists(hipcc) and shutil.which("hipcc") is None:
+        pytest.skip("no hipcc")
+    out = str(tmp_path / "grouped_wgrad.s")
+    subprocess.run([hipcc, "--offload-arch=gfx950", "-O3", "-std=c++17", "-Wno-inline-asm", "-Wno-unused-function",
+                    "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-I", os.path.join(ROOT, "include"),
+                    "--cuda-device-only", "-S", "-o", out,
+                    os.path.join(ROOT, "blockwise_fp8_linear_amd", "csrc", "grouped_wgrad.hip")],
+                   check=True, capture_output=True, text=True)
+    text = open(out).read()
+    sizes = re.findall(r"\.private_segment_fixed_size:\s+(\d+)", text)
+    assert sizes and all(int(s) == 0 for s in sizes) and "scratch_" not in text
