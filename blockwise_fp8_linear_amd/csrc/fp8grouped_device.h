@@ -11,7 +11,7 @@
 namespace fp8blk {
 
 constexpr int kGroupedMaxE = 1024;
-// Rows of a grouped product: below it an expert has at most 2^21 row tiles, and
+// Rows of a grouped product: below it an expert has fewer than 2^22 row tiles, and
 // 1024 of them, whatever the offsets hold, fewer than 2^32.
 constexpr int64_t kGroupedMaxRows = int64_t(1) << 29;
 

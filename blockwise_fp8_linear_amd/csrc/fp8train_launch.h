@@ -89,11 +89,33 @@ struct GroupedArgs {
 };
 hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);   // Fprop, Dgrad
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream);
-// On the block-scaled MFMA, tiles of 256x256: Fprop and Dgrad (gemm_mx.hip) up to
-// kMxMaxKb 128-blocks of reduction and 2^22 columns, Wgrad (grouped_wgrad.hip) up to
-// 2^22 rows.
+// On the block-scaled MFMA, tiles of 256x256: Fprop and Dgrad (gemm_mx.hip) where
+// gemm_mx_eligible and up to 2^22 columns; Wgrad (grouped_wgrad.hip) up to 2^22 rows,
+// whole groups of four 128-blocks, their scales 16-byte aligned.
 hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream);
 hipError_t launch_grouped_wgrad_mx(const GroupedArgs& a, hipStream_t stream);
-int64_t grouped_mx_tiles(const GroupedArgs& a);  // tiles of Fprop or Dgrad, whatever the segments
+
+// Wgrad's times on the two kernels, in quarters of a us, if every segment is as long
+// as the mean one, of b blocks.  On tiles of 256 x 256, one workgroup a CU: a tile takes
+// 2 b + 4.5 us, a workgroup 5 until its first loads are there; each: the tiles a
+// workgroup takes, those that end first, up to kWgradEach, so that what the longest
+// segments leave is taken by others (16 measured the same).  On tiles of 128 x 128 (in
+// gemm.hip), two a CU: 3 + 1.25 b us for both.  (294 rows of 11 experts, 1280 x 1152:
+// 16.7 us on the large tiles, 10.7 on the small ones; 2400 of 64, 2048 x 2048: 120 and
+// 133; 65536 of 64: 372 and 530.)
+constexpr int64_t kWgradEach = 8;
+struct WgradPlan {
+  int64_t each, large, small;
+};
+inline WgradPlan wgrad_plan(const GroupedArgs& a) {
+  const int64_t cus = 256, tile = 8 * (a.g.R / 128) / a.E + 18;
+  const int64_t tiles = a.E * ((a.g.I + 255) / 256) * ((a.g.J + 255) / 256), tiles128 = a.E * (a.g.I / 128) * (a.g.J / 128);
+  WgradPlan p{1, INT64_MAX, (tiles128 + 2 * cus - 1) / (2 * cus) * (12 + 5 * (a.g.R / 128) / a.E)};
+  for (int64_t n = 1; n <= kWgradEach; ++n) {
+    const int64_t rounds = ((tiles + n - 1) / n + cus - 1) / cus, time = rounds * (n * tile + 20);
+    if (time <= p.large) p.large = time, p.each = n;
+  }
+  return p;
+}
 
 }  // namespace fp8blk

@@ -38,7 +38,7 @@
 // that each lane ends up holding 4 consecutive output columns of one row,
 // which makes the scale a single value per lane (per row) for the weight
 // block case and the epilogue a row-contiguous 8- or 16-byte store.
-// Scales of a chunk of up to kChunk reduction blocks are staged in LDS, as
+// Scales of a chunk of up to CHUNK reduction blocks are staged in LDS, as
 // fp32 values (PROMOTE) or E8M0 bytes (the scaled MFMA).
 #include <type_traits>
 
@@ -51,15 +51,16 @@ namespace fp8blk {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 
-constexpr int kChunk = 32;  // reduction blocks whose scales sit in LDS at once
-
 // BT_: B stored [R][J] (Dgrad from the weight codes as quantized): the B
 // tile is staged as 128 reduction rows of BN bytes and its fragments come
 // from LDS transpose reads.
 // STAGES_: blocks in LDS at once; beyond two, STAGES_ - 1 are on the way, for tiles
 // that are small beside the time a load takes.
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool PROMOTE_, bool BROW_, bool BT_ = false, int STAGES_ = 2>
+// CHUNK_: reduction blocks whose scales sit in LDS at once.
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool PROMOTE_, bool BROW_, bool BT_ = false, int STAGES_ = 2,
+          int CHUNK_ = 32>
 struct Cfg {
+  static constexpr int CHUNK = CHUNK_;
   static constexpr int BM = BM_, BN = BN_, STAGES = STAGES_;
   static constexpr bool BT = BT_;
   static_assert(!BT_ || (!BROW_ && BN_ == 128), "transposed B: Dgrad's weight-block layout, 128-byte rows");
@@ -72,8 +73,8 @@ struct Cfg {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   // one staged scale: fp32 for PROMOTE, its E8M0 byte for the scaled MFMA
   using SType = typename std::conditional<PROMOTE_, float, uint8_t>::type;
-  static constexpr int SA_BYTES = kChunk * BM * (int)sizeof(SType);
-  static constexpr int SB_BYTES = (BROW ? kChunk * BN : kChunk * (BN / 128 > 0 ? BN / 128 : 1)) * (int)sizeof(SType);
+  static constexpr int SA_BYTES = CHUNK * BM * (int)sizeof(SType);
+  static constexpr int SB_BYTES = (BROW ? CHUNK * BN : CHUNK * (BN / 128 > 0 ? BN / 128 : 1)) * (int)sizeof(SType);
   static constexpr int LDS = STAGES * STAGE + SA_BYTES + ((SB_BYTES + 15) / 16) * 16;
   static_assert(A_BYTES % (1024 * (THREADS / 64)) == 0 && B_BYTES % (1024 * (THREADS / 64)) == 0,
                 "whole KiB of direct loads per wave");
@@ -225,7 +226,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
   // scaled MFMA wants [kbl][j % 16][j / 16]; block-mode B: [kbl][j / 128].
   auto load_scales = [&](int64_t kb0, int64_t n) {
     const int64_t nkb_all = nkb;
-    for (uint32_t idx = tid; idx < (uint32_t)(C::BM * kChunk); idx += C::THREADS) {
+    for (uint32_t idx = tid; idx < (uint32_t)(C::BM * C::CHUNK); idx += C::THREADS) {
       const uint32_t i = idx % C::BM, kbl = idx / C::BM;
       if (kbl < n) {
         int64_t row = i0 + i;
@@ -234,7 +235,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
       }
     }
     if constexpr (C::BROW) {
-      for (uint32_t idx = tid; idx < (uint32_t)(C::BN * kChunk); idx += C::THREADS) {
+      for (uint32_t idx = tid; idx < (uint32_t)(C::BN * C::CHUNK); idx += C::THREADS) {
         const uint32_t j = idx % C::BN, kbl = idx / C::BN;
         if (kbl < n) {
           int64_t row = j0 + j;
@@ -245,7 +246,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
       }
     } else {
       constexpr int NB = C::BN / 128;
-      for (uint32_t idx = tid; idx < (uint32_t)(NB * kChunk); idx += C::THREADS) {
+      for (uint32_t idx = tid; idx < (uint32_t)(NB * C::CHUNK); idx += C::THREADS) {
         const uint32_t jb = idx % NB, kbl = idx / NB;
         if (kbl < n) {
           int64_t jblk = (j0 >> 7) + jb;
@@ -275,7 +276,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
 #pragma unroll
       for (int s = 1; s < C::STAGES - 1; ++s) dma_ahead(kb_begin + s);
     }
-    load_scales(kb_begin, (kb_end - kb_begin) < kChunk ? (kb_end - kb_begin) : kChunk);
+    load_scales(kb_begin, (kb_end - kb_begin) < C::CHUNK ? (kb_end - kb_begin) : C::CHUNK);
     wait_vmcnt<C::STAGES == 2 ? 0 : (C::STAGES - 2) * PER_BLOCK>();
     __syncthreads();
   }
@@ -288,7 +289,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
 
     const uint8_t* ta = tiles + cur * C::STAGE;
     const uint8_t* tb = ta + C::A_BYTES;
-    const uint32_t kbl = (uint32_t)((kb - kb_begin) % kChunk);
+    const uint32_t kbl = (uint32_t)((kb - kb_begin) % C::CHUNK);
 
     // B fragments (the instruction's A operand) for the wave's TN sub-tiles
     v8i bf[C::TN];
@@ -409,10 +410,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
       }
     }
 
-    if (more && (kb + 1 - kb_begin) % kChunk == 0) {
+    if (more && (kb + 1 - kb_begin) % C::CHUNK == 0) {
       __syncthreads();  // everyone is done with this chunk's scales
       const int64_t rest = kb_end - (kb + 1);
-      load_scales(kb + 1, rest < kChunk ? rest : kChunk);
+      load_scales(kb + 1, rest < C::CHUNK ? rest : C::CHUNK);
     }
     // this wave's loads of block kb+1 have landed
     if constexpr (C::STAGES > 2) wait_vmcnt<(C::STAGES - 2) * PER_BLOCK>();
@@ -573,11 +574,70 @@ __global__ __launch_bounds__(256) void gk_fixup_kernel(GemmArgs g, SkGeom sg, co
   }
 }
 
+// Store a tile of the experts' products: through the wave's share of the ring, so
+// that whole lines leave, past the caches.  (Straight from the accumulators, 8 bytes
+// of each of 16 rows a lane: 414 rows of 52 experts, Wgrad of 896 x 3328, 147 us.)
+// The unit of 4 columns is XORed with the row (bf16: pair of rows), which spreads
+// writes and reads over the banks.  The caller passes a barrier before the ring is
+// filled again.
+template <class C>
+__device__ __forceinline__ void gk_store_rows(const v4f (&acc)[C::TM][C::TN], uint8_t* lds, void* out, const GemmArgs& g,
+                                              int64_t i0, int64_t j0) {
+  static_assert(C::WN == 64 && C::WM * 256 <= C::STAGES * C::STAGE / (C::THREADS / 64), "a wave's rows of fp32");
+  uint32_t lane = threadIdx.x & 63;
+  int64_t ld = g.J;
+  asm volatile("" : "+v"(lane), "+s"(ld));  // no address is to stay in registers from one tile to the next
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, g4 = lane >> 4;
+  uint8_t* const staging = lds + wave * (C::STAGES * C::STAGE / (C::THREADS / 64));
+  const int64_t row0 = i0 + (wave / C::WAVES_N) * C::WM, col0 = j0 + (wave % C::WAVES_N) * C::WN;
+  const int64_t rows = g.I - row0;  // (128 columns are all in)
+  if (!g.out_f32) {
+#pragma unroll
+    for (int ms = 0; ms < C::TM; ++ms)
+#pragma unroll
+      for (int ns = 0; ns < C::TN; ++ns) {
+        const v4f v = acc[ms][ns];
+        const uint32_t row = ms * 16 + l16;
+        *reinterpret_cast<uint2*>(staging + row * 128 + ((ns * 4 + g4) ^ ((row >> 1) & 15)) * 8) =
+            make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+      }
+    const uint32_t k = lane & 7;
+    uint16_t* const p = static_cast<uint16_t*>(out) + row0 * ld + col0 + 8 * k;
+#pragma unroll
+    for (int s = 0; s < C::WM / 8; ++s) {
+      const uint32_t row = 8 * s + (lane >> 3), pu = (2 * k) ^ ((row >> 1) & 15);
+      u32x4 o = *reinterpret_cast<const u32x4*>(staging + row * 128 + (pu & ~1u) * 8);
+      if (pu & 1) o = u32x4{o[2], o[3], o[0], o[1]};  // the pair is stored swapped
+      if (row < rows) __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p + row * ld));
+    }
+  } else {
+#pragma unroll
+    for (int ms = 0; ms < C::TM; ++ms)
+#pragma unroll
+      for (int ns = 0; ns < C::TN; ++ns)
+        *reinterpret_cast<v4f*>(staging + (ms * 16 + l16) * 256 + ((ns * 4 + g4) ^ l16) * 16) = acc[ms][ns];
+    const uint32_t k = lane & 15;
+    float* const p = static_cast<float*>(out) + row0 * ld + col0 + 4 * k;
+#pragma unroll
+    for (int s = 0; s < C::WM / 4; ++s) {
+      const uint32_t row = 4 * s + (lane >> 4);
+      v4f o = *reinterpret_cast<const v4f*>(staging + row * 256 + (k ^ (row & 15)) * 16);
+      if (row >= rows) continue;
+      v4f* const dst = reinterpret_cast<v4f*>(p + row * ld);
+      if (g.accumulate) {
+        const v4f was = *dst;
+        o = v4f{was[0] + o[0], was[1] + o[1], was[2] + o[2], was[3] + o[3]};
+      }
+      __builtin_nontemporal_store(o, dst);
+    }
+  }
+}
+
 // Every expert's product over its own segment of rows (Fprop and Dgrad of a
 // mixture): a persistent grid takes the tiles of all experts in turn, found by
 // the map that each workgroup makes at its start.
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void grouped_rows_kernel(GroupedArgs a, uint32_t tiles_n) {
+__global__ __launch_bounds__(C::THREADS, 2) void grouped_rows_kernel(GroupedArgs a, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ GroupedMap map;
   const int E = (int)a.E;
@@ -592,14 +652,15 @@ __global__ __launch_bounds__(C::THREADS) void grouped_rows_kernel(GroupedArgs a,
     const TileAt at = tile_at<8>(t - map.starts[e] * tiles_n, (uint32_t)(s.length + C::BM - 1) / C::BM, tiles_n);
     const int64_t i0 = (int64_t)at.m * C::BM, j0 = (int64_t)at.n * C::BN;
     gemm_tile<C>(g, lds, i0, j0, 0, g.R / 128, acc);
-    gk_store<C>(acc, g.out, g.J, g.I, g.J, g.out_f32, g.accumulate, i0, j0);
+    gk_store_rows<C>(acc, lds, g.out, g, i0, j0);
+    lds_barrier();
   }
 }
 
 // Every expert's Wgrad: the reduction runs over its segment alone.  A segment
 // without rows leaves zeros.
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void grouped_wgrad_kernel(GroupedArgs a, uint32_t tiles_m, uint32_t tiles_n) {
+__global__ __launch_bounds__(C::THREADS, 2) void grouped_wgrad_kernel(GroupedArgs a, uint32_t tiles_m, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const uint32_t tiles = tiles_m * tiles_n, total = (uint32_t)a.E * tiles;
   v4f acc[C::TM][C::TN];
@@ -609,8 +670,8 @@ __global__ __launch_bounds__(C::THREADS) void grouped_wgrad_kernel(GroupedArgs a
     const TileAt at = tile_at<8>(t - e * tiles, tiles_m, tiles_n);
     const int64_t i0 = (int64_t)at.m * C::BM, j0 = (int64_t)at.n * C::BN;
     gemm_tile<C>(a.g, lds, i0, j0, s.first / 128, (s.first + s.length) / 128, acc);
-    gk_store<C>(acc, element(a.g.out, e * a.out_stride, a.g.out_f32), a.g.J, a.g.I, a.g.J, a.g.out_f32,
-                a.g.accumulate, i0, j0);
+    gk_store_rows<C>(acc, lds, element(a.g.out, e * a.out_stride, a.g.out_f32), a.g, i0, j0);
+    lds_barrier();
   }
 }
 
@@ -672,6 +733,9 @@ hipError_t launch_gemm(const GemmArgs& g, GemmAlgo algo, hipStream_t stream) {
   return algo == GemmAlgo::Promote ? launch_cfg<PromoteBlock>(g, stream) : launch_cfg<ScaledBlock>(g, stream);
 }
 
+// The workgroups that the GPU holds at once, by LDS.
+constexpr int64_t at_once(size_t lds) { return kSkGrid * (int64_t)(160 * 1024 / lds); }
+
 template <class C>
 static hipError_t launch_grouped_rows_cfg(const GroupedArgs& a, hipStream_t stream) {
   const int64_t tiles_n = (a.g.J + C::BN - 1) / C::BN;
@@ -679,7 +743,7 @@ static hipError_t launch_grouped_rows_cfg(const GroupedArgs& a, hipStream_t stre
   static std::atomic<uint64_t> attr_set{0};
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_rows_kernel<C>), C::LDS, &attr_set))
     return e;
-  hipLaunchKernelGGL(grouped_rows_kernel<C>, dim3(grouped_grid(most, kSkGrid)), dim3(C::THREADS), C::LDS, stream, a,
+  hipLaunchKernelGGL(grouped_rows_kernel<C>, dim3(grouped_grid(most, at_once(C::LDS + sizeof(GroupedMap)))), dim3(C::THREADS), C::LDS, stream, a,
                      (uint32_t)tiles_n);
   return hipGetLastError();
 }
@@ -687,33 +751,53 @@ static hipError_t launch_grouped_rows_cfg(const GroupedArgs& a, hipStream_t stre
 template <class C>
 static hipError_t launch_grouped_wgrad_cfg(const GroupedArgs& a, hipStream_t stream) {
   const int64_t tiles_m = (a.g.I + C::BM - 1) / C::BM, tiles_n = (a.g.J + C::BN - 1) / C::BN;
-  const int64_t total = a.E * tiles_m * tiles_n;
+  const int64_t total = a.E * tiles_m * tiles_n, most = at_once(C::LDS);
   static std::atomic<uint64_t> attr_set{0};
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_wgrad_kernel<C>), C::LDS, &attr_set))
     return e;
-  hipLaunchKernelGGL(grouped_wgrad_kernel<C>, dim3((uint32_t)(total < kSkGrid ? total : kSkGrid)), dim3(C::THREADS),
+  hipLaunchKernelGGL(grouped_wgrad_kernel<C>, dim3((uint32_t)(total < most ? total : most)), dim3(C::THREADS),
                      C::LDS, stream, a, (uint32_t)tiles_m, (uint32_t)tiles_n);
   return hipGetLastError();
 }
 
+// Experts' products are many short ones: what a tile takes besides its blocks -- the
+// first loads, the scales, the store -- has to be hidden behind another tile.  So the
+// tiles are 128 x 128, two workgroups a CU (72 KiB of LDS each), against the dense
+// kernel's one of 256 x 128: 414 rows of 52 experts of 896 x 3328, amax / 448, Fprop
+// 80 us and 43, Wgrad 209 and 149; 65536 rows of 64 of 2048 x 2048 Dgrad 508 and 444.
+// Where no more than a CU's worth of them are left, 64 x 128, so that more CUs work:
+// 512 rows of 2 experts, Dgrad of 4736 x 256, 35 us and 27.
+template <bool PROMOTE, bool BROW, bool BT, int BM>
+using Expert = Cfg<BM, 128, 2, 2, PROMOTE, BROW, BT, 2, 8>;
+
+template <bool PROMOTE, bool BT>
+static hipError_t launch_experts(const GroupedArgs& a, bool few, hipStream_t stream) {
+  return few ? launch_grouped_rows_cfg<Expert<PROMOTE, false, BT, 64>>(a, stream)
+             : launch_grouped_rows_cfg<Expert<PROMOTE, false, BT, 128>>(a, stream);
+}
+
 hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
   const bool promote = algo == GemmAlgo::Promote;
-  // the weight-block scales of a reduction sit in LDS; per-lane 32-bit offsets of
-  // 128 rows; at most a workgroup a tile, of a launch below 2^32 threads
-  if (!promote && a.g.R <= kMxMaxKb * 128 && a.g.J <= (int64_t(1) << 22) && grouped_mx_tiles(a) < (1 << 24))
-    return launch_grouped_rows_mx(a, stream);
-  if (a.g.bt)
-    return promote ? launch_grouped_rows_cfg<PromoteBlockBT>(a, stream) : launch_grouped_rows_cfg<ScaledBlockBT>(a, stream);
-  return promote ? launch_grouped_rows_cfg<PromoteBlock>(a, stream) : launch_grouped_rows_cfg<ScaledBlock>(a, stream);
+  const bool few = (a.g.I / 128 + a.E) * (a.g.J / 128) <= kSkGrid;  // tiles of 128 x 128, at most
+  // the 256 x 256 tiles take whole groups of four 128-blocks (others on them, their
+  // scales one by one, were 53 us where these tiles take 48, 73 and 39, 59 and 47);
+  // per-lane 32-bit offsets of 128 rows
+  if (!promote && !few && gemm_mx_eligible(a.g) && a.g.J <= (int64_t(1) << 22)) return launch_grouped_rows_mx(a, stream);
+  if (a.g.bt) return promote ? launch_experts<true, true>(a, few, stream) : launch_experts<false, true>(a, few, stream);
+  return promote ? launch_experts<true, false>(a, few, stream) : launch_experts<false, false>(a, few, stream);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
-  // per-lane 32-bit offsets: 256 rows of R bytes; scales in 16-byte groups of four
+  // the 256 x 256 tiles take scales in 16-byte groups of four, per-lane 32-bit offsets
+  // of 256 rows of R bytes
   const auto quads = [](const float* s) { return reinterpret_cast<uintptr_t>(s) % 16 == 0; };
-  if (algo == GemmAlgo::ScaledMfma && a.g.R <= (int64_t(1) << 22) && a.g.R % 512 == 0 && quads(a.g.sa) && quads(a.g.sb))
-    return launch_grouped_wgrad_mx(a, stream);
-  return algo == GemmAlgo::Promote ? launch_grouped_wgrad_cfg<PromoteRow>(a, stream)
-                                   : launch_grouped_wgrad_cfg<ScaledRow>(a, stream);
+  const bool takes = a.g.R <= (int64_t(1) << 22) && a.g.R % 512 == 0 && quads(a.g.sa) && quads(a.g.sb);
+  if (algo == GemmAlgo::ScaledMfma && takes) {
+    const WgradPlan p = wgrad_plan(a);
+    if (p.large <= p.small) return launch_grouped_wgrad_mx(a, stream);
+  }
+  return algo == GemmAlgo::Promote ? launch_grouped_wgrad_cfg<Expert<true, true, false, 128>>(a, stream)
+                                   : launch_grouped_wgrad_cfg<Expert<false, true, false, 128>>(a, stream);
 }
 
 }  // namespace fp8blk

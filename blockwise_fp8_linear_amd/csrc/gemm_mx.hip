@@ -127,15 +127,12 @@ __device__ __forceinline__ void tile_origin(int64_t tile, int64_t tiles_m, int64
 // may still be read by other waves until the next barrier.
 // BT: B is stored [R][J] (the weight codes W[n][k] read as quantized, for
 // Dgrad) instead of [J][R]; weight-block scales only.
-// RAGGED: any 128-blocks, at least one, from any of them on.  Their scales are
-// then not 16-byte aligned and are loaded one by one; the last group of four may
-// hold fewer blocks.
 // TM = HALF: a tile of 128 rows.
-template <bool BROW, bool BT = false, bool RAGGED = false, int TM = fp8blk::TM>
+template <bool BROW, bool BT = false, int TM = fp8blk::TM>
 __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int64_t i0, int64_t j0, int64_t kb_begin,
                                             int64_t nkb_seg, v16f (&acc)[TM][TN]) {
   static_assert(!(BT && BROW), "the transposed-B layout is Dgrad's, with weight-block scales");
-  static_assert(!BROW || (TM == fp8blk::TM && !RAGGED), "row scales of B: whole groups, tiles of 256 rows");
+  static_assert(!BROW || TM == fp8blk::TM, "a tile of 128 rows has no room for B's row scales");
   typedef Ring<TM> Rg;
   constexpr int LOADS_A = Rg::LOADS_A, LOADS_PER_PAIR = LOADS_A + LOADS_B, WM = 32 * TM;
   constexpr int SLOTS = Rg::SLOTS, A_SLOT = Rg::A, SLOT = Rg::SLOT, SC_BYTES = Rg::SC;
@@ -221,15 +218,6 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   auto issue_scales = [&](int q) {  // group q -> scale buffer q & 1
     const uint32_t buf = sc0 + (uint32_t)(q & 1) * SC_BYTES;
     if (wave * 64 >= Rg::ROWS) return;  // a tile of 128 rows: two waves' rows
-    if constexpr (RAGGED) {
-      // [block of the group][row]; a block past the end loads the last one's
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 4 * q + i < npair ? 4 * q + i : npair - 1;
-        dma4(baseSA + 4 * k, offSA, buf + i * 4 * Rg::ROWS + wave * 256);
-      }
-      return;
-    }
     const int qc = q < ngroup ? q : ngroup - 1;
     dma16(baseSA + 16 * qc, offSA, buf + wave * 1024);
     if constexpr (BROW) dma16(baseSB + 16 * qc, offSB, buf + 4096 + wave * 1024);
@@ -301,22 +289,16 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
   };
   auto read_scales = [&](int q, uint32_t* pa, uint32_t* pb) {
     const uint8_t* buf = sc_lds + (q & 1) * SC_BYTES;
-    const auto four = [](const uint8_t* rows, uint32_t row) {
-      if constexpr (!RAGGED) return pack_e8(*reinterpret_cast<const u32x4*>(rows + row * 16));
-      u32x4 s;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const uint32_t*>(rows + i * 4 * Rg::ROWS + row * 4);
-      return pack_e8(s);
-    };
-#pragma unroll
-    for (int t = 0; t < TM; ++t) pa[t] = four(buf, wm0 + t * 32 + l32);
+    for (int t = 0; t < TM; ++t) pa[t] = pack_e8(*reinterpret_cast<const u32x4*>(buf + (wm0 + t * 32 + l32) * 16));
     if constexpr (BROW) {
 #pragma unroll
-      for (int t = 0; t < TN; ++t) pb[t] = four(buf + 4096, wn0 + t * 32 + l32);
+      for (int t = 0; t < TN; ++t)
+        pb[t] = pack_e8(*reinterpret_cast<const u32x4*>(buf + 4096 + (wn0 + t * 32 + l32) * 16));
     } else {
       // this wave's weight block, blocks 4q..4q+3 of the slice (same
       // address in every lane: a broadcast read)
-      const int groups = RAGGED ? (npair + 3) / 4 : ngroup, qc = q < groups ? q : groups - 1;
+      const int qc = q < ngroup ? q : ngroup - 1;
       const uint32_t e = pack_e8(*reinterpret_cast<const u32x4*>(lds + bs_area + wave * (MAX_KB * 4) + 16 * qc));
 #pragma unroll
       for (int t = 0; t < TN; ++t) pb[t] = e;
@@ -392,42 +374,22 @@ __device__ __forceinline__ void mma_segment(const GemmArgs& g, uint8_t* lds, int
     }
   };
 
-  if constexpr (RAGGED) {
-    // One iteration = one 128-block.  The byte of the packed scales that it takes
-    // is shifted to the bottom: by op_sel, the last group's blocks would need
-    // copies of the stages behind the loop, and the compiler runs out of
-    // registers where they meet.
-    for (int p = 0; p < npair; ++p) {
-      if ((p & 3) == 0) issue_scales((p >> 2) + 1);
-      stage_step(2 * p, IntC<0>{}, IntC<0>{});
-      stage_step(2 * p + 1, IntC<1>{}, IntC<0>{});
-      if ((p & 3) == 3) {
-        read_scales((p >> 2) + 1, sa_cur, sb_cur);
-      } else {
-#pragma unroll
-        for (int t = 0; t < TM; ++t) sa_cur[t] >>= 8;
-#pragma unroll
-        for (int t = 0; t < TN; ++t) sb_cur[t] >>= 8;
-      }
-    }
-  } else {
-    // One loop iteration = one group = four 128-blocks = eight 64-deep stages;
-    // op_sel (the byte of the packed scales) is a constant in each step.
-    for (int q = 0; q < ngroup; ++q) {
-      const int st = 8 * q;
-      issue_scales(q + 1);  // buffer (q+1)&1 was last read at the end of group q-2
-      stage_step(st + 0, IntC<0>{}, IntC<0>{});
-      stage_step(st + 1, IntC<1>{}, IntC<0>{});
-      stage_step(st + 2, IntC<0>{}, IntC<1>{});
-      stage_step(st + 3, IntC<1>{}, IntC<1>{});
-      stage_step(st + 4, IntC<0>{}, IntC<2>{});
-      stage_step(st + 5, IntC<1>{}, IntC<2>{});
-      stage_step(st + 6, IntC<0>{}, IntC<3>{});
-      stage_step(st + 7, IntC<1>{}, IntC<3>{});
-      // group q+1's scales were issued before the waits of this group's odd
-      // stages and every wave passed their barriers
-      read_scales(q + 1, sa_cur, sb_cur);
-    }
+  // One loop iteration = one group = four 128-blocks = eight 64-deep stages;
+  // op_sel (the byte of the packed scales) is a constant in each step.
+  for (int q = 0; q < ngroup; ++q) {
+    const int st = 8 * q;
+    issue_scales(q + 1);  // buffer (q+1)&1 was last read at the end of group q-2
+    stage_step(st + 0, IntC<0>{}, IntC<0>{});
+    stage_step(st + 1, IntC<1>{}, IntC<0>{});
+    stage_step(st + 2, IntC<0>{}, IntC<1>{});
+    stage_step(st + 3, IntC<1>{}, IntC<1>{});
+    stage_step(st + 4, IntC<0>{}, IntC<2>{});
+    stage_step(st + 5, IntC<1>{}, IntC<2>{});
+    stage_step(st + 6, IntC<0>{}, IntC<3>{});
+    stage_step(st + 7, IntC<1>{}, IntC<3>{});
+    // group q+1's scales were issued before the waits of this group's odd
+    // stages and every wave passed their barriers
+    read_scales(q + 1, sa_cur, sb_cur);
   }
   wait_vmcnt<0>();  // no direct load may still target this workgroup's LDS at exit
 }
@@ -841,7 +803,7 @@ __global__ __launch_bounds__(256) void bwd_fixup_kernel(GemmArgs gd, GemmArgs gw
 // is found by the map that each workgroup makes at its start.  A segment that ends
 // in a block of 128 rows has a tile of 128 there; where all tiles are of 128 rows
 // and there is still at most one a CU, all of them are.
-template <bool BT, bool RAGGED>
+template <bool BT>
 __global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   __shared__ GroupedMap map;
@@ -863,15 +825,13 @@ __global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a,
     lds_barrier();  // the previous tile's epilogue is done with LDS
     if (!halves && s.length - i0 > BM / 2) {
       v16f acc[TM][TN];
-      mma_segment<false, BT, RAGGED>(g, lds, i0, j0, 0, g.R / 128, acc);
+      mma_segment<false, BT>(g, lds, i0, j0, 0, g.R / 128, acc);
       store_tile<1>(d, lds, i0, j0, acc);
     } else {
       v16f acc[HALF][TN];
-      mma_segment<false, BT, RAGGED, HALF>(g, lds, i0, j0, 0, g.R / 128, acc);
+      mma_segment<false, BT, HALF>(g, lds, i0, j0, 0, g.R / 128, acc);
       store_tile<1>(d, lds, i0, j0, acc);
     }
-    // RAGGED, as a loop, runs out of registers: its grid has a workgroup for any tile
-    if constexpr (RAGGED) return;
   }
 }
 
@@ -922,28 +882,22 @@ hipError_t launch_bwd(const GemmArgs& gd, const GemmArgs& gw, float* ws, hipStre
   return hipGetLastError();
 }
 
-template <bool BT, bool RAGGED>
+template <bool BT>
 hipError_t launch_grouped_rows_as(const GroupedArgs& a, hipStream_t stream) {
-  // in halves there are at most 2 kSkGrid
-  const int64_t tiles_n = (a.g.J + BN - 1) / BN, tiles = grouped_mx_tiles(a);
-  const int64_t most = !RAGGED ? kSkGrid : tiles > 2 * kSkGrid ? (tiles + 7) / 8 * 8 : 2 * kSkGrid;
+  const int64_t tiles_n = (a.g.J + BN - 1) / BN, tiles = (a.g.I / BM + a.E) * tiles_n;
   static std::atomic<uint64_t> attr_set{0};
-  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_mx_rows_kernel<BT, RAGGED>),
-                                      LDS_BYTES_ROWS, &attr_set))
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_mx_rows_kernel<BT>), LDS_BYTES_ROWS,
+                                      &attr_set))
     return e;
-  hipLaunchKernelGGL((grouped_mx_rows_kernel<BT, RAGGED>), dim3(grouped_grid(2 * tiles, most)), dim3(THREADS),
-                     LDS_BYTES_ROWS, stream, a, (uint32_t)tiles_n);
+  hipLaunchKernelGGL(grouped_mx_rows_kernel<BT>, dim3(grouped_grid(2 * tiles, kSkGrid)), dim3(THREADS), LDS_BYTES_ROWS,
+                     stream, a, (uint32_t)tiles_n);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t grouped_mx_tiles(const GroupedArgs& a) { return (a.g.I / BM + a.E) * ((a.g.J + BN - 1) / BN); }
-
 hipError_t launch_grouped_rows_mx(const GroupedArgs& a, hipStream_t stream) {
-  if (gemm_mx_eligible(a.g))  // whole groups of four 128-blocks, their scales 16-byte aligned
-    return a.g.bt ? launch_grouped_rows_as<true, false>(a, stream) : launch_grouped_rows_as<false, false>(a, stream);
-  return a.g.bt ? launch_grouped_rows_as<true, true>(a, stream) : launch_grouped_rows_as<false, true>(a, stream);
+  return a.g.bt ? launch_grouped_rows_as<true>(a, stream) : launch_grouped_rows_as<false>(a, stream);
 }
 
 hipError_t launch_gemm_mx(const GemmArgs& g, hipStream_t stream) {

@@ -429,15 +429,8 @@ __global__ __launch_bounds__(THREADS) void grouped_mx_wgrad_kernel(GroupedArgs g
 
 hipError_t launch_grouped_wgrad_mx(const GroupedArgs& a, hipStream_t stream) {
   const int64_t tiles_m = (a.g.I + TILE - 1) / TILE, tiles_n = (a.g.J + TILE - 1) / TILE, tiles = a.E * tiles_m * tiles_n;
-  // As many tiles a workgroup as leave the fewest rounds of the GPU's CUs, up to
-  // kMostEach: a workgroup with one of the longest segments then still starts early,
-  // and others take what it leaves.
-  constexpr int64_t kMostEach = 8, kWhole = 8 * RUN;
-  int64_t each = 1, best = INT64_MAX;
-  for (int64_t n = 1; n <= kMostEach; ++n) {
-    const int64_t rounds = ((tiles + n - 1) / n + kSkGrid - 1) / kSkGrid * n;
-    if (rounds <= best) best = rounds, each = n;
-  }
+  const int64_t each = wgrad_plan(a).each;
+  constexpr int64_t kWhole = 8 * RUN;
   const int64_t workgroups = ((tiles + each - 1) / each + kWhole - 1) / kWhole * kWhole;
   static std::atomic<uint64_t> attr_set{0};
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&grouped_mx_wgrad_kernel), LDS_BYTES, &attr_set))

@@ -141,8 +141,9 @@ int fp8_moe_combine_backward(int64_t T, int64_t H, int64_t R, int k, const uint1
  * Rows of y and dx outside the segments are not written.  All operands dense,
  * 16-byte aligned (offsets 4-byte); R, N, K positive multiples of 128, R < 2^29,
  * N, K < 2^25, E <= FP8MOE_MAX_EXPERTS, R N and R K at most 2^40, E N K 2^38.
- * Results do not depend on how rows are spread over the other experts; sums are
- * fp32 with the accuracy of the GEMMs of fp8blk.h.
+ * For given sizes an expert's results do not depend on how the other rows are
+ * spread over the other experts; sums are fp32 with the accuracy of the GEMMs of
+ * fp8blk.h.
  */
 int fp8_moe_gemm_fprop(int64_t R, int64_t N, int64_t K, int64_t E, const uint8_t *qx, const float *sx,
                        const uint8_t *qw, const float *sw, const int32_t *offsets, void *y, int out_dtype,
