@@ -54,14 +54,11 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 // BT_: B stored [R][J] (Dgrad from the weight codes as quantized): the B
 // tile is staged as 128 reduction rows of BN bytes and its fragments come
 // from LDS transpose reads.
-// STAGES_: blocks in LDS at once; beyond two, STAGES_ - 1 are on the way, for tiles
-// that are small beside the time a load takes.
 // CHUNK_: reduction blocks whose scales sit in LDS at once.
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool PROMOTE_, bool BROW_, bool BT_ = false, int STAGES_ = 2,
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool PROMOTE_, bool BROW_, bool BT_ = false,
           int CHUNK_ = 32>
 struct Cfg {
-  static constexpr int CHUNK = CHUNK_;
-  static constexpr int BM = BM_, BN = BN_, STAGES = STAGES_;
+  static constexpr int BM = BM_, BN = BN_, CHUNK = CHUNK_;
   static constexpr bool BT = BT_;
   static_assert(!BT_ || (!BROW_ && BN_ == 128), "transposed B: Dgrad's weight-block layout, 128-byte rows");
   static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
@@ -75,7 +72,7 @@ struct Cfg {
   using SType = typename std::conditional<PROMOTE_, float, uint8_t>::type;
   static constexpr int SA_BYTES = CHUNK * BM * (int)sizeof(SType);
   static constexpr int SB_BYTES = (BROW ? CHUNK * BN : CHUNK * (BN / 128 > 0 ? BN / 128 : 1)) * (int)sizeof(SType);
-  static constexpr int LDS = STAGES * STAGE + SA_BYTES + ((SB_BYTES + 15) / 16) * 16;
+  static constexpr int LDS = 2 * STAGE + SA_BYTES + ((SB_BYTES + 15) / 16) * 16;
   static_assert(A_BYTES % (1024 * (THREADS / 64)) == 0 && B_BYTES % (1024 * (THREADS / 64)) == 0,
                 "whole KiB of direct loads per wave");
   static_assert(WN <= 128 && 128 % WN == 0, "a wave's columns must sit inside one 128-block");
@@ -163,8 +160,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
                                           int64_t kb_end, v4f (&acc)[C::TM][C::TN]) {
   uint8_t* const tiles = lds;
   typedef typename C::SType ST;
-  ST* const sa_lds = reinterpret_cast<ST*>(lds + C::STAGES * C::STAGE);
-  ST* const sb_lds = reinterpret_cast<ST*>(lds + C::STAGES * C::STAGE + C::SA_BYTES);
+  ST* const sa_lds = reinterpret_cast<ST*>(lds + 2 * C::STAGE);
+  ST* const sb_lds = reinterpret_cast<ST*>(lds + 2 * C::STAGE + C::SA_BYTES);
 
   const uint32_t tid = threadIdx.x;
   const uint32_t lane = tid & 63;
@@ -264,28 +261,17 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
 
   const uint32_t wm0 = wm * C::WM, wn0 = wn * C::WN;
 
-  constexpr int PER_BLOCK = A_DMA + B_DMA;
-  // block kb -> its stage; one past the end reloads the last into a stage that is
-  // not read again (which keeps the count of loads on the way the same)
-  const auto dma_ahead = [&](int64_t kb) {
-    dma_block(kb < kb_end ? kb : kb_end - 1, (int)((kb - kb_begin) % C::STAGES));
-  };
   if (kb_begin < kb_end) {
     dma_block(kb_begin, 0);
-    if constexpr (C::STAGES > 2) {
-#pragma unroll
-      for (int s = 1; s < C::STAGES - 1; ++s) dma_ahead(kb_begin + s);
-    }
     load_scales(kb_begin, (kb_end - kb_begin) < C::CHUNK ? (kb_end - kb_begin) : C::CHUNK);
-    wait_vmcnt<C::STAGES == 2 ? 0 : (C::STAGES - 2) * PER_BLOCK>();
+    wait_vmcnt<0>();
     __syncthreads();
   }
   for (int64_t kb = kb_begin; kb < kb_end; ++kb) {
-    const int cur = (int)((kb - kb_begin) % C::STAGES);
+    const int cur = (int)((kb - kb_begin) & 1);
     const bool more = kb + 1 < kb_end;
-    // the stage that is loaded was last read in the previous block, before its barrier
-    if constexpr (C::STAGES > 2) dma_ahead(kb + C::STAGES - 1);
-    else if (more) dma_block(kb + 1, cur ^ 1);
+    // the other stage was last read in the previous block, before its barrier
+    if (more) dma_block(kb + 1, cur ^ 1);
 
     const uint8_t* ta = tiles + cur * C::STAGE;
     const uint8_t* tb = ta + C::A_BYTES;
@@ -415,14 +401,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
       const int64_t rest = kb_end - (kb + 1);
       load_scales(kb + 1, rest < C::CHUNK ? rest : C::CHUNK);
     }
-    // this wave's loads of block kb+1 have landed
-    if constexpr (C::STAGES > 2) wait_vmcnt<(C::STAGES - 2) * PER_BLOCK>();
-    else wait_vmcnt<0>();
+    wait_vmcnt<0>();  // this wave's loads of block kb+1 have landed
     __syncthreads();  // ... and every wave's; no wave reads stage cur any more
-  }
-  if constexpr (C::STAGES > 2) {
-    wait_vmcnt<0>();  // those past the end
-    __syncthreads();
   }
 }
 
@@ -583,12 +563,12 @@ __global__ __launch_bounds__(256) void gk_fixup_kernel(GemmArgs g, SkGeom sg, co
 template <class C>
 __device__ __forceinline__ void gk_store_rows(const v4f (&acc)[C::TM][C::TN], uint8_t* lds, void* out, const GemmArgs& g,
                                               int64_t i0, int64_t j0) {
-  static_assert(C::WN == 64 && C::WM * 256 <= C::STAGES * C::STAGE / (C::THREADS / 64), "a wave's rows of fp32");
+  static_assert(C::WN == 64 && C::WM * 256 <= 2 * C::STAGE / (C::THREADS / 64), "a wave's rows of fp32");
   uint32_t lane = threadIdx.x & 63;
   int64_t ld = g.J;
   asm volatile("" : "+v"(lane), "+s"(ld));  // no address is to stay in registers from one tile to the next
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, g4 = lane >> 4;
-  uint8_t* const staging = lds + wave * (C::STAGES * C::STAGE / (C::THREADS / 64));
+  uint8_t* const staging = lds + wave * (2 * C::STAGE / (C::THREADS / 64));
   const int64_t row0 = i0 + (wave / C::WAVES_N) * C::WM, col0 = j0 + (wave % C::WAVES_N) * C::WN;
   const int64_t rows = g.I - row0;  // (128 columns are all in)
   if (!g.out_f32) {
@@ -768,7 +748,7 @@ static hipError_t launch_grouped_wgrad_cfg(const GroupedArgs& a, hipStream_t str
 // Where no more than a CU's worth of them are left, 64 x 128, so that more CUs work:
 // 512 rows of 2 experts, Dgrad of 4736 x 256, 35 us and 27.
 template <bool PROMOTE, bool BROW, bool BT, int BM>
-using Expert = Cfg<BM, 128, 2, 2, PROMOTE, BROW, BT, 2, 8>;
+using Expert = Cfg<BM, 128, 2, 2, PROMOTE, BROW, BT, 8>;
 
 template <bool PROMOTE, bool BT>
 static hipError_t launch_experts(const GroupedArgs& a, bool few, hipStream_t stream) {
