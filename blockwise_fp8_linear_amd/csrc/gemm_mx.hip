@@ -720,7 +720,7 @@ __global__ __launch_bounds__(THREADS) void gemm_mx_bwd_kernel(GemmArgs gd, GemmA
     if (lo == 0 && hi == U) {
       const Dst d{p1 ? gw.out : gd.out, p1 ? gw.J : gd.J, p1 ? gw.I : gd.I, p1 ? gw.J : gd.J,
                   p1 ? gw.out_f32 : gd.out_f32, p1 ? gw.accumulate : gd.accumulate};
-      store_tile<8>(d, lds, i0, j0, acc);
+      store_tile<1>(d, lds, i0, j0, acc);
     } else {
       float* const slot = partials + slot_of(bg.slot, r, u == ubeg) * (int64_t)(BM * BN);
       store_tile<1>(Dst{slot, BN, BM, BN, true, false}, lds, 0, 0, acc);
