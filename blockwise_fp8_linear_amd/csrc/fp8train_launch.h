@@ -118,4 +118,25 @@ inline WgradPlan wgrad_plan(const GroupedArgs& a) {
   return p;
 }
 
+// Which kernel: tiles of 256 x 256 (Large), of 128 x 128, or of 64 x 128 (Few).
+enum class GroupedTiles { Large, Small, Few };
+inline GroupedTiles grouped_rows_tiles(const GroupedArgs& a, GemmAlgo algo) {
+  // no more than a tile of 128 x 128 a CU, whatever the segments
+  if ((a.g.I / 128 + a.E) * (a.g.J / 128) <= 256) return GroupedTiles::Few;
+  // the large tiles take whole groups of four 128-blocks (others on them, their scales
+  // one by one, were 53 us where the small tiles take 48, 73 and 39, 59 and 47); per-lane
+  // 32-bit offsets of 128 rows
+  return algo == GemmAlgo::ScaledMfma && gemm_mx_eligible(a.g) && a.g.J <= (int64_t(1) << 22) ? GroupedTiles::Large
+                                                                                            : GroupedTiles::Small;
+}
+inline GroupedTiles grouped_wgrad_tiles(const GroupedArgs& a, GemmAlgo algo) {
+  // the large tiles take scales in 16-byte groups of four, per-lane 32-bit offsets of 256
+  // rows of R bytes
+  const auto quads = [](const float* s) { return reinterpret_cast<uintptr_t>(s) % 16 == 0; };
+  if (algo != GemmAlgo::ScaledMfma || a.g.R > (int64_t(1) << 22) || a.g.R % 512 != 0 || !quads(a.g.sa) || !quads(a.g.sb))
+    return GroupedTiles::Small;
+  const WgradPlan p = wgrad_plan(a);
+  return p.large <= p.small ? GroupedTiles::Large : GroupedTiles::Small;
+}
+
 }  // namespace fp8blk

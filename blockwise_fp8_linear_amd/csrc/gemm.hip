@@ -751,31 +751,21 @@ template <bool PROMOTE, bool BROW, bool BT, int BM>
 using Expert = Cfg<BM, 128, 2, 2, PROMOTE, BROW, BT, 8>;
 
 template <bool PROMOTE, bool BT>
-static hipError_t launch_experts(const GroupedArgs& a, bool few, hipStream_t stream) {
-  return few ? launch_grouped_rows_cfg<Expert<PROMOTE, false, BT, 64>>(a, stream)
-             : launch_grouped_rows_cfg<Expert<PROMOTE, false, BT, 128>>(a, stream);
+static hipError_t launch_experts(const GroupedArgs& a, GroupedTiles tiles, hipStream_t stream) {
+  return tiles == GroupedTiles::Few ? launch_grouped_rows_cfg<Expert<PROMOTE, false, BT, 64>>(a, stream)
+                                    : launch_grouped_rows_cfg<Expert<PROMOTE, false, BT, 128>>(a, stream);
 }
 
 hipError_t launch_grouped_rows(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
-  const bool promote = algo == GemmAlgo::Promote;
-  const bool few = (a.g.I / 128 + a.E) * (a.g.J / 128) <= kSkGrid;  // tiles of 128 x 128, at most
-  // the 256 x 256 tiles take whole groups of four 128-blocks (others on them, their
-  // scales one by one, were 53 us where these tiles take 48, 73 and 39, 59 and 47);
-  // per-lane 32-bit offsets of 128 rows
-  if (!promote && !few && gemm_mx_eligible(a.g) && a.g.J <= (int64_t(1) << 22)) return launch_grouped_rows_mx(a, stream);
-  if (a.g.bt) return promote ? launch_experts<true, true>(a, few, stream) : launch_experts<false, true>(a, few, stream);
-  return promote ? launch_experts<true, false>(a, few, stream) : launch_experts<false, false>(a, few, stream);
+  const GroupedTiles tiles = grouped_rows_tiles(a, algo);
+  if (tiles == GroupedTiles::Large) return launch_grouped_rows_mx(a, stream);
+  if (algo == GemmAlgo::Promote)
+    return a.g.bt ? launch_experts<true, true>(a, tiles, stream) : launch_experts<true, false>(a, tiles, stream);
+  return a.g.bt ? launch_experts<false, true>(a, tiles, stream) : launch_experts<false, false>(a, tiles, stream);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, GemmAlgo algo, hipStream_t stream) {
-  // the 256 x 256 tiles take scales in 16-byte groups of four, per-lane 32-bit offsets
-  // of 256 rows of R bytes
-  const auto quads = [](const float* s) { return reinterpret_cast<uintptr_t>(s) % 16 == 0; };
-  const bool takes = a.g.R <= (int64_t(1) << 22) && a.g.R % 512 == 0 && quads(a.g.sa) && quads(a.g.sb);
-  if (algo == GemmAlgo::ScaledMfma && takes) {
-    const WgradPlan p = wgrad_plan(a);
-    if (p.large <= p.small) return launch_grouped_wgrad_mx(a, stream);
-  }
+  if (grouped_wgrad_tiles(a, algo) == GroupedTiles::Large) return launch_grouped_wgrad_mx(a, stream);
   return algo == GemmAlgo::Promote ? launch_grouped_wgrad_cfg<Expert<true, true, false, 128>>(a, stream)
                                    : launch_grouped_wgrad_cfg<Expert<false, true, false, 128>>(a, stream);
 }

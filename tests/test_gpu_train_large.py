@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 import blockwise_fp8_linear_amd as fb
+import train_cases
 import train_ref
 from blockwise_fp8_linear_amd import synth
 from gpu_util import dev, dev_bf16, host, require_gpu
@@ -38,10 +39,10 @@ class Whole:
     two is a scale of both), at most 9 * 2^6 a product.  With at most 2^14 of them to a sum every partial sum is a whole
     number below 2^24."""
 
-    def __init__(self, E, N, K, lengths, behind, key, top=3):
+    def __init__(self, E, N, K, lengths, behind, key, off=0):
         import torch
         self.g = torch.Generator("cuda").manual_seed(key)
-        self.top = top
+        self.off = off      # words that the scales start behind an address of 16 bytes
         self.E, self.N, self.K, self.lengths = E, N, K, lengths
         self.offsets = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
         self.R = int(self.offsets[-1]) + behind
@@ -55,7 +56,8 @@ class Whole:
 
     def scales(self, rows, cols):
         import torch
-        return torch.randint(0, self.top + 1, (rows, cols), generator=self.g, device="cuda").float().exp2()
+        s = torch.randint(0, 4, (rows, cols), generator=self.g, device="cuda").float().exp2()
+        return torch.cat([s.new_zeros(self.off), s.view(-1)])[self.off:].view(rows, cols)
 
     def value(self, q, s, block=False):
         import torch
@@ -92,45 +94,37 @@ class Whole:
         assert bool((out[int(self.offsets[-1]):] == -0.5).all())
 
 
-def some_lengths(E, each):
-    """Segments of every remainder mod 256 and some without rows, about `each` rows a segment."""
-    return [0 if e % 4 == 3 else each + 128 * ((e * 5) % 7 - 3) for e in range(E)]
+@MODES
+@pytest.mark.parametrize("i", range(len(train_cases.GROUPED)))
+def test_grouped_every_kernel(i, mode):
+    way, N, K, lengths, behind = train_cases.GROUPED[i]
+    E = len(lengths)
+    # 16512 products of 9 * 2^6 stay below 2^24
+    Whole(E, N, K, lengths, behind, 100 + i).check(way, mode, None if E < 70 else [*range(0, E, 37), 1, 2, E // 2, E - 2, E - 1])
 
 
 @MODES
 @WAYS
-@pytest.mark.parametrize("cols,red,E,each", [(2048, 512, 12, 640), (2048, 640, 12, 640), (2304, 512, 9, 1408),
-                                             (2304, 384, 9, 1408), (256, 1024, 40, 384)])
-def test_more_tiles_than_workgroups(cols, red, E, each, way, mode):
-    """Tiles of 256 rows with segments that end in 128, fewer tiles than CUs and more, reductions of whole groups of four
-    blocks and others."""
-    N, K = (red, cols) if way == "dgrad" else (cols, red)
-    Whole(E, N, K, some_lengths(E, each), 256, cols + red).check(way, mode)
+def test_scales_off_16_bytes(way, mode):
+    """Scales need 4 bytes of alignment only."""
+    lengths = train_cases.some_lengths(12, 640)
+    N, K = (512, 2048) if way == "dgrad" else (2048, 512)
+    Whole(len(lengths), N, K, lengths, train_cases.whole(lengths), 99, off=1).check(way, mode)
 
 
 @MODES
-@WAYS
-@pytest.mark.parametrize("E", [255, 257, 1000, 1024])
-def test_hundreds_of_experts(E, way, mode):
-    lengths = [128 * (e % 3) for e in range(E)]
-    lengths[-1], lengths[E // 2] = 384, 1152
-    Whole(E, 256, 128, lengths, 128, E).check(way, mode, [*range(0, E, 37), 1, 2, E // 2, E - 2, E - 1])
-
-
-@MODES
-@pytest.mark.parametrize("way,N,K,lengths", [
-    ("fprop", 128, 16384, [128, 0, 384]), ("dgrad", 16512, 256, [256, 128]),       # a long reduction
-    ("fprop", 128, 66048, [128, 256]), ("dgrad", 66048, 128, [256, 128]),          # a longer one
-    ("fprop", (1 << 22) + 256, 128, [128, 256]), ("dgrad", 128, (1 << 22) + 128, [384])])   # many columns
-def test_long_reductions_and_many_columns(way, N, K, lengths, mode):
-    # 66048 products of at most 9 * 2^4: below 2^24
-    Whole(len(lengths), N, K, lengths, 128, 7, top=2 if 66048 in (N, K) else 3).check(way, mode)
-
-
-@MODES
-def test_wgrad_of_more_rows_than_32_bits_of_lane_offsets_take(mode):
-    lengths = [4096] * 1024
-    Whole(1024, 128, 128, lengths, 4096, 11).check("wgrad", mode, [0, 1, 511, 1022, 1023])
+def test_wgrad_types_on_the_large_tiles(mode):
+    """bf16, and what is added to, have the fp32 result."""
+    import torch
+    lengths = train_cases.some_lengths(64, 256)
+    c = Whole(64, 1024, 1024, lengths, train_cases.whole(lengths), 98)
+    a = c.codes(c.N, c.R), c.scales(c.N, c.R // 128), c.codes(c.K, c.R), c.scales(c.K, c.R // 128), dev(c.offsets)
+    y = fb.fp8_moe_gemm_wgrad(*a, out_dtype=torch.float32, scale_mode=mode)
+    assert torch.equal(fb.fp8_moe_gemm_wgrad(*a, scale_mode=mode), y.bfloat16())
+    acc = torch.randn(y.shape, generator=c.g, device="cuda")
+    want = acc + y
+    fb.fp8_moe_gemm_wgrad(*a, out_dtype=torch.float32, out=acc, accumulate=True, scale_mode=mode)
+    assert torch.equal(acc, want)
 
 
 # ------------------------------------------------------- elements past 32 bits --
