@@ -49,15 +49,18 @@ struct GatherArgs {
   uint32_t* order;  // the workspace of gather_order_bytes(), or null where that is 0
 };
 // Row groups of many rows are gathered in the order of their tokens, in runs of a
-// few rows, which a first launch finds: where x outgrows two XCDs' L2 and its
-// rows are read several times over.
+// few rows, which a first launch finds in 8 to 12 us: where x outgrows two XCDs' L2 and
+// the rows' second and further reads of it come to kOrderReread (8192 tokens, 2048
+// wide, to 4 experts each, 117 MB: 29 us either way; to 8, 252 MB: 43 us, unordered 58).
+constexpr int64_t kOrderReread = int64_t(160) << 20;
 constexpr int64_t kOrderRuns = 32768;
 inline int64_t order_run(int64_t R) {
   const int64_t least = (R + kOrderRuns - 1) / kOrderRuns;
   return least <= 4 ? 4 : (least + 7) / 8 * 8;
 }
 inline bool gather_ordered(int64_t T, int64_t H, int64_t R, int k, bool both) {
-  return !both && k > 1 && T * H * 2 > (int64_t(8) << 20) && R >= 2 * T && order_run(R) <= 64;
+  return !both && k > 1 && T * H * 2 > (int64_t(8) << 20) && R >= 2 * T && (R - T) * H * 2 > kOrderReread &&
+         order_run(R) <= 64;
 }
 inline size_t gather_order_bytes(int64_t T, int64_t H, int64_t R, int k, bool both) {
   return gather_ordered(T, H, R, k, both) ? (size_t)((R + order_run(R) - 1) / order_run(R)) * sizeof(uint32_t) : 0;

@@ -115,6 +115,7 @@ __global__ __launch_bounds__(kThreads) void gather_rows_kernel(GatherArgs a, uin
   const int n_rows = (int)(rows - r0 < run ? rows - r0 : run);
   const int64_t n = a.T * a.k, G = a.H / 128;
   const int32_t c0 = (int32_t)(part * kRowCols + lane * 8);  // the lane's first column
+  const int32_t left = (int32_t)(a.H - part * kRowCols);     // the wave's columns: steps behind them are left out
   // lane i: the i-th row's source and weight
   int32_t src = (int)lane < n_rows ? a.source[r0 + lane] : -1;
   if (src >= n) src = -1;
@@ -130,7 +131,8 @@ __global__ __launch_bounds__(kThreads) void gather_rows_kernel(GatherArgs a, uin
     const uint16_t* row = a.x + (int64_t)((uint32_t)s / (uint32_t)a.k) * a.ld_x;
 #pragma unroll
     for (int u = 0; u < kRowSteps; ++u)
-      v[u] = c0 + u * 512 < a.H ? *reinterpret_cast<const u32x4*>(row + c0 + u * 512) : u32x4{0, 0, 0, 0};
+      if (u * 512 < left)
+        v[u] = c0 + u * 512 < a.H ? *reinterpret_cast<const u32x4*>(row + c0 + u * 512) : u32x4{0, 0, 0, 0};
   };
   u32x4 v[kRowSteps], w[kRowSteps];
   load(0, v);
@@ -141,6 +143,7 @@ __global__ __launch_bounds__(kThreads) void gather_rows_kernel(GatherArgs a, uin
     float* const s = a.q.s + (r0 + i) * G;
 #pragma unroll
     for (int u = 0; u < kRowSteps; ++u) {
+      if (u * 512 >= left) break;
       u32x4 x = v[u];
       if constexpr (W) x = u32x4{scaled2(x.x, wt), scaled2(x.y, wt), scaled2(x.z, wt), scaled2(x.w, wt)};
       tile_u32x2 o;

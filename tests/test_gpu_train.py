@@ -156,7 +156,7 @@ def test_gather_used_and_sources_of_no_choice(used):
 
 @MODES
 @pytest.mark.parametrize("weighted", [False, True])
-@pytest.mark.parametrize("T,E,k,H,part", [(4000, 20, 4, 1152, 1.0), (2100, 300, 3, 2176, 0.7)])
+@pytest.mark.parametrize("T,E,k,H,part", [(4000, 20, 16, 1408, 1.0), (2100, 100, 14, 2176, 0.7)])
 def test_gather_in_the_order_of_tokens(T, E, k, H, part, weighted, mode):
     """Sizes that are gathered in the order of their tokens; a device count that ends inside a run's rows and in padding,
     sources of no choice, and a source that stands in many rows."""

@@ -35,10 +35,11 @@ def test_wgrads_rules(tmp_path):
 
 def test_gather_in_the_order_of_tokens(tmp_path):
     ask = host_program(tmp_path, "train_paths_dump.cpp", "plan.cpp")
-    yes = [(16384, 2048, 147456, 8, 0), (4000, 1152, 18944, 4, 0), (65536, 4224, 1 << 20, 16, 0)]
+    yes = [(16384, 2048, 147456, 8, 0), (4000, 1408, 66560, 16, 0), (65536, 4224, 1 << 20, 16, 0)]
     no = [(2048, 2048, 24576, 8, 0),        # x fits two XCDs' L2
           (16384, 2048, 147456, 8, 1),      # both orientations
           (16384, 2048, 24576, 1, 0),       # each row once
+          (8192, 2048, 36864, 4, 0),        # too little read again
           (16384, 2048, 1 << 22, 8, 0)]     # runs longer than a wave
     assert [g[0] for g in ask([(3, *s) for s in yes])] == [1] * 3
-    assert [g[0] for g in ask([(3, *s) for s in no])] == [0] * 4
+    assert [g[0] for g in ask([(3, *s) for s in no])] == [0] * 5
