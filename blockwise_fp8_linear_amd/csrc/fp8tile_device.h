@@ -205,10 +205,13 @@ __device__ __forceinline__ void tile_of(uint32_t bid, uint32_t col_tiles, bool b
 }
 
 // The same order for any shape, with workgroups that find no tile (rt or ct past
-// the end): blocks that the shape fills in part, and up to 7 whole ones.  Taken
-// where at least kTileSomeBlocks blocks make those few, and a launch of all of them
-// stays below 2^32 threads.
-constexpr uint32_t kTileSomeBlocks = 96, kTileMostBlocks = 1 << 16;
+// the end): blocks that the shape fills in part, and up to 7 whole ones.  Taken where
+// there are kTileSomeBlocks, no more than an eighth of them is empty, so that the XCDs
+// have about the same work (20608 rows of 2048 in 22 of 24 blocks: a turn 23.9 us, row
+// band by row band 21.7), and a launch of all of them stays below 2^32 threads.  Gated backward of 8192 rows of
+// 6144 118 us row band by row band and 106, of 65536 of 2048 284 and 242; a turn of
+// 69632 rows of 2048 66.6 and 63.8.
+constexpr uint32_t kTileSomeBlocks = 8, kTileMostBlocks = 1 << 16;
 struct TileGrid {
   uint32_t row_tiles, col_tiles;
   bool blocked;
@@ -216,10 +219,11 @@ struct TileGrid {
 };
 inline TileGrid tile_grid(int64_t rows, int64_t cols) {
   TileGrid g{(uint32_t)(rows / 128), (uint32_t)(cols / 128), false, 0};
-  const uint32_t blocks = (g.row_tiles + kTileBlockRows - 1) / kTileBlockRows *
-                          ((g.col_tiles + kTileBlockCols - 1) / kTileBlockCols);
-  g.blocked = blocks >= kTileSomeBlocks && blocks <= kTileMostBlocks && g.col_tiles >= kTileBlockCols / 2;
-  g.workgroups = g.blocked ? (blocks + 7) / 8 * 8 * kTileBlockCols * kTileBlockRows : g.row_tiles * g.col_tiles;
+  const uint32_t col_blocks = (g.col_tiles + kTileBlockCols - 1) / kTileBlockCols;
+  const uint32_t blocks = (g.row_tiles + kTileBlockRows - 1) / kTileBlockRows * col_blocks, all = (blocks + 7) / 8 * 8;
+  g.blocked = blocks >= kTileSomeBlocks && blocks <= kTileMostBlocks && g.col_tiles >= kTileBlockCols / 2 &&
+              uint64_t(8) * all * kTileBlockRows <= uint64_t(9) * g.row_tiles * col_blocks;
+  g.workgroups = g.blocked ? all * kTileBlockCols * kTileBlockRows : g.row_tiles * g.col_tiles;
   return g;
 }
 
