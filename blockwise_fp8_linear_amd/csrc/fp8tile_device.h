@@ -208,9 +208,10 @@ __device__ __forceinline__ void tile_of(uint32_t bid, uint32_t col_tiles, bool b
 // the end): blocks that the shape fills in part, and up to 7 whole ones.  Taken where
 // there are kTileSomeBlocks, no more than an eighth of them is empty, so that the XCDs
 // have about the same work (20608 rows of 2048 in 22 of 24 blocks: a turn 23.9 us, row
-// band by row band 21.7), and a launch of all of them stays below 2^32 threads.  Gated backward of 8192 rows of
-// 6144 118 us row band by row band and 106, of 65536 of 2048 284 and 242; a turn of
-// 69632 rows of 2048 66.6 and 63.8.
+// band by row band 21.7; 16384 of 1536, half of the blocks half as wide: gated backward
+// 63.6 and 54.1), and a launch of all of them stays below 2^32 threads.  Gated
+// backward of 8192 rows of 6144 118 us row band by row band and 106, of 65536 of 2048
+// 284 and 242; a turn of 69632 rows of 2048 66.6 and 63.8.
 constexpr uint32_t kTileSomeBlocks = 8, kTileMostBlocks = 1 << 16;
 struct TileGrid {
   uint32_t row_tiles, col_tiles;
@@ -221,8 +222,9 @@ inline TileGrid tile_grid(int64_t rows, int64_t cols) {
   TileGrid g{(uint32_t)(rows / 128), (uint32_t)(cols / 128), false, 0};
   const uint32_t col_blocks = (g.col_tiles + kTileBlockCols - 1) / kTileBlockCols;
   const uint32_t blocks = (g.row_tiles + kTileBlockRows - 1) / kTileBlockRows * col_blocks, all = (blocks + 7) / 8 * 8;
+  const uint32_t width = col_blocks == 1 ? g.col_tiles : kTileBlockCols;  // all blocks are as narrow, or the last ones
   g.blocked = blocks >= kTileSomeBlocks && blocks <= kTileMostBlocks && g.col_tiles >= kTileBlockCols / 2 &&
-              uint64_t(8) * all * kTileBlockRows <= uint64_t(9) * g.row_tiles * col_blocks;
+              uint64_t(8) * all * kTileBlockRows * width <= uint64_t(9) * g.row_tiles * g.col_tiles;
   g.workgroups = g.blocked ? all * kTileBlockCols * kTileBlockRows : g.row_tiles * g.col_tiles;
   return g;
 }
