@@ -37,40 +37,42 @@ __device__ __forceinline__ void store_codes(uint8_t* p, V v) {
   else *reinterpret_cast<V*>(p) = v;
 }
 
-// The amax / 448 rule with fewer instructions, for scales in [2^-64, infinity):
-// Fp32Scale's quotient without its factor, its clamp and its sign.  y = x r is
-// corrected by (x - s y) r, formed as -(s y - x) r + y: where x is a zero, s y - x
-// is +0 and the sum keeps y's sign.  The amax's own quotient may exceed 448 by an
-// ulp and rounds to 448 without the clamp.  Half of what a tile of this rule takes
-// goes into the quotients, and with Fp32Scale the kernels are bound by them.
+// The amax / 448 rule with fewer instructions, for scales in [2^-64, infinity).  The
+// scale: a product with 1 / 448 and one correction, which gives the correctly rounded
+// quotient of every such bf16 amax.  A value's quotient: Fp32Scale's without its factor,
+// its clamp and its sign, from a reciprocal in two parts, x r + x r2 with r at most 1 /
+// s and r2 = (1 - s r) r, in one rounding of what is then 2^-44 off.  r2 is not negative,
+// so both terms of a zero have its sign.  The amax's own quotient may exceed 448 by an
+// ulp and rounds to 448 without the clamp.  A thread of a tile has 16 scales and 128
+// quotients, which bind the kernels of this rule.
 struct Fp32Quotient {
   static constexpr bool kScaledCvt = false;
-  float s, r;
+  float s, r, r2;
   __device__ __forceinline__ explicit Fp32Quotient(uint32_t amax_bits) {
-    s = amax_bits == 0 ? 1.0f : __uint_as_float(amax_bits << 16) / 448.0f;
-    r = 1.0f / s;
+    const float a = __uint_as_float(amax_bits << 16), c = 1.0f / 448.0f, y = a * c;
+    s = amax_bits == 0 ? 1.0f : __builtin_fmaf(__builtin_fmaf(-448.0f, y, a), c, y);
+    const float q = __builtin_amdgcn_rcpf(s);  // an ulp off at most
+    r = __builtin_fmaf(-s, q, 1.0f) < 0.0f ? __uint_as_float(__float_as_uint(q) - 1) : q;
+    r2 = __builtin_fmaf(-s, r, 1.0f) * r;
   }
   __device__ __forceinline__ bool fits() const { return s >= 0x1p-64f && s < INFINITY; }
-  __device__ __forceinline__ float operator()(float x) const {
-    const float y = x * r;
-    return __builtin_fmaf(-__builtin_fmaf(s, y, -x), r, y);
-  }
+  __device__ __forceinline__ float operator()(float x) const { return __builtin_fmaf(x, r, x * r2); }
 };
 
 // f(scale) for the group of this amax: under the amax / 448 rule with the short
 // quotient where the whole wave's groups fit it.  Returns the scale that is stored.
 template <class S, class F>
 __device__ __forceinline__ float with_scale(uint32_t amax_bits, F f) {
-  if constexpr (S::kScaledCvt) {
-    const S sc(amax_bits);
-    f(sc);
-    return sc.s;
-  } else {
+  if constexpr (!S::kScaledCvt) {
     const Fp32Quotient sc(amax_bits);
-    if (__builtin_amdgcn_ballot_w64(!sc.fits()) == 0) f(sc);
-    else f(S(amax_bits));
-    return sc.s;
+    if (__builtin_amdgcn_ballot_w64(!sc.fits()) == 0) {
+      f(sc);
+      return sc.s;
+    }
   }
+  const S sc(amax_bits);
+  f(sc);
+  return sc.s;
 }
 
 // Eight values of a group of 128 that 16 lanes hold -> their codes and the scale.

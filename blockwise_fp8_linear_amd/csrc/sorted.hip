@@ -160,19 +160,31 @@ __global__ __launch_bounds__(kThreads) void gather_rows_kernel(GatherArgs a, uin
 // ---------------------------------------------------------------------------
 // Both orientations: a 128 x 128 tile a workgroup, as the one-pass quantizer.
 // ---------------------------------------------------------------------------
-// Eight values of the sorted row of choice src, from column c on: zeros where it
-// is none.  A choice's token is its number over k, by the multiplier 2^32 / k
-// rounded up, exact for choices below 2^28 and k up to 16.
+// The eight values of the thread's 8 sorted rows, from column c on: zeros where a row's
+// source is no choice.  Such a row loads token 0's: behind a branch for each row the
+// loads waited for each other (20608 rows of 2048, of 4095 tokens, 24 us and now 22,
+// amax / 448 33 and 29).  A choice's token is its number over k, by the multiplier 2^32
+// / k rounded up, exact for choices below 2^28 and k up to 16.
 template <bool W>
-__device__ __forceinline__ u32x4 gathered(const GatherArgs& a, int32_t src, int64_t n, uint32_t per_k, int64_t c) {
-  if (src < 0 || src >= n) return u32x4{0, 0, 0, 0};
-  const uint32_t t = a.k > 1 ? __umulhi((uint32_t)src, per_k) : (uint32_t)src;
-  u32x4 v = *reinterpret_cast<const u32x4*>(a.x + (int64_t)t * a.ld_x + c);
-  if constexpr (W) {
-    const float w = a.weights[src];
-    v = u32x4{scaled2(v.x, w), scaled2(v.y, w), scaled2(v.z, w), scaled2(v.w, w)};
+__device__ __forceinline__ void gathered(u32x4 (&v)[8], const GatherArgs& a, const int32_t* __restrict__ source,
+                                         int64_t c) {
+  const uint32_t n = (uint32_t)(a.T * a.k), per_k = (uint32_t)(((uint64_t(1) << 32) + a.k - 1) / (uint32_t)a.k);
+  uint32_t src[8];
+  float w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) src[i] = (uint32_t)source[i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t from = src[i] < n ? src[i] : 0, t = a.k > 1 ? __umulhi(from, per_k) : from;
+    v[i] = *reinterpret_cast<const u32x4*>(a.x + (int64_t)t * a.ld_x + c);
+    if constexpr (W) w[i] = a.weights[from];
   }
-  return v;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (W) v[i] = u32x4{scaled2(v[i].x, w[i]), scaled2(v[i].y, w[i]), scaled2(v[i].z, w[i]), scaled2(v[i].w, w[i])};
+    const uint32_t keep = src[i] < n ? ~0u : 0u;
+    v[i] = u32x4{v[i].x & keep, v[i].y & keep, v[i].z & keep, v[i].w & keep};
+  }
 }
 
 // mine: the column tiles that are one XCD's for all rows, or 0.  Where an eighth of
@@ -195,14 +207,9 @@ __global__ __launch_bounds__(kTileThreads, 6) void gather_both_kernel(GatherArgs
   }
   if (ct >= col_tiles || rt >= used_tiles(a.used, a.R)) return;
   const uint32_t rb = threadIdx.x >> 4, cb = threadIdx.x & 15;
-  const int64_t m0 = (int64_t)rt * 128, c0 = (int64_t)ct * 128, n = a.T * a.k;
-  const uint32_t per_k = (uint32_t)(((uint64_t(1) << 32) + a.k - 1) / (uint32_t)a.k);
-  int32_t src[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) src[i] = a.source[m0 + rb * 8 + i];
+  const int64_t m0 = (int64_t)rt * 128, c0 = (int64_t)ct * 128;
   u32x4 v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = gathered<W>(a, src[i], n, per_k, c0 + cb * 8);
+  gathered<W>(v, a, a.source + m0 + rb * 8, c0 + cb * 8);
   tile_row_groups<S, NT>(v, a.q.q + m0 * a.q.ld + c0 + cb * 8, a.q.ld, a.q.s + m0 * col_tiles + ct, col_tiles, rb, cb);
   tile_col_groups<S, NT>(v, lds, a.qT.q + c0 * a.qT.ld + m0, a.qT.ld, a.qT.s + c0 * row_tiles + rt, row_tiles, rb, cb);
 }

@@ -213,6 +213,21 @@ def test_short_quotient_gives_the_rule():
 
 
 @MODES
+def test_scale_of_every_amax(mode):
+    """Every bf16 amax above zero, one to a group; waves hold groups of one size or of very different ones."""
+    top = np.arange(1, 0x7F80, dtype=np.uint16)
+    for order in (np.arange(top.size), synth.rng_for(39).permutation(top.size)):
+        x = np.zeros((-(-top.size // 128) * 128, 128), np.uint16)
+        x[:top.size, 3] = top[order]
+        source = dev(np.arange(len(x), dtype=np.int32))
+        q, s = fb.fp8_moe_gather(dev_bf16(x), source, 1, scale_mode=mode)
+        expect_rows(q, s, x, mode, len(x))
+        _, _, qT, sT = fb.fp8_moe_gather(dev_bf16(np.ascontiguousarray(x.T)), source[:128].contiguous(), 1, transpose=True,
+                                         scale_mode=mode)
+        expect_cols(qT, sT, np.ascontiguousarray(x.T), mode, 128)
+
+
+@MODES
 def test_values_that_are_not_finite(mode):
     """Codes and scales of the library's own quantizers, NaN and infinities in some groups and none in others."""
     import torch
