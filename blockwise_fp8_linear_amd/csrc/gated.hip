@@ -8,8 +8,8 @@
 // All are bound by memory: per element of h the forward pass moves 4 bytes in
 // and 3 out, the backward pass 4 in and 5 out, the turn 1 in and 1 out (and a
 // thirty-second more for scales).  Under power-of-two scales 8192 rows of 6144 take 62
-// and 102 us, 5.7 and 4.5 TB/s, and the amax / 448 rule, whose quotients bind it, 77 and
-// 145; the turn of 69632 rows of 2048 61 us.
+// and 104 us, 5.7 and 4.4 TB/s, and the amax / 448 rule, whose quotients bind it, 72 and
+// 137; the turn of 69632 rows of 2048 60 us.
 #include "fp8blk_device.h"
 #include "fp8tile_device.h"
 #include "fp8train_launch.h"
