@@ -198,3 +198,41 @@ def test_forward_against_the_layer_of_few_tokens():
     # the mean: 2^-3.5 / sqrt(8) = 0.03 of h's norm; the results' own rounding and the sums' order are small beside it
     assert float((got - y).norm()) <= 0.04 * float(y.norm())
     assert bool((got[host(ids)[:, 0] < 0] == 0).all())
+
+
+def test_two_graphs_share_workspaces():
+    """The workspaces of the sort and of a gather in the order of tokens, between two graphs, filled with other bytes
+    before each replay."""
+    import torch
+    sizes = [(12000, 20, 8, 1152), (9001, 40, 8, 1408)]
+    need = [(fb.fp8_moe_sort_workspace_size(T, E, k),
+             fb.fp8_moe_gather_workspace_size(T, H, fb.fp8_moe_sorted_rows(T, E, k), k)) for T, E, k, H in sizes]
+    assert all(n > 0 for pair in need for n in pair)
+    ws = [torch.empty(max(p[i] for p in need), dtype=torch.uint8, device="cuda") for i in (0, 1)]
+    graphs = []
+    for T, E, k, H in sizes:
+        gen = torch.Generator("cuda").manual_seed(T)
+        ids = torch.randint(-1, E + 1, (T, k), generator=gen, device="cuda").int()
+        x = torch.randn((T, H), generator=gen, device="cuda").bfloat16()
+
+        def run(ids=ids, x=x, E=E, k=k):
+            rows, source, offsets = fb.fp8_moe_sort(ids, E, workspace=ws[0])
+            return rows, source, offsets, *fb.fp8_moe_gather(x, source, k, used=offsets[-1:], workspace=ws[1])
+
+        want = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run()
+        graphs.append((g, out, want, run))
+    for _ in range(3):
+        for g, out, want, _ in graphs:
+            for w in ws:
+                w.fill_(0xFF)
+            for o in out:
+                o.fill_(1)
+            g.replay()
+            torch.cuda.synchronize()
+            used = int(want[2][-1])
+            for i, (o, w) in enumerate(zip(out, want)):
+                assert torch.equal(o[:used], w[:used]) if i > 2 else torch.equal(o, w), i
