@@ -180,6 +180,7 @@ int fp8_gated_forward(int64_t M, int64_t I, const uint16_t *gu, int64_t ld_gu, c
  *   dh [M][I] bf16, row stride ld_dh;  qc, sc: fp8_gated_forward's checkpoint
  *   q [M][2 I] + s [M][2 I/128], qT [2 I][M] + sT [2 I][M/128]: (dg, du)
  *   qhT [I][M] + shT [I][M/128]: h
+ *   scale_mode: the checkpoint's rule, and the results'.
  *   M and I positive multiples of 128; limits as for fp8_gated_forward.
  */
 int fp8_gated_backward(int64_t M, int64_t I, const uint16_t *dh, int64_t ld_dh,
@@ -194,6 +195,7 @@ int fp8_gated_backward(int64_t M, int64_t I, const uint16_t *dh, int64_t ld_dh,
  * becomes the one that Wgrad reads, so no second copy lives through the step.
  *   q [rows][cols] codes (row stride ld_q), s [rows][cols/128]
  *   qT [cols][rows] codes (row stride ld_qT), sT [cols][rows/128]
+ *   scale_mode: the result's rule; s may hold any scales.
  *   rows and cols positive multiples of 128; rows < 2^31, rows cols < 2^37; rows
  *   ld_q and cols ld_qT at most 2^40.
  */
