@@ -13,7 +13,6 @@ namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24;  // of a launch with a workgroup a token
 constexpr int64_t kMaxRows = int64_t(1) << 31;    // a row's number is an int32
-constexpr int64_t kMaxGroupedRows = int64_t(1) << 29;  // of a product: fp8grouped_device.h
 
 int check_choice(int64_t T, int64_t E, int k) {
   if (T <= 0 || E <= 0 || k <= 0) return FP8BLK_ERR_DIM;
@@ -73,7 +72,7 @@ int grouped(Way way, int64_t R, int64_t N, int64_t K, int64_t E, const uint8_t* 
     return FP8BLK_ERR_ARG;
   if (!a || !sa || !b || !sb || !offsets || !out) return FP8BLK_ERR_NULL;
   if (!mult128(R) || !mult128(N) || !mult128(K) || E <= 0) return FP8BLK_ERR_DIM;
-  if (R >= kMaxGroupedRows || N >= (int64_t(1) << 25) || K >= (int64_t(1) << 25) || E > FP8MOE_MAX_EXPERTS ||
+  if (R >= kGroupedMaxRows || N >= (int64_t(1) << 25) || K >= (int64_t(1) << 25) || E > FP8MOE_MAX_EXPERTS ||
       !prod_le(R, N, kMaxElems) || !prod_le(R, K, kMaxElems) || !prod_le(N, K, (kMaxElems >> 2) / E))
     return FP8BLK_ERR_ARG;
   if (!aligned16(a) || !aligned16(b) || !aligned16(out) || !aligned4(sa) || !aligned4(sb) || !aligned4(offsets))

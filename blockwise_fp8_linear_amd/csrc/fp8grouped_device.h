@@ -11,9 +11,6 @@
 namespace fp8blk {
 
 constexpr int kGroupedMaxE = 1024;
-// Rows of a grouped product: below it an expert has fewer than 2^22 row tiles, and
-// 1024 of them, whatever the offsets hold, fewer than 2^32.
-constexpr int64_t kGroupedMaxRows = int64_t(1) << 29;
 
 // An offset as a whole multiple of 128 inside [0, rows], whatever it holds.
 __device__ __forceinline__ int32_t segment_edge(int32_t offset, int32_t rows) {

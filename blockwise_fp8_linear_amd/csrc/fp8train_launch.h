@@ -82,6 +82,10 @@ hipError_t launch_gated_backward(int64_t M, int64_t I, const uint16_t* dh, int64
 hipError_t launch_requantize_colgroup(const uint8_t* q, int64_t rows, int64_t cols, int64_t ld_q, const float* s,
                                       const int32_t* used, CodesOut qT, bool fp32_scale, hipStream_t stream);
 
+// Rows of a grouped product: below it an expert has fewer than 2^22 tiles of 128 rows,
+// and 1024 of them, whatever the offsets hold, fewer than 2^32.
+constexpr int64_t kGroupedMaxRows = int64_t(1) << 29;
+
 // Every expert's contraction: a GemmArgs whose rows (Wgrad: reduction) are cut
 // into the experts' segments; b and sb (Wgrad: out) are expert 0's.
 struct GroupedArgs {
