@@ -36,24 +36,24 @@ __device__ __forceinline__ uint32_t scaled2(uint32_t v, float w) {
 constexpr int kRowSteps = 4, kRowCols = kRowSteps * 512;
 constexpr int kMaxRun = 16;
 
-// The order in which the runs are taken (GatherArgs::order): by the token of a
-// run's first row.  A token's rows are far apart, one in each of its experts'
+// The order in which pairs of runs are taken (GatherArgs::order): by the token of a
+// pair's first row.  A token's rows are far apart, one in each of its experts'
 // segments; taken in the order of the rows they are fetched from memory k times
 // (16384 tokens to 8 of 64 experts: 554 MB, with 285 MB of codes 113 us).  By
 // tokens, and each XCD with a range of its own, a token's rows are taken at about
 // the same time by CUs that share an L2.  Each of kOrderBlocks workgroups looks at
-// all runs, counts those before its share of the token ranges, and in LDS those of
+// all pairs, counts those before its share of the token ranges, and in LDS those of
 // each range of it, and places them -- those of a range in no particular order,
 // which changes no result.  (One workgroup for all: 19 us, most of it scattered
 // stores; each counting every range: 12.)
-constexpr int kOrderThreads = 1024, kOrderKeys = (int)(kOrderRuns / kOrderThreads), kOrderRanges = 1024;
+constexpr int kOrderThreads = 1024, kOrderKeys = (int)(kOrderPairs / kOrderThreads), kOrderRanges = 1024;
 constexpr uint32_t kOrderBlocks = 16, kOrderShare = kOrderRanges / kOrderBlocks;
 static_assert(kOrderShare == 64, "a lane per range");
 
-__global__ __launch_bounds__(kOrderThreads) void gather_order_kernel(GatherArgs a, uint32_t run, int shift) {
+__global__ __launch_bounds__(kOrderThreads) void gather_order_kernel(GatherArgs a, uint32_t pair, int shift) {
   __shared__ uint32_t count[kOrderShare], wave_before[kOrderThreads / 64];
   const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const uint32_t runs = (used_tiles(a.used, a.R) * 128 + run - 1) / run;
+  const uint32_t pairs = (used_tiles(a.used, a.R) * 128 + pair - 1) / pair;
   const uint32_t n = (uint32_t)(a.T * a.k), first = blockIdx.x * kOrderShare;
   if (t < kOrderShare) count[t] = 0;
   __syncthreads();
@@ -61,14 +61,14 @@ __global__ __launch_bounds__(kOrderThreads) void gather_order_kernel(GatherArgs 
 #pragma unroll
   for (int i = 0; i < kOrderKeys; ++i) {
     const uint32_t r = i * kOrderThreads + t;
-    key[i] = r < runs ? (uint32_t)a.source[(int64_t)r * run] : 0;
+    key[i] = r < pairs ? (uint32_t)a.source[(int64_t)r * pair] : 0;
   }
 #pragma unroll
   for (int i = 0; i < kOrderKeys; ++i) {
     const uint32_t r = i * kOrderThreads + t;
     // choices are in the order of their tokens; padding goes anywhere, but not all
-    // of it to one counter; what is behind the last run nowhere
-    const uint32_t range = r >= runs ? kOrderRanges : key[i] < n ? key[i] >> shift : r % kOrderRanges;
+    // of it to one counter; what is behind the last pair nowhere
+    const uint32_t range = r >= pairs ? kOrderRanges : key[i] < n ? key[i] >> shift : r % kOrderRanges;
     before += range < first ? 1 : 0;
     key[i] = range - first;
     if (key[i] < kOrderShare) atomicAdd(&count[key[i]], 1u);
@@ -102,12 +102,12 @@ __global__ __launch_bounds__(kThreads) void gather_rows_kernel(GatherArgs a, uin
   const int64_t rows = (int64_t)used_tiles(a.used, a.R) * 128;
   uint32_t item = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (a.order) {
-    // an eighth of the ordered runs for each XCD
-    const uint32_t runs = (uint32_t)((rows + run - 1) / run), per = (runs + 7) / 8, xcd = blockIdx.x % 8;
+    // an eighth of the ordered pairs for each XCD
+    const uint32_t pairs = (uint32_t)((rows + 2 * run - 1) / (2 * run)), per = (pairs + 7) / 8, xcd = blockIdx.x % 8;
     const uint32_t at = (blockIdx.x / 8) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t in = at / parts, nth = xcd * per + in;
-    if (in >= per || nth >= runs) return;
-    item = a.order[nth] * parts + at % parts;
+    const uint32_t in = at / (2 * parts), nth = xcd * per + in;
+    if (in >= per || nth >= pairs) return;
+    item = a.order[nth] * 2 * parts + at % (2 * parts);
   }
   const uint32_t part = item % parts;
   const int64_t r0 = (int64_t)(item / parts) * run;
@@ -349,11 +349,11 @@ hipError_t gather_as(const GatherArgs& a, hipStream_t stream) {
     int64_t run, waves;
     if (a.order) {
       run = order_run(a.R);
-      waves = ((a.R + run - 1) / run + 7) / 8 * parts;  // of an XCD
+      waves = ((a.R + 2 * run - 1) / (2 * run) + 7) / 8 * 2 * parts;  // of an XCD
       waves = (waves + per - 1) / per * per * 8;
       int shift = 0;
       while (((a.T * a.k - 1) >> shift) >= kOrderRanges) ++shift;
-      hipLaunchKernelGGL(gather_order_kernel, dim3(kOrderBlocks), dim3(kOrderThreads), 0, stream, a, (uint32_t)run, shift);
+      hipLaunchKernelGGL(gather_order_kernel, dim3(kOrderBlocks), dim3(kOrderThreads), 0, stream, a, (uint32_t)(2 * run), shift);
       if (hipError_t e = hipGetLastError()) return e;
     } else {
       // as many rows a wave as leave 8192 waves, which fill the GPU
