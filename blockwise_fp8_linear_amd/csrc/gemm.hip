@@ -40,44 +40,15 @@
 // block case and the epilogue a row-contiguous 8- or 16-byte store.
 // Scales of a chunk of up to CHUNK reduction blocks are staged in LDS, as
 // fp32 values (PROMOTE) or E8M0 bytes (the scaled MFMA).
-#include <type_traits>
-
 #include "fp8blk_device.h"
 #include "fp8blk_launch.h"
 #include "fp8blk_plan.h"
+#include "fp8gemm_tile.h"
 #include "fp8grouped_device.h"
 
 namespace fp8blk {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-
-// BT_: B stored [R][J] (Dgrad from the weight codes as quantized): the B
-// tile is staged as 128 reduction rows of BN bytes and its fragments come
-// from LDS transpose reads.
-// CHUNK_: reduction blocks whose scales sit in LDS at once.
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool PROMOTE_, bool BROW_, bool BT_ = false,
-          int CHUNK_ = 32>
-struct Cfg {
-  static constexpr int BM = BM_, BN = BN_, CHUNK = CHUNK_;
-  static constexpr bool BT = BT_;
-  static_assert(!BT_ || (!BROW_ && BN_ == 128), "transposed B: Dgrad's weight-block layout, 128-byte rows");
-  static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
-  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
-  static constexpr int TM = WM / 16, TN = WN / 16;
-  static constexpr int THREADS = 64 * WAVES_M * WAVES_N;
-  static constexpr bool PROMOTE = PROMOTE_, BROW = BROW_;
-  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  // one staged scale: fp32 for PROMOTE, its E8M0 byte for the scaled MFMA
-  using SType = typename std::conditional<PROMOTE_, float, uint8_t>::type;
-  static constexpr int SA_BYTES = CHUNK * BM * (int)sizeof(SType);
-  static constexpr int SB_BYTES = (BROW ? CHUNK * BN : CHUNK * (BN / 128 > 0 ? BN / 128 : 1)) * (int)sizeof(SType);
-  static constexpr int LDS = 2 * STAGE + SA_BYTES + ((SB_BYTES + 15) / 16) * 16;
-  static_assert(A_BYTES % (1024 * (THREADS / 64)) == 0 && B_BYTES % (1024 * (THREADS / 64)) == 0,
-                "whole KiB of direct loads per wave");
-  static_assert(WN <= 128 && 128 % WN == 0, "a wave's columns must sit inside one 128-block");
-  static_assert(TM % 4 == 0 || TM < 4, "scale bytes are read in words");
-};
 
 __device__ __forceinline__ uint32_t e8_of(float s) { return (__float_as_uint(s) >> 23) & 0xFFu; }
 
@@ -219,7 +190,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
             st + C::A_BYTES + (wave * B_DMA + u) * 1024);
   };
   // ---- scales of reduction blocks [kb0, kb0 + n) -> LDS (fp32 or E8M0).
-  // sa_lds[kbl][i % 16][i / 16]; row-mode B: promote keeps [kbl][j], the
+  // sa_lds[kbl][i % 16][i / 16] (Cfg::sa_at); row-mode B: promote keeps [kbl][j], the
   // scaled MFMA wants [kbl][j % 16][j / 16]; block-mode B: [kbl][j / 128].
   auto load_scales = [&](int64_t kb0, int64_t n) {
     const int64_t nkb_all = nkb;
@@ -283,9 +254,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
     for (int ns = 0; ns < C::TN; ++ns)
       bf[ns] = C::BT ? read_frag_bt(tb, (wn0 >> 4) + ns, lane) : read_frag(tb, wn0 + ns * 16 + l16, g4);
 
-    // A-row scales of this lane's rows i = wm0 + ms*16 + l16 sit at
-    // sa_lds[kbl][l16][wm0 / 16 + ms]
-    const ST* const sa_row = sa_lds + kbl * C::BM + l16 * (C::BM / 16) + (wm0 >> 4);
+    // A-row scales of this lane's rows i = wm0 + ms*16 + l16
+    const ST* const sa_row = sa_lds + C::sa_at(kbl, l16, wm);
 
     if constexpr (C::PROMOTE) {
       // scale of the B side: one value (weight block) or 4 per sub-tile (rows)
@@ -351,11 +321,13 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
       }
     } else {
       // scaled MFMA: every lane passes the E8M0 byte of its own operand row
-      uint32_t saw[(C::TM + 3) / 4];
+      uint32_t saw[C::SA_WORDS];
 #pragma unroll
-      for (int w = 0; w < (C::TM + 3) / 4; ++w) saw[w] = *reinterpret_cast<const uint32_t*>(sa_row + 4 * w);
+      for (int w = 0; w < C::SA_WORDS; ++w)
+        saw[w] = reinterpret_cast<const typename C::SAWord*>(sa_row)[w];
       uint32_t sbw[(C::TN + 3) / 4];
       if constexpr (C::BROW) {
+        static_assert(C::TN % 4 == 0, "whole words of scale bytes");
 #pragma unroll
         for (int w = 0; w < (C::TN + 3) / 4; ++w)
           sbw[w] = *reinterpret_cast<const uint32_t*>(sb_lds + kbl * C::BN + l16 * (C::BN / 16) + (wn0 >> 4) + 4 * w);
@@ -657,13 +629,6 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_wgrad_kernel(GroupedArg
 
 // ------------------------------------------------------------ dispatch ----
 
-using PromoteBlock = Cfg<256, 128, 2, 2, true, false>;
-using PromoteRow = Cfg<256, 128, 2, 2, true, true>;
-using ScaledBlock = Cfg<256, 128, 2, 2, false, false>;
-using ScaledRow = Cfg<256, 128, 2, 2, false, true>;
-using PromoteBlockBT = Cfg<256, 128, 2, 2, true, false, true>;
-using ScaledBlockBT = Cfg<256, 128, 2, 2, false, false, true>;
-
 hipError_t ensure_lds_limit(const void* kernel, int bytes, std::atomic<uint64_t>* done) {
   int dev = 0;
   if (hipError_t e = hipGetDevice(&dev)) return e;
@@ -739,16 +704,6 @@ static hipError_t launch_grouped_wgrad_cfg(const GroupedArgs& a, hipStream_t str
                      C::LDS, stream, a, (uint32_t)tiles_m, (uint32_t)tiles_n);
   return hipGetLastError();
 }
-
-// Experts' products are many short ones: what a tile takes besides its blocks -- the
-// first loads, the scales, the store -- has to be hidden behind another tile.  So the
-// tiles are 128 x 128, two workgroups a CU (72 KiB of LDS each), against the dense
-// kernel's one of 256 x 128: 414 rows of 52 experts of 896 x 3328, amax / 448, Fprop
-// 80 us and 43, Wgrad 209 and 149; 65536 rows of 64 of 2048 x 2048 Dgrad 508 and 444.
-// Where no more than a CU's worth of them are left, 64 x 128, so that more CUs work:
-// 512 rows of 2 experts, Dgrad of 4736 x 256, 35 us and 27.
-template <bool PROMOTE, bool BROW, bool BT, int BM>
-using Expert = Cfg<BM, 128, 2, 2, PROMOTE, BROW, BT, 8>;
 
 template <bool PROMOTE, bool BT>
 static hipError_t launch_experts(const GroupedArgs& a, GroupedTiles tiles, hipStream_t stream) {
