@@ -30,8 +30,8 @@ constexpr int kThreads = 256;
 // - d r) r, as near as a division in a third of the instructions (the backward pass
 // on 8192 rows of 6144: 119 us, 125 with exp2f and a division).  The hardware's
 // power of two gives 0 below fp32's normal range, which vanishes beside 1, and
-// infinity beyond it, whose reciprocal is 0 and needs no correction; a sigmoid
-// below 2^-126 (g < -87.3) is 0.
+// infinity beyond it, whose reciprocal is 0 and needs no correction.  A sigmoid below
+// 2^-126 is not a normal number and comes out as 0: below kFarBelow see far_sigmoid.
 __device__ __forceinline__ float sigmoid(float g) {
   const float d = 1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f);
   const float r = __builtin_amdgcn_rcpf(d);
@@ -41,6 +41,35 @@ __device__ __forceinline__ float sigmoid(float g) {
 __device__ __forceinline__ float gated(float g, float u) {
 #pragma clang fp contract(off)
   return g * sigmoid(g) * u;
+}
+
+// The sigmoid of a g below -87, e^g there (1 + e^g is 1 in fp64 too), in 64 bits: times
+// a u, or a dh and a u, near fp32's limit it leaves a result that is not small.  e^g is
+// the fourth power of e^(g / 4), which is a normal number down to g = -349, where no
+// product with two bf16 values is left.  Few waves ever come here, by a test of all that
+// a wave holds, and the results of its other values are those without it.
+constexpr float kFarBelow = -87.0f;
+constexpr uint32_t kFarBelowBits = 0xC2AE;  // as bf16; the patterns above it are of lower values and of NaN
+__device__ __forceinline__ double far_sigmoid(float g) {
+  const double e = (double)__builtin_amdgcn_exp2f(g * (1.4426950408889634f / 4));
+  return (e * e) * (e * e);
+}
+
+// Whether the wave holds a g below kFarBelow among eight of its lanes' values.
+__device__ __forceinline__ bool any_far_below(u32x4 g) {
+  const uint32_t m = pk_max_u16(pk_max_u16(g.x, g.y), pk_max_u16(g.z, g.w));
+  return __builtin_amdgcn_ballot_w64(max(m & 0xFFFFu, m >> 16) > kFarBelowBits) != 0;
+}
+
+// Two elements of h (the word was) with those of a g below kFarBelow put right.
+__device__ __forceinline__ uint32_t far_gated2(uint32_t g, uint32_t u, uint32_t was) {
+  float h[2] = {bf16_lo(was), bf16_hi(was)};
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const float gv = b ? bf16_hi(g) : bf16_lo(g), uv = b ? bf16_hi(u) : bf16_lo(u);
+    if (gv < kFarBelow) h[b] = (float)(gv * far_sigmoid(gv) * uv);
+  }
+  return bf16x2_rne(h[0], h[1]);
 }
 
 // ---------------------------------------------------------------------------
@@ -75,6 +104,10 @@ __global__ __launch_bounds__(kThreads) void gated_forward_kernel(int64_t M, uint
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       h[j] = bf16x2_rne(gated(bf16_lo(g[i][j]), bf16_lo(u[i][j])), gated(bf16_hi(g[i][j]), bf16_hi(u[i][j])));
+    if (any_far_below(g[i])) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = far_gated2(g[i][j], u[i][j], h[j]);
+    }
     u32x2 oh, og, ou;
     const float sh = quant_group<S>(h, oh);
     const bool live = g0 + i * 4 + sub < total;
@@ -172,8 +205,49 @@ __device__ __forceinline__ uint32_t rounded_here(float lo, float hi) {
   return w;
 }
 
+// A code of the largest scale of the power-of-two rule may stand for 2^128, which fp32
+// does not hold (255 is rounded to 256): then, and only then, a g or u is infinite.
+constexpr float kTopScale = 0x1p120f;
+__device__ __forceinline__ double code_value(float v) {
+  return __builtin_fabsf(v) == INFINITY ? __builtin_copysign(0x1p128, (double)v) : (double)v;
+}
+
+// Word j of dg, du and h: puts those of its two elements right that are not right in 32
+// bits: a g below kFarBelow, a g or u of 2^128, and a dh u past fp32's range, whose dg
+// need not be.
+__device__ __forceinline__ void far_row2(int j, v2f_t g, v2f_t u, uint32_t dh, u32x4& dg, u32x4& du, u32x4& h) {
+  float o[3][2] = {{bf16_lo(dg[j]), bf16_hi(dg[j])}, {bf16_lo(du[j]), bf16_hi(du[j])}, {bf16_lo(h[j]), bf16_hi(h[j])}};
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const float dv = b ? bf16_hi(dh) : bf16_lo(dh);
+    const bool all = g[b] < kFarBelow || __builtin_fabsf(g[b]) == INFINITY || __builtin_fabsf(u[b]) == INFINITY;
+    if (!all && __builtin_fabsf(dv * u[b]) != INFINITY) continue;
+    const double gv = code_value(g[b]), uv = code_value(u[b]);
+    const double sig = g[b] < kFarBelow ? far_sigmoid(g[b]) : (double)sigmoid(g[b]), silu = gv * sig;
+    o[0][b] = (float)(dv * uv * (sig * (1.0 + gv * (1.0 - sig))));
+    if (all) {
+      o[1][b] = (float)(dv * silu);
+      o[2][b] = (float)(silu * uv);
+    }
+  }
+  dg[j] = bf16x2_rne(o[0][0], o[0][1]);
+  du[j] = bf16x2_rne(o[1][0], o[1][1]);
+  h[j] = bf16x2_rne(o[2][0], o[2][1]);
+}
+
+// What a thread has seen that may need far_row2: the lowest g (as bits, where a lower
+// negative number is a larger one; floats would be quieted first), the largest |dh u|.
+struct FarSeen {
+  uint32_t lowest = 0;
+  float most = 0.0f;
+  __device__ __forceinline__ bool any(float top_scale) const {
+    return lowest > __float_as_uint(kFarBelow) || most == INFINITY || top_scale >= kTopScale;
+  }
+};
+
 // dg, du and h of eight elements, two to a word.
-__device__ __forceinline__ void gated_row(const Eight& g, const Eight& u, u32x4 dh, u32x4& dg, u32x4& du, u32x4& h) {
+__device__ __forceinline__ void gated_row(const Eight& g, const Eight& u, u32x4 dh, u32x4& dg, u32x4& du, u32x4& h,
+                                          FarSeen& seen) {
 #pragma clang fp contract(off)
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -181,10 +255,12 @@ __device__ __forceinline__ void gated_row(const Eight& g, const Eight& u, u32x4 
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const float gv = g.v[j][b], uv = u.v[j][b], dv = b ? bf16_hi(dh[j]) : bf16_lo(dh[j]);
-      const float sig = sigmoid(gv), silu = gv * sig;
-      o[0][b] = dv * uv * (sig * (1.0f + gv * (1.0f - sig)));
+      const float sig = sigmoid(gv), silu = gv * sig, dhu = dv * uv;
+      o[0][b] = dhu * (sig * (1.0f + gv * (1.0f - sig)));
       o[1][b] = dv * silu;
       o[2][b] = silu * uv;
+      seen.lowest = max(seen.lowest, __float_as_uint(gv));
+      seen.most = __builtin_fmaxf(seen.most, __builtin_fabsf(dhu));
     }
     dg[j] = rounded_here(o[0][0], o[0][1]);
     du[j] = rounded_here(o[1][0], o[1][1]);
@@ -214,9 +290,11 @@ __global__ __launch_bounds__(kTileThreads, S::kScaledCvt ? 3 : 2) void gated_bac
         reinterpret_cast<const u32x4*>(a.dh + (m0 + rb * 8 + i) * a.ld_dh + c0 + cb * 8));
   // dg, du, and h in dh's place, row by row: the fence keeps the compiler from
   // working on all rows at once, which takes 372 registers (one wave a SIMD)
-#define FP8BLK_ROW(R)                                                                                        \
-  __builtin_amdgcn_sched_barrier(0);                                                                         \
-  gated_row(values8<S>(cg[R], from_lane<R>(sc)), values8<S>(cu[R], from_lane<8 + R>(sc)), dh[R], g[R], u[R], dh[R])
+  FarSeen seen;
+#define FP8BLK_ROW(R)                                                                                           \
+  __builtin_amdgcn_sched_barrier(0);                                                                            \
+  gated_row(values8<S>(cg[R], from_lane<R>(sc)), values8<S>(cu[R], from_lane<8 + R>(sc)), dh[R], g[R], u[R], dh[R], \
+            seen)
   FP8BLK_ROW(0);
   FP8BLK_ROW(1);
   FP8BLK_ROW(2);
@@ -227,6 +305,26 @@ __global__ __launch_bounds__(kTileThreads, S::kScaledCvt ? 3 : 2) void gated_bac
   FP8BLK_ROW(7);
 #undef FP8BLK_ROW
   __builtin_amdgcn_sched_barrier(0);
+  if (__builtin_amdgcn_ballot_w64(seen.any(sc)) != 0) {
+    // a row at a time, its operands once more: their registers hold the results
+#pragma unroll 1
+    for (uint32_t i = 0; i < 8; ++i) {
+      const int64_t r = m0 + rb * 8 + i;
+      const uint8_t* const c = a.qc + r * a.ld_qc + c0 + cb * 8;
+      const Eight gv = values8<S>(*reinterpret_cast<const u32x2*>(c), __shfl(sc, (threadIdx.x & 48) | i, 64));
+      const Eight uv = values8<S>(*reinterpret_cast<const u32x2*>(c + I), __shfl(sc, (threadIdx.x & 48) | 8 | i, 64));
+      const u32x4 d = *reinterpret_cast<const u32x4*>(a.dh + r * a.ld_dh + c0 + cb * 8);
+      u32x4 o[3] = {g[0], u[0], dh[0]};
+#pragma unroll
+      for (uint32_t k = 1; k < 8; ++k)
+        if (i == k) o[0] = g[k], o[1] = u[k], o[2] = dh[k];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) far_row2(j, gv.v[j], uv.v[j], d[j], o[0], o[1], o[2]);
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k)
+        if (i == k) g[k] = o[0], u[k] = o[1], dh[k] = o[2];
+    }
+  }
   // one tensor after the other, each in both orientations: its registers are free
   // for the next
   tile_row_groups<S, NT>(g, a.q.q + m0 * a.q.ld + c0 + cb * 8, a.q.ld, a.q.s + m0 * G + ct, G, rb, cb);

@@ -176,7 +176,8 @@ int fp8_gated_forward(int64_t M, int64_t I, const uint16_t *gu, int64_t ld_gu, c
  *   du = dh g sig,  dg = dh u sig (1 + g (1 - sig)),
  * each rounded to bf16 once and quantized in both orientations, and h =
  * bf16(g sig u) once more, in the orientation that the second linear's Wgrad
- * takes.
+ * takes.  As h in the forward pass, they are right for all finite values: where sig, dh u
+ * or a code's value leaves fp32's range, and the result does not, in 64 bits.
  *   dh [M][I] bf16, row stride ld_dh;  qc, sc: fp8_gated_forward's checkpoint
  *   q [M][2 I] + s [M][2 I/128], qT [2 I][M] + sT [2 I][M/128]: (dg, du)
  *   qhT [I][M] + shT [I][M/128]: h
