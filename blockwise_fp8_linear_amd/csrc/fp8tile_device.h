@@ -14,6 +14,7 @@
 #pragma once
 
 #include "fp8blk_device.h"
+#include "fp8quotient.h"
 
 namespace fp8blk {
 
@@ -37,25 +38,25 @@ __device__ __forceinline__ void store_codes(uint8_t* p, V v) {
   else *reinterpret_cast<V*>(p) = v;
 }
 
-// The amax / 448 rule with fewer instructions, for scales in [2^-64, infinity).  The
-// scale: a product with 1 / 448 and one correction, which gives the correctly rounded
-// quotient of every such bf16 amax.  A value's quotient: Fp32Scale's without its factor,
-// its clamp and its sign, from a reciprocal in two parts, x r + x r2 with r at most 1 /
-// s and r2 = (1 - s r) r, in one rounding of what is then 2^-44 off.  r2 is not negative,
-// so both terms of a zero have its sign.  The amax's own quotient may exceed 448 by an
-// ulp and rounds to 448 without the clamp.  A thread of a tile has 16 scales and 128
-// quotients, which bind the kernels of this rule.
+// The amax / 448 rule with fewer instructions, for scales in [kQuotientLeast,
+// kQuotientMost) of fp8quotient.h.  The scale: a product with 1 / 448 and one
+// correction, which gives the correctly rounded quotient of every such bf16 amax.  A
+// value's quotient: Fp32Scale's without its factor, its clamp and its sign, from a
+// reciprocal in two parts, x r + x r2, in one rounding of what is then 2^-44 off.  r2 is
+// not negative, so both terms of a zero have its sign.  The amax's own quotient may
+// exceed 448 by an ulp and rounds to 448 without the clamp.  A thread of a tile has 16
+// scales and 128 quotients, which bind the kernels of this rule.
 struct Fp32Quotient {
   static constexpr bool kScaledCvt = false;
   float s, r, r2;
   __device__ __forceinline__ explicit Fp32Quotient(uint32_t amax_bits) {
     const float a = __uint_as_float(amax_bits << 16), c = 1.0f / 448.0f, y = a * c;
     s = amax_bits == 0 ? 1.0f : __builtin_fmaf(__builtin_fmaf(-448.0f, y, a), c, y);
-    const float q = __builtin_amdgcn_rcpf(s);  // an ulp off at most
-    r = __builtin_fmaf(-s, q, 1.0f) < 0.0f ? __uint_as_float(__float_as_uint(q) - 1) : q;
-    r2 = __builtin_fmaf(-s, r, 1.0f) * r;
+    const ReciprocalParts p = reciprocal_parts(s, __builtin_amdgcn_rcpf(s));  // an ulp off at most
+    r = p.r;
+    r2 = p.r2;
   }
-  __device__ __forceinline__ bool fits() const { return s >= 0x1p-64f && s < INFINITY; }
+  __device__ __forceinline__ bool fits() const { return s >= kQuotientLeast && s < kQuotientMost; }
   __device__ __forceinline__ float operator()(float x) const { return __builtin_fmaf(x, r, x * r2); }
 };
 

@@ -1,6 +1,7 @@
-"""The gated unit where 32 bits end, on the GPU: a sigmoid below fp32's normal
+"""Where 32 bits end, on the GPU.  The gated unit: a sigmoid below fp32's normal
 range times values near its limit, and a product dh u past it whose gradient is not.
-Against the formulas in 64 bits."""
+Against the formulas in 64 bits.  And the ends of the range of the amax / 448
+quotients."""
 import numpy as np
 import pytest
 
@@ -8,7 +9,7 @@ import blockwise_fp8_linear_amd as fb
 import oracle
 import train_ref
 from blockwise_fp8_linear_amd import synth
-from gpu_util import dev_bf16, host, require_gpu
+from gpu_util import dev, dev_bf16, host, require_gpu
 from train_ref import U, f64
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +142,28 @@ def test_values_beside_those_far_from_zero_are_the_same(mode):
     got = fb.fp8_gated_backward(dev_bf16(dmixed), *got[2:], scale_mode=mode)
     for a, b in zip(got[:2], plain[:2]):
         assert np.array_equal(host(a)[~far], host(b)[~far])
+
+
+# ------------------------------------------------------------- the quotient --
+
+def test_quotients_at_the_ends_of_the_range():
+    """amax / 448 where the short quotient ends and another takes over, and up to the largest amax: every mantissa of the
+    amax, elements of 12 octaves below it."""
+    rng = synth.rng_for(905)
+    top = np.concatenate([np.arange(e << 7, (e + 1) << 7) for e in (*range(127 - 58, 127 - 52), *range(127 + 106, 255))])
+    top = np.repeat(top, 4)
+    x = np.maximum(top[:, None] - rng.integers(0, 12 * 128, (top.size, 128)), 0)
+    x[:, 5] = top
+    x = (x | (rng.integers(0, 2, x.shape) << 15)).astype(np.uint16)
+    n = len(x)
+    assert n % 128 == 0
+    source = dev(np.arange(n, dtype=np.int32))
+    want = oracle.quantize_rowgroup(x, mode=FP32)
+    for got in (fb.fp8_moe_gather(dev_bf16(x), source, 1, scale_mode=FP32),
+                fb.fp8_moe_gather(dev_bf16(x), source, 1, transpose=True, scale_mode=FP32)[:2],
+                fb.fp8_gated_forward(dev_bf16(np.concatenate([x, x], 1)), scale_mode=FP32)[2:]):
+        k = got[1].shape[1]
+        assert np.array_equal(host(got[0]), np.tile(want[0], (1, k))) and np.array_equal(host(got[1]), np.tile(want[1], (1, k)))
+    across = np.ascontiguousarray(x.T)
+    qT, sT = fb.fp8_moe_gather(dev_bf16(across), source[:128].contiguous(), 1, transpose=True, scale_mode=FP32)[2:]
+    assert np.array_equal(host(qT), want[0]) and np.array_equal(host(sT), want[1])
