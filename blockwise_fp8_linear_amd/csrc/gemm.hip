@@ -610,7 +610,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_rows_kernel(GroupedArgs
 }
 
 // Every expert's Wgrad: the reduction runs over its segment alone.  A segment
-// without rows leaves zeros.
+// without rows leaves zeros, or what it would add to.
 template <class C>
 __global__ __launch_bounds__(C::THREADS, 2) void grouped_wgrad_kernel(GroupedArgs a, uint32_t tiles_m, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -619,6 +619,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_wgrad_kernel(GroupedArg
   for (uint32_t t = xcd_remap(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
     const uint32_t e = t / tiles;
     const Segment s = segment_of(a.offsets, (int)e, (int32_t)a.g.R);
+    if (s.length == 0 && a.g.accumulate) continue;
     const TileAt at = tile_at<8>(t - e * tiles, tiles_m, tiles_n);
     const int64_t i0 = (int64_t)at.m * C::BM, j0 = (int64_t)at.n * C::BN;
     gemm_tile<C>(a.g, lds, i0, j0, s.first / 128, (s.first + s.length) / 128, acc);

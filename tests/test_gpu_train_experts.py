@@ -165,3 +165,20 @@ def test_odd_offsets_stay_inside(size, mode):
     c.run(down, out_dtype=torch.float32, out=room[1:-1])
     c.run(down[::-1].copy(), out_dtype=torch.float32, out=room[1:-1])
     assert bool((room[0] == -0.5).all()) and bool((room[-1] == -0.5).all())
+
+
+@MODES
+@pytest.mark.parametrize("size", [size for size, _ in expert_cases.SIZES if size[0] == "wgrad"],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_accumulating_nothing_leaves_every_bit(size, mode):
+    """An expert without rows keeps what was there, negative zeros and NaN among it."""
+    import torch
+    c = Experts(size, mode, 34)
+    e, lists = expert_cases.spreads(c.E, c.R)
+    c.place(lists[0])       # that expert alone has rows
+    was = torch.randint(-2 ** 31, 2 ** 31 - 1, c.shape, generator=c.g, device="cuda", dtype=torch.int32)
+    was[:, :, ::5] = -2 ** 31
+    out = was.clone().view(torch.float32)
+    c.run(out_dtype=torch.float32, out=out, accumulate=True)
+    for i in range(c.E):
+        assert torch.equal(out[i].view(torch.int32), was[i]) == (i != e), i
