@@ -55,8 +55,9 @@ using ScaledBlockBT = Cfg<256, 128, 2, 2, false, false, true>;
 // Experts' products are many short ones: what a tile takes besides its blocks -- the
 // first loads, the scales, the store -- has to be hidden behind another tile.  So the
 // tiles are 128 x 128, two workgroups a CU (72 KiB of LDS each), against the dense
-// kernel's one of 256 x 128: 414 rows of 52 experts of 896 x 3328, amax / 448, Fprop
-// 80 us and 43, Wgrad 209 and 149; 65536 rows of 64 of 2048 x 2048 Dgrad 508 and 444.
+// kernel's one of 256 x 128 (both before their store went through LDS: 414 rows of 52
+// experts of 896 x 3328, amax / 448, Fprop 80 us and 43, Wgrad 209 and 149; 65536 rows
+// of 64 of 2048 x 2048 Dgrad 508 and 444, now 413).
 // Where no more than a CU's worth of them are left, 64 x 128, so that more CUs work:
 // 512 rows of 2 experts, Dgrad of 4736 x 256, 35 us and 27.
 template <bool PROMOTE, bool BROW, bool BT, int BM>

@@ -30,7 +30,7 @@ struct TileLds {
 // Codes are stored past the caches (NT) where a call writes more of them than the
 // Infinity Cache keeps for the next one: what the call reads again -- a token's row
 // for each of its experts -- stays in the caches then.  Gather of 135296 rows of
-// 2048 in both orientations, weighted: 190 us with plain stores, 161 past the caches.
+// 2048 in both orientations, weighted: 219 us with plain stores, 163 past the caches.
 constexpr int64_t kStoreNt = int64_t(128) << 20;  // bytes of codes
 typedef uint32_t tile_u32x2 __attribute__((ext_vector_type(2)));
 template <bool NT, class V>

@@ -51,11 +51,11 @@ __host__ __device__ inline void tile_of(uint32_t bid, uint32_t col_tiles, bool b
 // The same order for any shape, with workgroups that find no tile (rt or ct past
 // the end): blocks that the shape fills in part, and up to 7 whole ones.  Taken where
 // there are kTileSomeBlocks, no more than an eighth of them is empty, so that the XCDs
-// have about the same work (20608 rows of 2048 in 22 of 24 blocks: a turn 23.9 us, row
-// band by row band 21.7; 16384 of 1536, half of the blocks half as wide: gated backward
-// 63.6 and 54.1), and a launch of all of them stays below 2^32 threads.  Gated
-// backward of 8192 rows of 6144 118 us row band by row band and 106, of 65536 of 2048
-// 284 and 242; a turn of 69632 rows of 2048 66.6 and 63.8.
+// have about the same work (20608 rows of 2048 in 22 of 24 blocks: a turn 24.5 us, row
+// band by row band 22.1; 16384 of 1536, half of the blocks half as wide: gated backward
+// 70 and 61), and a launch of all of them stays below 2^32 threads.  Gated
+// backward of 8192 rows of 6144 113 us row band by row band and 103.5, of 65536 of 2048
+// 272 and 238; a turn of 69632 rows of 2048 66 and 63.
 constexpr uint32_t kTileSomeBlocks = 8, kTileMostBlocks = 1 << 16;
 struct TileGrid {
   uint32_t row_tiles, col_tiles;

@@ -51,7 +51,7 @@ struct GatherArgs {
 // Row groups of many rows are gathered in the order of their tokens, in runs of a
 // few rows, which a first launch finds in 6 to 9 us: where x outgrows two XCDs' L2 and
 // the rows' second and further reads of it come to kOrderReread (8192 tokens, 2048
-// wide, to 4 experts each, 117 MB: 29 us either way; to 8, 252 MB: 43 us, unordered 58).
+// wide, to 4 experts each, 117 MB: 38 us, unordered 33; to 8, 252 MB: 39 and 59).
 constexpr int64_t kOrderReread = int64_t(160) << 20;
 // Runs are ordered in pairs (one by one: 18432 instead of 9216 to look at, 12.5 us and 9).
 constexpr int64_t kOrderPairs = 16384;
@@ -110,8 +110,8 @@ hipError_t launch_grouped_wgrad_mx(const GroupedArgs& a, hipStream_t stream);
 // workgroup takes, those that end first, up to kWgradEach, so that what the longest
 // segments leave is taken by others (16 measured the same).  On tiles of 128 x 128 (in
 // gemm.hip), two a CU: 3 + 1.25 b us for both.  (294 rows of 11 experts, 1280 x 1152:
-// 16.7 us on the large tiles, 10.7 on the small ones; 2400 of 64, 2048 x 2048: 120 and
-// 133; 65536 of 64: 372 and 530.)
+// 18 us on the large tiles, 12 on the small ones; 2400 of 64, 2048 x 2048: 120 and
+// 141; 65536 of 64: 386 and 593.)
 constexpr int64_t kWgradEach = 8;
 struct WgradPlan {
   int64_t each, large, small;

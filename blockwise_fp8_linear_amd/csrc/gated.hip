@@ -7,9 +7,9 @@
 //
 // All are bound by memory: per element of h the forward pass moves 4 bytes in
 // and 3 out, the backward pass 4 in and 5 out, the turn 1 in and 1 out (and a
-// thirty-second more for scales).  Under power-of-two scales 8192 rows of 6144 take 62
-// and 104 us, 5.7 and 4.4 TB/s, and the amax / 448 rule, whose quotients bind it, 72 and
-// 137; the turn of 69632 rows of 2048 60 us.
+// thirty-second more for scales).  Under power-of-two scales 8192 rows of 6144 take 66
+// and 103 us, 5.4 and 4.5 TB/s, and under the amax / 448 rule, whose quotients bind the
+// backward pass, 68 and 114; the turn of 69632 rows of 2048 63 us.
 #include "fp8blk_device.h"
 #include "fp8tile_device.h"
 #include "fp8train_launch.h"
@@ -28,7 +28,7 @@ constexpr int kThreads = 256;
 // then as far off, stays within 2^-17, well inside the bf16 rounding (2^-9) that
 // follows.  The quotient is the hardware's reciprocal r with one correction, r + (1
 // - d r) r, as near as a division in a third of the instructions (the backward pass
-// on 8192 rows of 6144: 119 us, 125 with exp2f and a division).  The hardware's
+// on 8192 rows of 6144: 103.5 us, 106 with a division; amax / 448: 115 and 118).  The hardware's
 // power of two gives 0 below fp32's normal range, which vanishes beside 1, and
 // infinity beyond it, whose reciprocal is 0 and needs no correction.  A sigmoid below
 // 2^-126 is not a normal number and comes out as 0: below kFarBelow see far_sigmoid.

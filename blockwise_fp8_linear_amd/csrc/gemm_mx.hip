@@ -804,8 +804,8 @@ __global__ __launch_bounds__(256) void bwd_fixup_kernel(GemmArgs gd, GemmArgs gw
 // in a block of 128 rows has a tile of 128 there; where all tiles are of 128 rows
 // and there is still at most one a CU, all of them are (600 rows of 8 experts of 4096 x
 // 2048: 30 us in tiles of 256 rows, 18).  Bound by the matrix cores where a reduction is
-// long (16384 rows of 8 experts of 2048 x 7168: 2.1 PFLOP/s); 65536 rows of 64 of 2048 x
-// 2048 1.9, where a seventh of a tile's time goes into its first loads and its store.
+// long (16384 rows of 8 experts of 2048 x 7168: 1.9 PFLOP/s); 65536 rows of 64 of 2048 x
+// 2048 as much, where a seventh of a tile's time goes into its first loads and its store.
 template <bool BT>
 __global__ __launch_bounds__(THREADS) void grouped_mx_rows_kernel(GroupedArgs a, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];

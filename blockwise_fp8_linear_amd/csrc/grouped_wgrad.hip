@@ -10,9 +10,11 @@
 // the time with a tile a workgroup: 64 experts of 1024 rows each, 2048 x 2048, 552
 // us.  So a workgroup takes several tiles, and its loads run through them without a
 // pause: the last stages of a tile load the next one's first pairs, and its store,
-// staged through 4 KiB a wave beside the ring, passes while they are on the way: 388
-// us, 1.4 PFLOP/s, and 2.2 to 2.4 with 8 experts of 8192 rows.  What is left beyond the
-// blocks is the store, 537 MB at memory's rate.
+// staged through 4 KiB a wave beside the ring, passes while they are on the way: 386
+// us, 1.4 PFLOP/s, and 1.9 with 8 experts of 8192 rows.  What is left beyond the
+// blocks is the store, 537 MB at memory's rate (fp32 instead of bf16: 455 us; added to
+// what was there, whose loads wait for each other piece by piece: 614, of a floor of
+// 416).
 //
 // The segments differ in length.  So that no XCD gets the long ones, and the last
 // tiles to start are short, the experts come in the order of their loads and their

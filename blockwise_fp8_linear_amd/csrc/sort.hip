@@ -12,7 +12,7 @@
 // the waves' first rows.  Up to kSortAloneRounds rounds of 1024 choices one
 // workgroup does it all in one launch; beyond, the workgroups count in a first
 // launch, and in the second each adds up the others' counts for itself.  14 choices of
-// 8 experts 3.9 us, 131072 of 128 3.6 and 7.0.
+// 8 experts 4.0 us, 131072 of 128 5.1 and 7.8.
 #include "fp8blk_device.h"
 #include "fp8train_launch.h"
 

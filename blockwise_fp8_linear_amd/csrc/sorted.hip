@@ -39,7 +39,8 @@ constexpr int kMaxRun = 16;
 // The order in which pairs of runs are taken (GatherArgs::order): by the token of a
 // pair's first row.  A token's rows are far apart, one in each of its experts'
 // segments; taken in the order of the rows they are fetched from memory k times
-// (16384 tokens to 8 of 64 experts: 554 MB, with 285 MB of codes 113 us).  By
+// (16384 tokens to 8 of 128 experts: 511 MB, with 295 MB of codes 121 us; in this
+// order 126 MB and 74 us).  By
 // tokens, and each XCD with a range of its own, a token's rows are taken at about
 // the same time by CUs that share an L2.  Each of kOrderBlocks workgroups looks at
 // all pairs, counts those before its share of the token ranges, and in LDS those of
@@ -189,8 +190,9 @@ __device__ __forceinline__ void gathered(u32x4 (&v)[8], const GatherArgs& a, con
 
 // mine: the column tiles that are one XCD's for all rows, or 0.  Where an eighth of
 // x's columns fits an XCD's L2 with room to spare (kSliceL2), a token's rows beyond
-// the first are read from there: 4095 tokens to 4 of 60 experts, 2048 wide, 36.5 us
-// and 31.8; 16384 tokens, whose slices do not fit, 160 and 169.
+// the first are read from there: 4095 tokens to 4 of 60 experts, 2048 wide,
+// 27.6 us and 26.6, amax / 448 35.2 and 32.4; 16384 tokens, whose slices do not fit, 152
+// to 164 us either way.
 constexpr int64_t kSliceL2 = int64_t(5) << 19;
 
 template <class S, bool W, bool NT>

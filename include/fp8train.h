@@ -32,7 +32,9 @@
  * writes them.  `used` arguments are a DEVICE pointer to one int32, the number
  * of rows in use (offsets + E of the sort), or NULL for all of them; a value
  * outside [0, rows] counts as the nearer end.  Where groups of 128 rows are
- * quantized, or rows are multiplied, it is rounded up to a multiple of 128.
+ * quantized, or rows are multiplied, it is rounded up to a multiple of 128, and
+ * the rows up to there have to hold values (fp8_gated_forward, whose groups lie
+ * along the rows, stops at the row itself).
  *
  * Values that are not finite: a group of 128 with a NaN or an infinity has the
  * codes and the scale that the quantizers of fp8blk.h give it, and leaves the
@@ -191,8 +193,8 @@ int fp8_gated_backward(int64_t M, int64_t I, const uint16_t *dh, int64_t ld_dh,
 
 /*
  * Row groups to column groups: the values that (q, s) stand for, rounded to bf16
- * (exact for power-of-two scales from 2^-124 on), quantized as
- * fp8_quantize_colgroup does.  The operand that Fprop read and that was kept
+ * (exact for power-of-two scales from 2^-124 on; 2^128, which a code of the largest
+ * one may stand for, is infinity), quantized as fp8_quantize_colgroup does.  The operand that Fprop read and that was kept
  * becomes the one that Wgrad reads, so no second copy lives through the step.
  *   q [rows][cols] codes (row stride ld_q), s [rows][cols/128]
  *   qT [cols][rows] codes (row stride ld_qT), sT [cols][rows/128]
